@@ -10,7 +10,8 @@ raises ImportError if it is missing: there is no fallback path.
 import importlib
 
 __all__ = ["gemm_f32", "gemm_bf16", "gemm_f16", "gemm_s8", "gemm_s8_noalloc", "gemm", "GemmError",
-           "check_device_error", "lib"]
+           "check_device_error", "lib", "gemm_epilogue", "gemm_dact", "act_grad", "rms_norm",
+           "rms_norm_grad"]
 
 
 def __getattr__(name):

@@ -1,0 +1,160 @@
+// act_grad.cu -- the gradient at a linear layer's pre-activation when the
+// output's gradient is already in memory:
+//
+//     dZ_ij = dD_ij act'(Z_ij),    dbias_j = sum_i dZ_ij
+//
+// Bound by memory: 2 matrices in, 1 out, nothing used twice. A block owns 256
+// columns of a chunk of rows: 32 threads x 8 columns (512 contiguous bytes of a
+// row) times 8 rows at a time. Each thread keeps the fp32 sums of its 8 columns
+// over its rows (of the unrounded products), the block adds its 8 row slots in
+// shared memory in slot order, and writes one partial row; col_sums adds them.
+// The chunk count is what fills the GPU once, so the partial rows are about 1 %
+// of the traffic at 8192 x 4096.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "epi.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace dgr {
+namespace {
+
+constexpr int kCols = 256;  // columns per block
+constexpr int kSlots = 8;   // rows at a time
+
+// Column of element e of lane x within the block's 256 columns: contiguous
+// 8-element groups (kVec), or strided by 32 for matrices whose rows cannot be
+// read in 16-byte units.
+template <bool kVec>
+__device__ __forceinline__ int col_of(int x, int e) {
+  return kVec ? 8 * x + e : x + 32 * e;
+}
+
+template <bool kBf16, bool kVec>
+__device__ __forceinline__ void load8(const uint16_t *p, int x, int left, uint32_t (&v)[8]) {
+  if constexpr (kVec) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (8 * x < left) w = __ldcs(reinterpret_cast<const uint4 *>(p + 8 * x));
+    v[0] = w.x & 0xffffu, v[1] = w.x >> 16, v[2] = w.y & 0xffffu, v[3] = w.y >> 16;
+    v[4] = w.z & 0xffffu, v[5] = w.z >> 16, v[6] = w.w & 0xffffu, v[7] = w.w >> 16;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = x + 32 * e < left ? __ldcs(p + x + 32 * e) : 0;
+  }
+}
+
+template <bool kBf16, bool kVec, int kAct>
+__device__ __forceinline__ void act_grad_body(int M, int N, const uint16_t *dD, int64_t ldd,
+                                              const uint16_t *Z, int64_t ldz, uint16_t *dZ,
+                                              int64_t lddz, float *part, int chunk,
+                                              float (&red)[kSlots][kCols]) {
+  const int x = threadIdx.x, y = threadIdx.y;
+  const int c0 = blockIdx.x * kCols, left = N - c0;
+  const int64_t r0 = blockIdx.y * static_cast<int64_t>(chunk);
+  const int64_t r1 = r0 + chunk < M ? r0 + chunk : M;
+  float sum[8] = {};
+#pragma unroll 2
+  for (int64_t r = r0 + y; r < r1; r += kSlots) {
+    uint32_t d[8], z[8];
+    load8<kBf16, kVec>(dD + r * ldd + c0, x, left, d);
+    if constexpr (kAct != kActNone) load8<kBf16, kVec>(Z + r * ldz + c0, x, left, z);
+    float g[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      g[e] = from16<kBf16>(d[e]);
+      if constexpr (kAct != kActNone) g[e] *= act_slope<kAct>(from16<kBf16>(z[e]));
+      if (kVec || col_of<kVec>(x, e) < left) sum[e] += g[e];
+    }
+    if (dZ != nullptr) {
+      uint16_t *out = dZ + r * lddz + c0;
+      if constexpr (kVec) {
+        if (8 * x < left)
+          __stcs(reinterpret_cast<uint4 *>(out + 8 * x),
+                 make_uint4(pack16<kBf16>(g[0], g[1]), pack16<kBf16>(g[2], g[3]),
+                            pack16<kBf16>(g[4], g[5]), pack16<kBf16>(g[6], g[7])));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (x + 32 * e < left) out[x + 32 * e] = to16<kBf16>(g[e]);
+      }
+    }
+  }
+  if (part == nullptr) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) red[y][col_of<kVec>(x, e)] = sum[e];
+  __syncthreads();
+  const int c = y * 32 + x;
+  if (c < left) {
+    float t = 0.f;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) t += red[s][c];
+    part[blockIdx.y * static_cast<int64_t>(N) + c0 + c] = t;
+  }
+}
+
+template <bool kBf16, bool kVec>
+__global__ void __launch_bounds__(32 * kSlots)
+    act_grad_kernel(int M, int N, int act, const uint16_t *dD, int64_t ldd, const uint16_t *Z,
+                    int64_t ldz, uint16_t *dZ, int64_t lddz, float *part, int chunk) {
+  __shared__ float red[kSlots][kCols];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  with_act(act, [&](auto a) {
+    act_grad_body<kBf16, kVec, decltype(a)::value>(M, N, dD, ldd, Z, ldz, dZ, lddz, part, chunk,
+                                                 red);
+  });
+}
+
+bool vec_ok(const void *p, int64_t ld) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0);
+}
+
+}  // namespace
+
+cudaError_t launch_act_grad(const DeviceInfo &dev, bool bf16, int M, int N, int act,
+                            const uint16_t *dD, int64_t ldd, const uint16_t *Z, int64_t ldz,
+                            uint16_t *dZ, int64_t lddz, uint16_t *dbias, cudaStream_t stream) {
+  if (M == 0) return launch_col_sums(bf16, nullptr, 0, N, N, dbias, stream);
+  // As many row chunks as fill the GPU once (8 blocks of 256 threads per SM).
+  const int strips = (N + kCols - 1) / kCols;
+  const int64_t want = std::max<int64_t>(1, static_cast<int64_t>(dev.sm_count) * 8 / strips);
+  int chunk = static_cast<int>((M + want - 1) / want);
+  chunk = (chunk + kSlots - 1) / kSlots * kSlots;
+  const int chunks = (M + chunk - 1) / chunk;
+  float *part = nullptr;
+  if (dbias != nullptr) {
+    cudaMemPool_t pool;
+    cudaError_t e = device_pool(dev, &pool);
+    if (e != cudaSuccess) return e;
+    void *p = nullptr;
+    e = cudaMallocFromPoolAsync(&p, static_cast<size_t>(chunks) * N * 4, pool, stream);
+    if (e != cudaSuccess) return e;
+    part = static_cast<float *>(p);
+  }
+  const bool vec = N % 8 == 0 && vec_ok(dD, ldd) && vec_ok(Z, ldz) && vec_ok(dZ, lddz);
+  auto kern = bf16 ? (vec ? act_grad_kernel<true, true> : act_grad_kernel<true, false>)
+                   : (vec ? act_grad_kernel<false, true> : act_grad_kernel<false, false>);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(strips), static_cast<unsigned>(chunks), 1);
+  cfg.blockDim = dim3(32, kSlots, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e =
+      cudaLaunchKernelEx(&cfg, kern, M, N, act, dD, ldd, Z, ldz, dZ, lddz, part, chunk);
+  if (e == cudaSuccess && part != nullptr)
+    e = launch_col_sums(bf16, part, chunks, N, N, dbias, stream);
+  if (part != nullptr) {
+    cudaError_t f = cudaFreeAsync(part, stream);
+    if (e == cudaSuccess) e = f;
+  }
+  return e;
+}
+
+}  // namespace dgr

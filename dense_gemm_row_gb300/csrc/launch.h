@@ -191,6 +191,73 @@ cudaError_t launch_small_m_s8(const DeviceInfo &dev, int M, int N, int K, int32_
 // freed blocks stay mapped for reuse).
 cudaError_t device_pool(const DeviceInfo &dev, cudaMemPool_t *out);
 
+// ------------------------------------------------ linear-layer operators
+// (include/dense_gemm_row.h, "Linear-layer operators"). All 16-bit matrices of
+// a call share one format (bf16 or fp16).
+
+// What a product's epilogue does with acc = sum_k op(A)_ik op(B)_kj.
+//   forward   z = alpha acc scale_a[i] scale_b[j] + bias[j]; Z = z; D = act(z) + R
+//   gradient  d = alpha acc act'(Zin); D = d; column sums of d into dbias
+// Null pointers leave their term out.
+struct EpiCall {
+  bool bf16 = true;       // format of bias, R, Z and D
+  bool grad = false;
+  int act = 0;
+  float alpha = 1.f;
+  const float *scale_a = nullptr, *scale_b = nullptr;
+  const uint16_t *bias = nullptr;
+  const uint16_t *R = nullptr;  // forward: the residual; gradient: Zin
+  int64_t ldr = 0;
+  uint16_t *Z = nullptr;
+  int64_t ldz = 0;
+  uint16_t *D = nullptr;
+  int64_t ldd = 0;
+  uint16_t *dbias = nullptr;
+};
+// The product with that epilogue. 16-bit A and B of the call's format, or, with
+// e4m3, 8-bit A (M x K) and B stored N x K. Layout already checked: A and B
+// 16-byte aligned with row strides in whole 16-byte units. K >= 0.
+cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t, int M, int N,
+                            int K, const void *A, int64_t lda, const void *B, int64_t ldb,
+                            const EpiCall &epi, cudaStream_t stream);
+
+// dZ = act'(Z) * dD (dZ and Z may be null when act is none), dbias = column sums.
+cudaError_t launch_act_grad(const DeviceInfo &dev, bool bf16, int M, int N, int act,
+                            const uint16_t *dD, int64_t ldd, const uint16_t *Z, int64_t ldz,
+                            uint16_t *dZ, int64_t lddz, uint16_t *dbias, cudaStream_t stream);
+
+// out[j] = sum over p of part[p][j] (p in increasing order within a fixed tree;
+// parts rows of n values, row stride ld), rounded to 16 bits (col_sums.cu).
+cudaError_t launch_col_sums(bool bf16, const float *part, int parts, int n, int64_t ld,
+                            uint16_t *out, cudaStream_t stream);
+
+struct RmsCall {
+  bool bf16 = true;
+  int rows = 0, cols = 0;
+  float eps = 0.f;
+  const uint16_t *X = nullptr, *R = nullptr, *W = nullptr;
+  int64_t ldx = 0, ldr = 0;
+  uint16_t *H = nullptr;
+  int64_t ldh = 0;
+  void *Y = nullptr;  // 16-bit, or e4m3 when scale is set
+  int64_t ldy = 0;
+  float *scale = nullptr, *rstd = nullptr;
+};
+cudaError_t launch_rms_norm(const DeviceInfo &dev, const RmsCall &c, cudaStream_t stream);
+
+struct RmsGradCall {
+  bool bf16 = true;
+  int rows = 0, cols = 0;
+  const uint16_t *dY = nullptr, *H = nullptr, *W = nullptr, *dH = nullptr;
+  int64_t lddy = 0, ldh = 0, lddh = 0;
+  const float *rstd = nullptr;
+  uint16_t *dX = nullptr;
+  int64_t lddx = 0;
+  uint16_t *dW = nullptr;
+};
+cudaError_t launch_rms_norm_grad(const DeviceInfo &dev, const RmsGradCall &c,
+                                 cudaStream_t stream);
+
 // K == 0: C = beta * C (C = 0 when beta == 0), M x N window only.
 cudaError_t launch_scale_f32(int M, int N, float beta, float *C, int64_t ldc,
                              cudaStream_t stream);

@@ -269,6 +269,191 @@ GEMM_API gemm_status_t gemm_s8_noalloc(int64_t M, int64_t N, int64_t K, int32_t 
                                        int64_t ldb, int32_t beta, int32_t *C, int64_t ldc,
                                        cudaStream_t stream);
 
+/* ------------------------------------------------ Linear-layer operators
+ *
+ * A linear layer of a model is a product followed by a bias, an activation and
+ * an addition to the residual stream; a root-mean-square norm stands before it.
+ * These entry points do each in one pass, with 16-bit results, forward and
+ * backward. The rules of the plain entry points hold: sizes 0 <= x < 2^31,
+ * row-major matrices with row strides in elements, checks on the host before
+ * anything is enqueued, statuses, streams and device errors. Elements must be
+ * aligned to their size (else GEMM_ERR_UNSUPPORTED_LAYOUT). Outputs must not
+ * overlap inputs, except that an output may be the very same matrix (pointer
+ * and row stride) as an input where this is said below. Arithmetic is fp32 (the
+ * tensor cores' fp32 accumulation for products); each output is rounded once to
+ * nearest even.
+ */
+
+/* Activations. gelu is z Phi(z) (Phi: the normal distribution function),
+ * gelu_tanh its tanh form 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))),
+ * silu z / (1 + exp(-z)). They are evaluated to a few 2^-20 relative; at an
+ * infinite z the formulas' 0 * inf gives NaN. */
+typedef enum {
+    GEMM_ACT_NONE = 0,
+    GEMM_ACT_RELU = 1,
+    GEMM_ACT_GELU = 2,
+    GEMM_ACT_GELU_TANH = 3,
+    GEMM_ACT_SILU = 4
+} gemm_act_t;
+
+/* An 8-bit float: 4 exponent bits, 3 fraction bits, no infinities, largest
+ * value 448, one NaN pattern per sign. */
+typedef uint8_t gemm_e4m3_t;
+
+/*
+ * gemm_bf16_epi, gemm_f16_epi -- the product with its epilogue:
+ *
+ *     Z = alpha * op(A) * op(B) + bias      (bias_j added to column j)
+ *     D = act(Z) + R
+ *
+ * A, B, bias (N values), R, Z and D share one 16-bit format. bias and R may be
+ * NULL (no such term); Z may be NULL (not written), else the rounded
+ * pre-activation is stored for gemm_*_dact. D may be the same matrix as R.
+ * act(Z) is taken of the fp32 value, not of the rounded one. op, M, N, K, lda,
+ * ldb and the layout rule (A and B 16-byte aligned, lda and ldb multiples of 8)
+ * are those of gemm_bf16_ex; R, Z and D may have any layout, with ldr, ldz,
+ * ldd >= N. K == 0 gives Z = bias. Scratch for split sums comes from the
+ * library's pool. Results are the same bits on every call.
+ *
+ * gemm_e4m3_bf16_epi, gemm_e4m3_f16_epi -- the same with 8-bit operands, A as
+ * stored (M x K) and B stored transposed (N x K), and a scale per row of op(A)
+ * and per column of op(B):
+ *
+ *     Z_ij = alpha * scale_a[i] * scale_b[j] * sum_k A_ik B_jk + bias_j
+ *
+ * scale_a (M values) and scale_b (N values) are fp32 and may each be NULL (1).
+ * bias, R, Z and D are bf16 / fp16. A and B start on 16-byte boundaries and
+ * lda, ldb are multiples of 16, else GEMM_ERR_UNSUPPORTED_LAYOUT.
+ */
+GEMM_API gemm_status_t gemm_bf16_epi(gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N,
+                                     int64_t K, float alpha, const gemm_bf16_t *A, int64_t lda,
+                                     const gemm_bf16_t *B, int64_t ldb, gemm_act_t act,
+                                     const gemm_bf16_t *bias, const gemm_bf16_t *R, int64_t ldr,
+                                     gemm_bf16_t *Z, int64_t ldz, gemm_bf16_t *D, int64_t ldd,
+                                     cudaStream_t stream);
+GEMM_API gemm_status_t gemm_f16_epi(gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N, int64_t K,
+                                    float alpha, const gemm_f16_t *A, int64_t lda,
+                                    const gemm_f16_t *B, int64_t ldb, gemm_act_t act,
+                                    const gemm_f16_t *bias, const gemm_f16_t *R, int64_t ldr,
+                                    gemm_f16_t *Z, int64_t ldz, gemm_f16_t *D, int64_t ldd,
+                                    cudaStream_t stream);
+GEMM_API gemm_status_t gemm_e4m3_bf16_epi(int64_t M, int64_t N, int64_t K, float alpha,
+                                          const gemm_e4m3_t *A, int64_t lda, const float *scale_a,
+                                          const gemm_e4m3_t *B, int64_t ldb, const float *scale_b,
+                                          gemm_act_t act, const gemm_bf16_t *bias,
+                                          const gemm_bf16_t *R, int64_t ldr, gemm_bf16_t *Z,
+                                          int64_t ldz, gemm_bf16_t *D, int64_t ldd,
+                                          cudaStream_t stream);
+GEMM_API gemm_status_t gemm_e4m3_f16_epi(int64_t M, int64_t N, int64_t K, float alpha,
+                                         const gemm_e4m3_t *A, int64_t lda, const float *scale_a,
+                                         const gemm_e4m3_t *B, int64_t ldb, const float *scale_b,
+                                         gemm_act_t act, const gemm_f16_t *bias,
+                                         const gemm_f16_t *R, int64_t ldr, gemm_f16_t *Z,
+                                         int64_t ldz, gemm_f16_t *D, int64_t ldd,
+                                         cudaStream_t stream);
+
+/*
+ * gemm_bf16_dact, gemm_f16_dact -- the product that carries a gradient back to
+ * a layer's pre-activation, with the activation's derivative in its epilogue:
+ *
+ *     dZ = (alpha * op(A) * op(B)) .* act'(Z),    dbias_j = sum_i dZ_ij
+ *
+ * (A the next layer's output gradient, B its weights.) Z (M x N) is what the
+ * forward call stored; with GEMM_ACT_NONE it may be NULL. dbias (N values) may
+ * be NULL; it is summed in fp32 from the unrounded dZ, in a fixed order, and
+ * rounded to the format of the bias it belongs to. dZ may be the same matrix as
+ * Z. M == 0 or K == 0 gives zero sums. Layout rules as gemm_bf16_epi.
+ *
+ * gemm_act_grad_bf16, gemm_act_grad_f16 -- the same when the output gradient
+ * dD (M x N) is already in memory: dZ = dD .* act'(Z). With GEMM_ACT_NONE, Z
+ * may be NULL, and dZ may be NULL too (only the sums are wanted). dZ may be the
+ * same matrix as dD or Z. Any layout.
+ *
+ * The rest of a linear layer's gradient are products: dA = dZ * op(B)^T and
+ * dB = op(A)^T * dZ (gemm_*_epi with 16-bit results, gemm_*_ex with fp32 ones
+ * and accumulation), and dR = dD.
+ */
+GEMM_API gemm_status_t gemm_bf16_dact(gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N,
+                                      int64_t K, float alpha, const gemm_bf16_t *A, int64_t lda,
+                                      const gemm_bf16_t *B, int64_t ldb, gemm_act_t act,
+                                      const gemm_bf16_t *Z, int64_t ldz, gemm_bf16_t *dZ,
+                                      int64_t lddz, gemm_bf16_t *dbias, cudaStream_t stream);
+GEMM_API gemm_status_t gemm_f16_dact(gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N,
+                                     int64_t K, float alpha, const gemm_f16_t *A, int64_t lda,
+                                     const gemm_f16_t *B, int64_t ldb, gemm_act_t act,
+                                     const gemm_f16_t *Z, int64_t ldz, gemm_f16_t *dZ,
+                                     int64_t lddz, gemm_f16_t *dbias, cudaStream_t stream);
+GEMM_API gemm_status_t gemm_act_grad_bf16(int64_t M, int64_t N, gemm_act_t act,
+                                          const gemm_bf16_t *dD, int64_t lddd,
+                                          const gemm_bf16_t *Z, int64_t ldz, gemm_bf16_t *dZ,
+                                          int64_t lddz, gemm_bf16_t *dbias, cudaStream_t stream);
+GEMM_API gemm_status_t gemm_act_grad_f16(int64_t M, int64_t N, gemm_act_t act,
+                                         const gemm_f16_t *dD, int64_t lddd, const gemm_f16_t *Z,
+                                         int64_t ldz, gemm_f16_t *dZ, int64_t lddz,
+                                         gemm_f16_t *dbias, cudaStream_t stream);
+
+/*
+ * gemm_rms_norm_bf16, gemm_rms_norm_f16 -- root-mean-square norm of each of
+ * `rows` rows of `cols` values, with the residual's addition:
+ *
+ *     H = X + R,   rstd_i = (mean_j H_ij^2 + eps)^(-1/2),   Y_ij = H_ij rstd_i W_j
+ *
+ * R may be NULL (H = X), H may be NULL (not written), W (cols values) may be
+ * NULL (1), rstd (rows fp32 values) may be NULL. rstd and Y are those of the
+ * unrounded sum. H may be the same matrix as X or R, Y the same as X or R
+ * (H and Y distinct). eps >= 0. A row of zeros with eps == 0 gives NaN, as the
+ * formula does.
+ *
+ * gemm_rms_norm_bf16_e4m3, gemm_rms_norm_f16_e4m3 -- the same with Y in 8 bits
+ * and a scale per row, what gemm_e4m3_*_epi takes as A and scale_a:
+ * scale_i = max_j |Y_ij| / 448 and Y8_ij = Y_ij / scale_i rounded to nearest
+ * even. A row whose largest |Y_ij| is below 1e-30 gets scale 0 and zeros. A row
+ * with a NaN or an infinity gets a NaN or infinite scale.
+ *
+ * gemm_rms_norm_grad_bf16, gemm_rms_norm_grad_f16 -- the gradient. From dY, the
+ * H and rstd of the forward call, and W (NULL: 1):
+ *
+ *     n_ij = H_ij rstd_i,   g_ij = dY_ij W_j
+ *     dX_ij = rstd_i (g_ij - n_ij mean_k(g_ik n_ik)) + dH_ij,  dW_j = sum_i dY_ij n_ij
+ *
+ * dH (the gradient that reaches H past the norm) and dW may be NULL. dX is the
+ * gradient of both X and R; it may be the same matrix as dY or dH. dW is summed
+ * in fp32 in a fixed order; rows == 0 gives zeros. Any layout.
+ */
+GEMM_API gemm_status_t gemm_rms_norm_bf16(int64_t rows, int64_t cols, float eps,
+                                          const gemm_bf16_t *X, int64_t ldx, const gemm_bf16_t *R,
+                                          int64_t ldr, const gemm_bf16_t *W, gemm_bf16_t *H,
+                                          int64_t ldh, gemm_bf16_t *Y, int64_t ldy, float *rstd,
+                                          cudaStream_t stream);
+GEMM_API gemm_status_t gemm_rms_norm_f16(int64_t rows, int64_t cols, float eps,
+                                         const gemm_f16_t *X, int64_t ldx, const gemm_f16_t *R,
+                                         int64_t ldr, const gemm_f16_t *W, gemm_f16_t *H,
+                                         int64_t ldh, gemm_f16_t *Y, int64_t ldy, float *rstd,
+                                         cudaStream_t stream);
+GEMM_API gemm_status_t gemm_rms_norm_bf16_e4m3(int64_t rows, int64_t cols, float eps,
+                                               const gemm_bf16_t *X, int64_t ldx,
+                                               const gemm_bf16_t *R, int64_t ldr,
+                                               const gemm_bf16_t *W, gemm_bf16_t *H, int64_t ldh,
+                                               gemm_e4m3_t *Y8, int64_t ldy, float *scale,
+                                               float *rstd, cudaStream_t stream);
+GEMM_API gemm_status_t gemm_rms_norm_f16_e4m3(int64_t rows, int64_t cols, float eps,
+                                              const gemm_f16_t *X, int64_t ldx,
+                                              const gemm_f16_t *R, int64_t ldr,
+                                              const gemm_f16_t *W, gemm_f16_t *H, int64_t ldh,
+                                              gemm_e4m3_t *Y8, int64_t ldy, float *scale,
+                                              float *rstd, cudaStream_t stream);
+GEMM_API gemm_status_t gemm_rms_norm_grad_bf16(int64_t rows, int64_t cols, const gemm_bf16_t *dY,
+                                               int64_t lddy, const gemm_bf16_t *H, int64_t ldh,
+                                               const float *rstd, const gemm_bf16_t *W,
+                                               const gemm_bf16_t *dH, int64_t lddh,
+                                               gemm_bf16_t *dX, int64_t lddx, gemm_bf16_t *dW,
+                                               cudaStream_t stream);
+GEMM_API gemm_status_t gemm_rms_norm_grad_f16(int64_t rows, int64_t cols, const gemm_f16_t *dY,
+                                              int64_t lddy, const gemm_f16_t *H, int64_t ldh,
+                                              const float *rstd, const gemm_f16_t *W,
+                                              const gemm_f16_t *dH, int64_t lddh, gemm_f16_t *dX,
+                                              int64_t lddx, gemm_f16_t *dW, cudaStream_t stream);
+
 /* A constant, human-readable name for a status. Never NULL. */
 GEMM_API const char *gemm_status_string(gemm_status_t status);
 
