@@ -20,6 +20,16 @@ cudaError_t launch_epi_fwd8(const DeviceInfo &dev, int tile_n, int M, int N, int
 cudaError_t launch_epi_grad(const DeviceInfo &dev, int tile_n, bool a_t, bool b_t, int M, int N,
                             int K, const void *A, int64_t lda, const void *B, int64_t ldb,
                             const EpiCall &epi, float *part, cudaStream_t stream);
+// The few-rows kernel's (gemm_epi_split_fwd.cu, _fwd8.cu, _grad.cu); mp: rows per token tile.
+cudaError_t launch_split_fwd(const DeviceInfo &dev, int mp, bool b_t, int M, int N, int K,
+                             const void *A, int64_t lda, const void *B, int64_t ldb,
+                             const EpiCall &epi, float *part, cudaStream_t stream);
+cudaError_t launch_split_fwd8(const DeviceInfo &dev, int mp, bool b_t, int M, int N, int K,
+                              const void *A, int64_t lda, const void *B, int64_t ldb,
+                              const EpiCall &epi, float *part, cudaStream_t stream);
+cudaError_t launch_split_grad(const DeviceInfo &dev, int mp, bool b_t, int M, int N, int K,
+                              const void *A, int64_t lda, const void *B, int64_t ldb,
+                              const EpiCall &epi, float *part, cudaStream_t stream);
 
 namespace {
 
@@ -51,17 +61,30 @@ cudaError_t launch_empty(int M, int N, const EpiCall &epi, cudaStream_t stream) 
   return e;
 }
 
+// Rows per token tile of the few-rows kernel, or 0 for the 256-row tiles.
+int split_rows(const DeviceInfo &dev, bool a_t, int M, int N, int K) {
+  (void)dev, (void)N, (void)K;
+  if (a_t || M > 256) return 0;  // its token tiles are K-major
+  return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t, int M, int N,
                             int K, const void *A, int64_t lda, const void *B, int64_t ldb,
                             const EpiCall &epi, cudaStream_t stream) {
   if (K == 0) return launch_empty(M, N, epi, stream);
+  const int mp = split_rows(dev, a_t, M, N, K);
   const int tile_n = 256;
-  if (e4m3) return launch_epi_fwd8(dev, tile_n, M, N, K, A, lda, B, ldb, epi, stream);
-  if (!epi.grad) return launch_epi_fwd(dev, tile_n, a_t, b_t, M, N, K, A, lda, B, ldb, epi, stream);
-  // Gradient: partial column sums, one row per 32 rows of D.
-  const int parts = static_cast<int>((static_cast<int64_t>(M) + 31) / 32);
+  if (!epi.grad) {
+    if (e4m3)
+      return mp ? launch_split_fwd8(dev, mp, true, M, N, K, A, lda, B, ldb, epi, nullptr, stream)
+                : launch_epi_fwd8(dev, tile_n, M, N, K, A, lda, B, ldb, epi, stream);
+    return mp ? launch_split_fwd(dev, mp, b_t, M, N, K, A, lda, B, ldb, epi, nullptr, stream)
+              : launch_epi_fwd(dev, tile_n, a_t, b_t, M, N, K, A, lda, B, ldb, epi, stream);
+  }
+  // Gradient: partial column sums, one row per token tile or per 32 rows of D.
+  const int parts = static_cast<int>((static_cast<int64_t>(M) + (mp ? mp : 32) - 1) / (mp ? mp : 32));
   void *part = nullptr;
   if (epi.dbias != nullptr) {
     cudaMemPool_t pool;
@@ -70,12 +93,13 @@ cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t
     e = cudaMallocFromPoolAsync(&part, static_cast<size_t>(parts) * N * 4, pool, stream);
     if (e != cudaSuccess) return e;
   }
-  cudaError_t e = launch_epi_grad(dev, tile_n, a_t, b_t, M, N, K, A, lda, B, ldb, epi,
-                                  static_cast<float *>(part), stream);
+  float *sums = static_cast<float *>(part);
+  cudaError_t e = mp ? launch_split_grad(dev, mp, b_t, M, N, K, A, lda, B, ldb, epi, sums, stream)
+                     : launch_epi_grad(dev, tile_n, a_t, b_t, M, N, K, A, lda, B, ldb, epi, sums,
+                                       stream);
   if (part != nullptr) {
     if (e == cudaSuccess)
-      e = launch_col_sums(epi.bf16, static_cast<const float *>(part), parts, N, N, epi.dbias,
-                          stream);
+      e = launch_col_sums(epi.bf16, sums, parts, N, N, epi.dbias, stream);
     cudaError_t f = cudaFreeAsync(part, stream);
     if (e == cudaSuccess) e = f;
   }

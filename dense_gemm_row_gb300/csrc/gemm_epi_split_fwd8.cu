@@ -1,0 +1,14 @@
+// gemm_epi_split_fwd8.cu -- the few-rows kernel, e4m3 operands, forward epilogue (gemm_epi_split.cuh).
+#include <algorithm>
+
+#include "gemm_epi_split.cuh"
+
+namespace dgr {
+
+cudaError_t launch_split_fwd8(const DeviceInfo &dev, int mp, bool b_t, int M, int N, int K,
+                              const void *A, int64_t lda, const void *B, int64_t ldb,
+                              const EpiCall &epi, float *part, cudaStream_t stream) {
+  return launch_split<true, false>(dev, mp, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
+}
+
+}  // namespace dgr
