@@ -42,6 +42,7 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t cluster_addr) {
 }
 
 constexpr int kSplitThreads = 192;  // TMA warp, MMA warp, four warps that drain TMEM
+constexpr int kSplitFinish = 128;  // threads that add and finish: those four warps
 constexpr int kSplitN = 128;        // columns of D per tile (the MMA's M)
 constexpr int kSplitMaxCl = 8;      // portable cluster size
 constexpr int kSplitCtasPerSm = 2;
@@ -97,45 +98,65 @@ __device__ __forceinline__ void store4(uint16_t *p, bool vec, int n, uint2 v) {
   }
 }
 
-// Adds the partial sums of this CTA's columns over the cluster and writes them.
-template <bool kGrad, bool kBf16, int kAct>
-__device__ __forceinline__ void split_finish(const SplitArgs &p, uint32_t red, int rank, int m0,
-                                             int n0, float (&sum)[4]) {
-  const int W = kSplitN / p.cl, wq = W / 4;
-  const int t = static_cast<int>(threadIdx.x);
-  const int rows = min(p.M - m0, p.mp);
-  // wq divides the thread count, so a thread keeps its columns from item to item.
-  const int lc = rank * W + (t % wq) * 4;
-  const int col = n0 + lc;
-  const int left = p.N - col;
-  if (left <= 0) return;
-  float bias[4] = {0.f, 0.f, 0.f, 0.f}, sb[4];
+// What one finishing thread needs besides the sums: its four columns' bias and
+// scales and one row's R and scale, as stored. Loaded before the accumulator is
+// waited for, so the loads' latency is off the tail.
+struct SplitCols {
+  uint32_t bias[4];
+  float scale[4];
+};
+struct SplitRow {
+  uint2 r;
+  float scale;
+};
+template <bool kGrad>
+__device__ __forceinline__ void split_load_cols(const SplitArgs &p, int col, SplitCols &k) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    sb[e] = p.c.alpha;
-    if (!kGrad && e < left) {
-      if (p.c.bias) bias[e] = from16<kBf16>(__ldg(p.c.bias + col + e));
-      if (p.c.scale_b) sb[e] *= __ldg(p.c.scale_b + col + e);
-    }
+    k.bias[e] = !kGrad && p.c.bias && col + e < p.N ? __ldg(p.c.bias + col + e) : 0;
+    k.scale[e] = !kGrad && p.c.scale_b && col + e < p.N ? __ldg(p.c.scale_b + col + e) : 1.f;
   }
-#pragma unroll 2
-  for (int m = t / wq; m < rows; m += kSplitThreads / wq) {
+}
+template <bool kGrad>
+__device__ __forceinline__ void split_load_row(const SplitArgs &p, int64_t row, int col,
+                                               SplitRow &k) {
+  k.r = make_uint2(0, 0);
+  k.scale = 1.f;
+  if (row >= p.M || col >= p.N) return;
+  if (p.c.R) k.r = load4(p.c.R + row * p.c.ldr + col, p.r_vec, p.N - col);
+  if (!kGrad && p.c.scale_a) k.scale = __ldg(p.c.scale_a + row);
+}
+
+// Adds the partial sums of this CTA's columns over the cluster and writes them.
+// Thread t of kSplitFinish owns four columns and rows t / wq, + kSplitFinish / wq ...
+template <bool kGrad, bool kBf16, int kAct>
+__device__ __forceinline__ void split_finish(const SplitArgs &p, uint32_t red, int t, int lc,
+                                             int m0, int col, const SplitCols &cols,
+                                             SplitRow next, float (&sum)[4]) {
+  const int wq = kSplitN / p.cl / 4, step = kSplitFinish / wq;
+  const int rows = min(p.M - m0, p.mp), left = p.N - col;
+  if (left <= 0) return;
+  for (int m = t / wq; m < rows; m += step) {
     const int64_t row = m0 + m;
-    uint2 r16 = make_uint2(0, 0);
-    if (p.c.R) r16 = load4(p.c.R + row * p.c.ldr + col, p.r_vec, left);
-    const float sa = !kGrad && p.c.scale_a ? __ldg(p.c.scale_a + row) : 1.f;
+    const SplitRow now = next;
     const uint32_t off = red + static_cast<uint32_t>((m * kSplitN + lc) * 4);
+    float4 s[kSplitMaxCl];
+#pragma unroll
+    for (int q = 0; q < kSplitMaxCl; ++q)
+      if (q < p.cl) s[q] = ld_dsmem_f4(mapa_shared(off, static_cast<uint32_t>(q)));
+    if (m + step < rows) split_load_row<kGrad>(p, row + step, col, next);
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int q = 0; q < p.cl; ++q) {  // CTA order: one fixed order per element
-      const float4 s = ld_dsmem_f4(mapa_shared(off, static_cast<uint32_t>(q)));
-      v[0] += s.x, v[1] += s.y, v[2] += s.z, v[3] += s.w;
-    }
+#pragma unroll
+    for (int q = 0; q < kSplitMaxCl; ++q)  // CTA order: one fixed order per element
+      if (q < p.cl) v[0] += s[q].x, v[1] += s[q].y, v[2] += s[q].z, v[3] += s[q].w;
     float r[4];
-    unpack16<kBf16>(r16.x, r[0], r[1]);
-    unpack16<kBf16>(r16.y, r[2], r[3]);
+    unpack16<kBf16>(now.r.x, r[0], r[1]);
+    unpack16<kBf16>(now.r.y, r[2], r[3]);
+    const float sa = p.c.alpha * now.scale;
     if constexpr (!kGrad) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = fmaf(v[e] * sa, sb[e], bias[e]);
+      for (int e = 0; e < 4; ++e)
+        v[e] = fmaf(v[e] * sa, cols.scale[e], from16<kBf16>(cols.bias[e]));
       if (p.c.Z)
         store4(p.c.Z + row * p.c.ldz + col, p.z_vec, left,
                make_uint2(pack16<kBf16>(v[0], v[1]), pack16<kBf16>(v[2], v[3])));
@@ -148,7 +169,7 @@ __device__ __forceinline__ void split_finish(const SplitArgs &p, uint32_t red, i
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] *= sb[e] * act_slope<kAct>(r[e]);
+        v[e] *= sa * act_slope<kAct>(r[e]);
         sum[e] += v[e];
       }
     }
@@ -205,6 +226,13 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * KB / cl);
   const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * KB / cl);
 
+  // Finishing threads: t owns columns lc .. lc + 3 of the tile (wq divides the
+  // thread count, so they stay the same from row to row).
+  const int W = kSplitN / cl, wq = W / 4;
+  const int t = static_cast<int>(threadIdx.x) - 64;
+  const int lc = rank * W + (t & (wq - 1)) * 4, col = n0 + lc;
+  SplitCols cols;
+  SplitRow first;
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -284,32 +312,34 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   } else {
     // ------------------------------------------- accumulator -> partial sums
     const int quarter = warp & 3;
+    split_load_cols<kGrad>(p, col, cols);
+    split_load_row<kGrad>(p, m0 + t / wq, col, first);
     int got = 0;
     if (lane == 0)
       got = mbar_wait_bounded(smem_u32(&sm.done), 0, abort, p.err_word, kWaitTmemFull);
     got = __shfl_sync(0xffffffffu, got, 0);
-    if (got) {
-      tc_fence_after_sync();
-      // Every MMA has completed and every copy was consumed by one, so the
-      // stages are free: partial sums [row][column], lanes on columns.
-      float *red = reinterpret_cast<float *>(sm.b[0]) + quarter * 32 + lane;
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    // Every MMA has completed and every copy was consumed by one, so the stages
+    // are free: partial sums [row][column], lanes on columns. A CTA whose wait
+    // gave up (recorded in the error word) has NaN for sums.
+    tc_fence_after_sync();
+    float *red = reinterpret_cast<float *>(sm.b[0]) + quarter * 32 + lane;
+    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
-      for (int c = 0; c < kMP; c += 16) {
-        if (c < p.mp) {
-          uint32_t r[16];
-          asm volatile(
-              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-              "%10, %11, %12, %13, %14, %15}, [%16];\n"
-              : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-                "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-              : "r"(taddr + c)
-              : "memory");
-          tmem_ld_wait();
+    for (int c = 0; c < kMP; c += 16) {
+      if (c < p.mp) {
+        uint32_t r[16];
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+            "%10, %11, %12, %13, %14, %15}, [%16];\n"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+              "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr + c)
+            : "memory");
+        tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) red[(c + j) * kSplitN] = __uint_as_float(r[j]);
-        }
+        for (int j = 0; j < 16; ++j)
+          red[(c + j) * kSplitN] = got ? __uint_as_float(r[j]) : __uint_as_float(0x7fffffffu);
       }
     }
   }
@@ -321,29 +351,24 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     __syncthreads();
   }
 
-  // A CTA whose waits gave up has recorded the error; no CTA of the cluster
-  // writes results then.
-  int bad = 0;
-  for (int q = 0; q < cl; ++q) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];\n"
-                 : "=r"(v)
-                 : "r"(mapa_shared(smem_u32(&sm.abort), static_cast<uint32_t>(q)))
-                 : "memory");
-    bad |= static_cast<int>(v);
-  }
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  if (!bad) {
+  if (warp >= 2) {
+    const uint32_t red = smem_u32(sm.b[0]);
     with_act(p.c.act, [&](auto a) {
+      constexpr int kAct = decltype(a)::value;
       if (p.c.bf16) {
-        split_finish<kGrad, true, decltype(a)::value>(p, smem_u32(sm.b[0]), rank, m0, n0, sum);
+        split_finish<kGrad, true, kAct>(p, red, t, lc, m0, col, cols, first, sum);
       } else {
-        split_finish<kGrad, false, decltype(a)::value>(p, smem_u32(sm.b[0]), rank, m0, n0, sum);
+        split_finish<kGrad, false, kAct>(p, red, t, lc, m0, col, cols, first, sum);
       }
     });
   }
   if (cl > 1) {
-    cluster_sync();  // no CTA leaves, or reuses its stages, while another reads its sums
+    // No CTA leaves, or reuses its stages, while another reads its sums. Reads
+    // only, so the barrier orders no memory: a releasing arrive would wait for
+    // the results' stores to global memory (1 us at 1 x 4096 x 4096).
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n"
+                 "barrier.cluster.wait.aligned;\n" ::: "memory");
   } else {
     __syncthreads();
   }
@@ -352,17 +377,16 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     if (p.part != nullptr) {
       // Column sums of this CTA's columns: the threads of a column in row order.
       // The stages are free: every read of the partial sums is behind the barrier.
-      static_assert(Cf::kStages * Cf::kABytes >= kSplitThreads * 16, "room for the sums");
+      static_assert(Cf::kStages * Cf::kABytes >= kSplitFinish * 16, "room for the sums");
       float4 *slots = reinterpret_cast<float4 *>(sm.a[0]);
-      slots[threadIdx.x] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+      if (warp >= 2) slots[t] = make_float4(sum[0], sum[1], sum[2], sum[3]);
       __syncthreads();
-      const int W = kSplitN / cl, wq = W / 4;
-      const int t = static_cast<int>(threadIdx.x), col = n0 + rank * W + t;
-      if (t < W && col < p.N && !bad) {
+      const int at = n0 + rank * W + t;
+      if (warp >= 2 && t < W && at < p.N) {
         float s = 0.f;
-        for (int i = t / 4; i < kSplitThreads; i += wq)
+        for (int i = t / 4; i < kSplitFinish; i += wq)
           s += reinterpret_cast<const float *>(slots + i)[t & 3];
-        p.part[static_cast<int64_t>(tile % p.tiles_m) * p.N + col] = s;
+        p.part[static_cast<int64_t>(tile % p.tiles_m) * p.N + at] = s;
       }
     }
   }
