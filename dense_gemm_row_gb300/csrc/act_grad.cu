@@ -24,6 +24,10 @@ namespace {
 
 constexpr int kCols = 256;  // columns per block
 constexpr int kSlots = 8;   // rows at a time
+constexpr int kBlocksPerSm = 3;
+// row groups whose loads are in flight together (2-byte loads: fewer registers)
+template <bool kVec>
+constexpr int kAheadOf = kVec ? 4 : 2;
 
 // Column of element e of lane x within the block's 256 columns: contiguous
 // 8-element groups (kVec), or strided by 32 for matrices whose rows cannot be
@@ -33,17 +37,20 @@ __device__ __forceinline__ int col_of(int x, int e) {
   return kVec ? 8 * x + e : x + 32 * e;
 }
 
-template <bool kBf16, bool kVec>
-__device__ __forceinline__ void load8(const uint16_t *p, int x, int left, uint32_t (&v)[8]) {
+// A thread's 8 values of one row, packed.
+template <bool kVec>
+__device__ __forceinline__ uint4 load8(const uint16_t *p, int x, int left) {
+  uint4 w = make_uint4(0, 0, 0, 0);
   if constexpr (kVec) {
-    uint4 w = make_uint4(0, 0, 0, 0);
     if (8 * x < left) w = __ldcs(reinterpret_cast<const uint4 *>(p + 8 * x));
-    v[0] = w.x & 0xffffu, v[1] = w.x >> 16, v[2] = w.y & 0xffffu, v[3] = w.y >> 16;
-    v[4] = w.z & 0xffffu, v[5] = w.z >> 16, v[6] = w.w & 0xffffu, v[7] = w.w >> 16;
   } else {
+    uint32_t v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = x + 32 * e < left ? __ldcs(p + x + 32 * e) : 0;
+    w = make_uint4(v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16),
+                   v[6] | (v[7] << 16));
   }
+  return w;
 }
 
 template <bool kBf16, bool kVec, int kAct>
@@ -51,34 +58,57 @@ __device__ __forceinline__ void act_grad_body(int M, int N, const uint16_t *dD, 
                                               const uint16_t *Z, int64_t ldz, uint16_t *dZ,
                                               int64_t lddz, float *part, int chunk,
                                               float (&red)[kSlots][kCols]) {
+  constexpr int kAhead = kAheadOf<kVec>;
   const int x = threadIdx.x, y = threadIdx.y;
   const int c0 = blockIdx.x * kCols, left = N - c0;
   const int64_t r0 = blockIdx.y * static_cast<int64_t>(chunk);
   const int64_t r1 = r0 + chunk < M ? r0 + chunk : M;
   float sum[8] = {};
-#pragma unroll 2
-  for (int64_t r = r0 + y; r < r1; r += kSlots) {
-    uint32_t d[8], z[8];
-    load8<kBf16, kVec>(dD + r * ldd + c0, x, left, d);
-    if constexpr (kAct != kActNone) load8<kBf16, kVec>(Z + r * ldz + c0, x, left, z);
-    float g[8];
+  for (int64_t r = r0 + y; r < r1; r += kSlots * kAhead) {
+    // The loads of kAhead rows are in flight together (a store between them
+    // could alias the next row's loads, so the compiler would not move them up).
+    uint4 d[kAhead], z[kAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      g[e] = from16<kBf16>(d[e]);
-      if constexpr (kAct != kActNone) g[e] *= act_slope<kAct>(from16<kBf16>(z[e]));
-      if (kVec || col_of<kVec>(x, e) < left) sum[e] += g[e];
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t row = r + i * kSlots;
+      d[i] = z[i] = make_uint4(0, 0, 0, 0);
+      if (row < r1) {
+        d[i] = load8<kVec>(dD + row * ldd + c0, x, left);
+        if constexpr (kAct != kActNone) z[i] = load8<kVec>(Z + row * ldz + c0, x, left);
+      }
     }
-    if (dZ != nullptr) {
-      uint16_t *out = dZ + r * lddz + c0;
-      if constexpr (kVec) {
-        if (8 * x < left)
-          __stcs(reinterpret_cast<uint4 *>(out + 8 * x),
-                 make_uint4(pack16<kBf16>(g[0], g[1]), pack16<kBf16>(g[2], g[3]),
-                            pack16<kBf16>(g[4], g[5]), pack16<kBf16>(g[6], g[7])));
-      } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (x + 32 * e < left) out[x + 32 * e] = to16<kBf16>(g[e]);
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t row = r + i * kSlots;
+      if (row >= r1) break;
+      const uint32_t dw[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
+      const uint32_t zw[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
+      uint32_t g[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float a, b;
+        unpack16<kBf16>(dw[e], a, b);
+        if constexpr (kAct != kActNone) {
+          float za, zb;
+          unpack16<kBf16>(zw[e], za, zb);
+          a *= act_slope<kAct>(za);
+          b *= act_slope<kAct>(zb);
+        }
+        sum[2 * e] += a;
+        sum[2 * e + 1] += b;
+        g[e] = pack16<kBf16>(a, b);
+      }
+      if (dZ != nullptr) {
+        uint16_t *out = dZ + row * lddz + c0;
+        if constexpr (kVec) {
+          if (8 * x < left)
+            __stcs(reinterpret_cast<uint4 *>(out + 8 * x), make_uint4(g[0], g[1], g[2], g[3]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (x + 32 * e < left)
+              out[x + 32 * e] = static_cast<uint16_t>(g[e >> 1] >> (16 * (e & 1)));
+        }
       }
     }
   }
@@ -96,7 +126,7 @@ __device__ __forceinline__ void act_grad_body(int M, int N, const uint16_t *dD, 
 }
 
 template <bool kBf16, bool kVec>
-__global__ void __launch_bounds__(32 * kSlots)
+__global__ void __launch_bounds__(32 * kSlots, kBlocksPerSm)
     act_grad_kernel(int M, int N, int act, const uint16_t *dD, int64_t ldd, const uint16_t *Z,
                     int64_t ldz, uint16_t *dZ, int64_t lddz, float *part, int chunk) {
   __shared__ float red[kSlots][kCols];
@@ -118,9 +148,10 @@ cudaError_t launch_act_grad(const DeviceInfo &dev, bool bf16, int M, int N, int 
                             const uint16_t *dD, int64_t ldd, const uint16_t *Z, int64_t ldz,
                             uint16_t *dZ, int64_t lddz, uint16_t *dbias, cudaStream_t stream) {
   if (M == 0) return launch_col_sums(bf16, nullptr, 0, N, N, dbias, stream);
-  // As many row chunks as fill the GPU once (8 blocks of 256 threads per SM).
+  // As many row chunks as fill the GPU once (kBlocksPerSm blocks per SM).
   const int strips = (N + kCols - 1) / kCols;
-  const int64_t want = std::max<int64_t>(1, static_cast<int64_t>(dev.sm_count) * 8 / strips);
+  const int64_t want =
+      std::max<int64_t>(1, static_cast<int64_t>(dev.sm_count) * kBlocksPerSm / strips);
   int chunk = static_cast<int>((M + want - 1) / want);
   chunk = (chunk + kSlots - 1) / kSlots * kSlots;
   const int chunks = (M + chunk - 1) / chunk;

@@ -3,8 +3,9 @@
 //
 // Every producer writes one partial row per block of rows it owns, so the sums
 // need no atomics and are the same bits on every run: row slot y of a block
-// adds partial rows y, y + 16, ... in order, then the 16 slots are added in
-// slot order.
+// adds partial rows y, y + 32, ... in order, then the 32 slots are added in
+// slot order. Latency is what it costs (a few hundred partial rows at most), so
+// a thread's loads are issued together.
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -16,7 +17,7 @@
 namespace dgr {
 namespace {
 
-constexpr int kSlots = 16;
+constexpr int kSlots = 32;
 
 template <bool kBf16>
 __global__ void __launch_bounds__(32 * kSlots)
@@ -26,8 +27,8 @@ __global__ void __launch_bounds__(32 * kSlots)
   const int j = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
   if (j < n) {
-#pragma unroll 4
-    for (int p = threadIdx.y; p < parts; p += kSlots) s += part[p * ld + j];
+#pragma unroll 8
+    for (int p = threadIdx.y; p < parts; p += kSlots) s += part[static_cast<int64_t>(p) * ld + j];
   }
   red[threadIdx.y][threadIdx.x] = s;
   __syncthreads();

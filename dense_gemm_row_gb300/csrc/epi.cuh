@@ -61,12 +61,24 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   }
 }
 
-// 1 / (1 + exp(-x)). exp(-x) overflows to +inf for x < -88, where the quotient
-// is 0, its limit. __expf and __fdividef are within a few 2^-22 (relative), far
-// below one 16-bit rounding (2^-9 for bf16, 2^-12 for fp16).
-__device__ __forceinline__ float logistic(float x) {
-  return __fdividef(1.f, 1.f + __expf(-x));
+// The hardware's exponential and reciprocal, subnormals taken as zero: a few
+// 2^-22 (relative), far below one 16-bit rounding (2^-9 for bf16, 2^-12 for
+// fp16). One instruction each; __expf and __fdividef add the handling of
+// subnormals around them, which an element-wise pass pays for.
+__device__ __forceinline__ float exp_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
 }
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / (1 + exp(-x)). exp(-x) overflows to +inf for x < -88, where the quotient
+// is 0, its limit.
+__device__ __forceinline__ float logistic(float x) { return rcp_fast(1.f + exp_fast(-x)); }
 
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
@@ -83,8 +95,8 @@ constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 // so an element-wise pass stays bound by memory.
 __device__ __forceinline__ float normal_cdf(float z, float &e) {
   const float x = fabsf(z) * kInvSqrt2;
-  const float t = __fdividef(1.f, fmaf(0.5f, x, 1.f));
-  e = __expf(-x * x);
+  const float t = rcp_fast(fmaf(0.5f, x, 1.f));
+  e = exp_fast(-0.5f * z * z);
   float p = 0.08912812918424606f;
   p = fmaf(p, t, -0.35999614000320435f);
   p = fmaf(p, t, 0.39379453659057617f);

@@ -14,11 +14,12 @@
 //
 // Both are bound by memory: every value is read once, kept in registers and
 // written once. A row belongs to one block, or (short rows) to one warp of a
-// block; threads hold 8 consecutive values per 16-byte load. The largest |h w|
+// block. The largest |h w|
 // is reduced together with the sum of squares, so the 8-bit form has one block
 // reduction too: max |y| = s max |h w| up to rounding.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -49,41 +50,80 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   return r;
 }
 
-// V values of a row from column c (V = 8: one 16-byte load).
-template <bool kBf16, int V>
-__device__ __forceinline__ void load_row(const uint16_t *p, int c, float (&v)[V]) {
-  if constexpr (V == 8) {
-    const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p + c));
-    unpack16<kBf16>(w.x, v[0], v[1]);
-    unpack16<kBf16>(w.y, v[2], v[3]);
-    unpack16<kBf16>(w.z, v[4], v[5]);
-    unpack16<kBf16>(w.w, v[6], v[7]);
-  } else {
-    v[0] = from16<kBf16>(__ldcs(p + c));
-  }
+// How a row of `cols` values is walked: `head` values up to the first 16-byte
+// boundary of its first matrix, `units` whole 16-byte units of 8 values, and
+// fewer than 8 values of tail. Head and tail are one extra value for 16 threads
+// each row (thread t < 8: head, 8 <= t < 16: tail), so that no load waits for
+// another and nothing outside the row is touched.
+struct RowWalk {
+  int head, units;
+  int extra;  // this thread's extra column, or -1
+};
+__device__ __forceinline__ int row_offset(const void *row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 7);
 }
-template <bool kBf16, int V>
-__device__ __forceinline__ void store_row(uint16_t *p, int c, const float (&v)[V]) {
-  if constexpr (V == 8) {
-    __stcs(reinterpret_cast<uint4 *>(p + c),
-           make_uint4(pack16<kBf16>(v[0], v[1]), pack16<kBf16>(v[2], v[3]),
-                      pack16<kBf16>(v[4], v[5]), pack16<kBf16>(v[6], v[7])));
-  } else {
-    p[c] = to16<kBf16>(v[0]);
+__device__ __forceinline__ RowWalk row_walk(const void *row, int cols, int t) {
+  RowWalk k;
+  k.head = min((8 - row_offset(row)) & 7, cols);
+  k.units = (cols - k.head) >> 3;
+  const int tail0 = k.head + 8 * k.units;
+  k.extra = t < k.head ? t : (t >= 8 && t - 8 < cols - tail0) ? tail0 + t - 8 : -1;
+  return k;
+}
+// Unit u, packed (zeros past the last, or without a matrix). `same`: the matrix
+// has the first one's alignment; others go element by element.
+__device__ __forceinline__ uint4 load_unit(const uint16_t *row, const RowWalk &k, int u,
+                                           bool same) {
+  if (row == nullptr || u >= k.units) return make_uint4(0, 0, 0, 0);
+  const uint16_t *p = row + k.head + 8 * u;
+  if (same) return __ldcs(reinterpret_cast<const uint4 *>(p));
+  uint32_t h[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h[e] = p[e];
+  return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
+                    h[6] | (h[7] << 16));
+}
+__device__ __forceinline__ uint32_t load_extra(const uint16_t *row, const RowWalk &k) {
+  return row != nullptr && k.extra >= 0 ? row[k.extra] : 0u;
+}
+__device__ __forceinline__ void store_unit(uint16_t *row, const RowWalk &k, int u, bool same,
+                                           const uint4 &w) {
+  if (u >= k.units) return;
+  uint16_t *p = row + k.head + 8 * u;
+  if (same) {
+    __stcs(reinterpret_cast<uint4 *>(p), w);
+    return;
   }
+  const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p[e] = static_cast<uint16_t>(h[e >> 1] >> (16 * (e & 1)));
+}
+// The same for 8-bit values (same: the unit is 8 aligned bytes).
+__device__ __forceinline__ void store_unit8(uint8_t *row, const RowWalk &k, int u, bool same,
+                                            const uint2 &w) {
+  if (u >= k.units) return;
+  uint8_t *p = row + k.head + 8 * u;
+  if (same) {
+    *reinterpret_cast<uint2 *>(p) = w;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p[e] = static_cast<uint8_t>((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
+}
+template <bool kBf16>
+__device__ __forceinline__ void unit_values(const uint4 &w, float (&v)[8]) {
+  unpack16<kBf16>(w.x, v[0], v[1]);
+  unpack16<kBf16>(w.y, v[2], v[3]);
+  unpack16<kBf16>(w.z, v[4], v[5]);
+  unpack16<kBf16>(w.w, v[6], v[7]);
+}
+template <bool kBf16>
+__device__ __forceinline__ uint4 unit_pack(const float (&v)[8]) {
+  return make_uint4(pack16<kBf16>(v[0], v[1]), pack16<kBf16>(v[2], v[3]),
+                    pack16<kBf16>(v[4], v[5]), pack16<kBf16>(v[6], v[7]));
 }
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-template <int V>
-__device__ __forceinline__ void store_e4m3(uint8_t *p, int c, const float (&v)[V]) {
-  if constexpr (V == 8) {
-    *reinterpret_cast<uint2 *>(p + c) =
-        make_uint2(e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16),
-                   e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16));
-  } else {
-    p[c] = static_cast<uint8_t>(e4m3x2(v[0], 0.f));
-  }
 }
 
 // The sum of a and the largest of m over the T threads of a row (a whole block
@@ -109,9 +149,30 @@ __device__ __forceinline__ void row_reduce(float &a, float &m, float2 *red) {
   }
 }
 
-// T threads per row, V values per load, at most NV loads per thread and array:
-// rows of up to T * V * NV columns. Blocks of max(T, 128) threads.
-template <bool kBf16, int T, int V, int NV>
+// The sum of a over the T threads of a row, in one fixed order.
+template <int T>
+__device__ __forceinline__ float row_sum(float a, float *red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if constexpr (T > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+    __syncthreads();
+    a = 0.f;
+#pragma unroll
+    for (int i = 0; i < T / 32; i += 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(red + i);
+      a += v.x;
+      a += v.y;
+      a += v.z;
+      a += v.w;
+    }
+  }
+  return a;
+}
+
+// T threads per row, at most NV units per thread and array: rows of up to T * NV
+// units. Blocks of max(T, 128) threads.
+template <bool kBf16, int T, int NV>
 __global__ void __launch_bounds__(T < 128 ? 128 : T) rms_norm_kernel(const RmsCall c) {
   __shared__ float2 red[T / 32];
   constexpr int kRows = T < 128 ? 128 / T : 1;
@@ -122,69 +183,68 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) rms_norm_kernel(const RmsCa
   if (kRows > 1 && row >= c.rows) return;  // whole warps; no block barrier follows
   const int64_t r = row;
   const uint16_t *X = c.X + r * c.ldx, *R = c.R ? c.R + r * c.ldr : nullptr;
-  float h[NV][V], w[NV][V];
+  uint16_t *H = c.H ? c.H + r * c.ldh : nullptr;
+  const int cols = c.cols, off = row_offset(X);
+  const RowWalk k = row_walk(X, cols, t);
+  const bool same_r = row_offset(R) == off, same_w = row_offset(c.W) == off;
+  uint4 x[NV], q[NV], w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    x[i] = load_unit(X, k, i * T + t, true);
+    q[i] = load_unit(R, k, i * T + t, same_r);
+  }
+  const uint32_t xe = load_extra(X, k), qe = load_extra(R, k), we = load_extra(c.W, k);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) w[i] = load_unit(c.W, k, i * T + t, same_w);
+  float h[NV][8], g[NV][8];
   float sum = 0.f, top = 0.f;
+  auto add = [&](float &hv, float rv, float &gv) {
+    if (R) hv += rv;
+    gv = c.W ? gv * hv : hv;
+    sum = fmaf(hv, hv, sum);
+    if (c.scale) top = max_nan(top, fabsf(gv));
+  };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * T + t) * V;
+    float a[8];
+    unit_values<kBf16>(x[i], h[i]);
+    unit_values<kBf16>(q[i], a);
+    unit_values<kBf16>(w[i], g[i]);
 #pragma unroll
-    for (int e = 0; e < V; ++e) h[i][e] = 0.f, w[i][e] = 1.f;
-    if (col < c.cols) {
-      load_row<kBf16, V>(X, col, h[i]);
-      if (R) {
-        float x[V];
-        load_row<kBf16, V>(R, col, x);
-#pragma unroll
-        for (int e = 0; e < V; ++e) h[i][e] += x[e];
-      }
-      if (c.W) {
-        if constexpr (V == 8) {
-          const uint4 q = __ldg(reinterpret_cast<const uint4 *>(c.W + col));
-          unpack16<kBf16>(q.x, w[i][0], w[i][1]);
-          unpack16<kBf16>(q.y, w[i][2], w[i][3]);
-          unpack16<kBf16>(q.z, w[i][4], w[i][5]);
-          unpack16<kBf16>(q.w, w[i][6], w[i][7]);
-        } else {
-          w[i][0] = from16<kBf16>(__ldg(c.W + col));
-        }
-      }
-    }
+    for (int e = 0; e < 8; ++e) add(h[i][e], a[e], g[i][e]);
+    if (H) store_unit(H, k, i * T + t, row_offset(H) == off, unit_pack<kBf16>(h[i]));
   }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = (i * T + t) * V;
-    if (c.H && col < c.cols) store_row<kBf16, V>(c.H + r * c.ldh, col, h[i]);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      sum = fmaf(h[i][e], h[i][e], sum);
-      w[i][e] *= h[i][e];
-      top = max_nan(top, fabsf(w[i][e]));
-    }
-  }
+  float he = from16<kBf16>(xe), ge = from16<kBf16>(we);
+  add(he, from16<kBf16>(qe), ge);
+  if (H && k.extra >= 0) H[k.extra] = to16<kBf16>(he);
   row_reduce<T>(sum, top, red);
-  const float s = rsqrtf(sum / static_cast<float>(c.cols) + c.eps);
+  const float s = rsqrtf(sum / static_cast<float>(cols) + c.eps);
   if (t == 0 && c.rstd) c.rstd[r] = s;
   if (c.scale) {
     float scale, inv;
     e4m3_scale(top * s, scale, inv);
     if (t == 0) c.scale[r] = scale;
     uint8_t *Y = static_cast<uint8_t *>(c.Y) + r * c.ldy;
+    const bool same = ((reinterpret_cast<uintptr_t>(Y) + k.head) & 7) == 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * T + t) * V;
 #pragma unroll
-      for (int e = 0; e < V; ++e) w[i][e] = w[i][e] * s * inv;
-      if (col < c.cols) store_e4m3<V>(Y, col, w[i]);
+      for (int e = 0; e < 8; ++e) g[i][e] = g[i][e] * s * inv;
+      store_unit8(Y, k, i * T + t, same,
+                  make_uint2(e4m3x2(g[i][0], g[i][1]) | (e4m3x2(g[i][2], g[i][3]) << 16),
+                             e4m3x2(g[i][4], g[i][5]) | (e4m3x2(g[i][6], g[i][7]) << 16)));
     }
+    if (k.extra >= 0) Y[k.extra] = static_cast<uint8_t>(e4m3x2(ge * s * inv, 0.f));
   } else {
     uint16_t *Y = static_cast<uint16_t *>(c.Y) + r * c.ldy;
+    const bool same = row_offset(Y) == off;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * T + t) * V;
 #pragma unroll
-      for (int e = 0; e < V; ++e) w[i][e] *= s;
-      if (col < c.cols) store_row<kBf16, V>(Y, col, w[i]);
+      for (int e = 0; e < 8; ++e) g[i][e] *= s;
+      store_unit(Y, k, i * T + t, same, unit_pack<kBf16>(g[i]));
     }
+    if (k.extra >= 0) Y[k.extra] = to16<kBf16>(ge * s);
   }
 }
 
@@ -227,81 +287,245 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const RmsCall c) {
 
 // Blocks walk rows blockIdx.x, + gridDim.x, ...; each thread keeps the sums of
 // dw for its columns over the block's rows and writes them once, as one partial
-// row per block (and per warp, where a warp has its own row).
-template <bool kBf16, int T, int V, int NV>
-__global__ void __launch_bounds__(T < 128 ? 128 : T)
-    rms_norm_grad_kernel(const RmsGradCall c, float *part) {
-  __shared__ float2 red[2][T / 32];
-  constexpr int kRows = T < 128 ? 128 / T : 1;
-  const int t = static_cast<int>(threadIdx.x) % T;
-  const int64_t slot = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
-  grid_dependency_wait();
-  grid_launch_dependents();
-  float w[NV][V], dw[NV][V];
+// row per block (or per warp, where a warp has its own row). The launcher makes
+// the stride between a block's rows a multiple of 8 rows, so that all of them
+// have the same alignment and a thread the same columns in each.
+template <bool kBf16, int NV>
+struct GradSums {
+  uint4 w[NV];
+  uint32_t we;
+  float dw[NV][8], dwe;
+
+  template <int T>
+  __device__ __forceinline__ void begin(const RmsGradCall &c, const RowWalk &k, int off, int t) {
+    dwe = 0.f;
+    const uint32_t one = kBf16 ? 0x3f803f80u : 0x3c003c00u;  // no gain: ones
+    we = c.W ? load_extra(c.W, k) : one & 0xffffu;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+      w[i] = c.W ? load_unit(c.W, k, i * T + t, row_offset(c.W) == off)
+                 : make_uint4(one, one, one, one);
+    }
+  }
+  template <int T>
+  __device__ __forceinline__ void end(float *out, const RowWalk &k, int t) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (i * T + t >= k.units) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[k.head + 8 * (i * T + t) + e] = dw[i][e];
+    }
+    if (k.extra >= 0) out[k.extra] = dwe;
+  }
+};
+
+// One row by T threads. get(a, i): packed unit i of this thread of matrix a (0:
+// dY, 1: H, 2: dH); extra[a]: its extra value. Units are read twice, before and
+// after the reduction, instead of being held in registers over it. between() runs
+// behind the reduction. X: the row of dX.
+template <bool kBf16, int T, int NV, typename Get, typename Between>
+__device__ __forceinline__ void grad_row(uint16_t *X, int cols, const RowWalk &k, bool same,
+                                         int t, GradSums<kBf16, NV> &sums, float s,
+                                         const uint32_t (&extra)[3], float *red, Get &&get,
+                                         Between &&between) {
+  // With t = dy s: dw += t h and sum(g n) = sum(t w h), so that
+  // dx = s (dy w) - h (s^2 mean(g n)) + dh takes three operations per value.
+  float dot = 0.f;
+  auto first = [&](float yv, float hv, float wv, float &acc) {
+    const float ts = yv * s;
+    acc = fmaf(ts, hv, acc);
+    dot = fmaf(ts * wv, hv, dot);
+  };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * T + t) * V;
+    float yv[8], hv[8], wv[8];
+    unit_values<kBf16>(get(0, i), yv);
+    unit_values<kBf16>(get(1, i), hv);
+    unit_values<kBf16>(sums.w[i], wv);
 #pragma unroll
-    for (int e = 0; e < V; ++e) w[i][e] = 1.f, dw[i][e] = 0.f;
-    if (c.W && col < c.cols) load_row<kBf16, V>(c.W, col, w[i]);
+    for (int e = 0; e < 8; ++e) first(yv[e], hv[e], wv[e], sums.dw[i][e]);
   }
-  const float inv_n = 1.f / static_cast<float>(c.cols);
-  int flip = 0;
-  for (int64_t r = slot; r < c.rows; r += static_cast<int64_t>(gridDim.x) * kRows) {
-    const uint16_t *dY = c.dY + r * c.lddy, *H = c.H + r * c.ldh;
-    const float s = c.rstd[r];
-    float g[NV][V], n[NV][V], b[NV][V];
-    float dot = 0.f, unused = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = (i * T + t) * V;
-#pragma unroll
-      for (int e = 0; e < V; ++e) g[i][e] = n[i][e] = b[i][e] = 0.f;
-      if (col < c.cols) {
-        load_row<kBf16, V>(dY, col, g[i]);
-        load_row<kBf16, V>(H, col, n[i]);
-        if (c.dH) load_row<kBf16, V>(c.dH + r * c.lddh, col, b[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        n[i][e] *= s;
-        dw[i][e] = fmaf(g[i][e], n[i][e], dw[i][e]);
-        g[i][e] *= w[i][e];
-        dot = fmaf(g[i][e], n[i][e], dot);
-      }
-    }
-    // Two sets of slots in turn: a warp may write the next row's while another
-    // still reads this row's.
-    row_reduce<T>(dot, unused, red[flip]);
-    flip ^= 1;
-    const float mean = dot * inv_n;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = (i * T + t) * V;
-#pragma unroll
-      for (int e = 0; e < V; ++e) g[i][e] = fmaf(s, g[i][e] - n[i][e] * mean, b[i][e]);
-      if (col < c.cols) store_row<kBf16, V>(c.dX + r * c.lddx, col, g[i]);
-    }
-  }
-  if (part == nullptr) return;
+  if (k.extra >= 0)
+    first(from16<kBf16>(extra[0]), from16<kBf16>(extra[1]), from16<kBf16>(sums.we), sums.dwe);
+  dot = row_sum<T>(dot, red);
+  between();
+  const float back = -s * s * (dot / static_cast<float>(cols));
+  auto second = [&](float yv, float hv, float wv, float bv) {
+    return fmaf(yv * wv, s, fmaf(hv, back, bv));
+  };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * T + t) * V;
+    float yv[8], hv[8], wv[8], bv[8];
+    unit_values<kBf16>(get(0, i), yv);
+    unit_values<kBf16>(get(1, i), hv);
+    unit_values<kBf16>(sums.w[i], wv);
+    unit_values<kBf16>(get(2, i), bv);
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (col + e < c.cols) part[slot * c.cols + col + e] = dw[i][e];
+    for (int e = 0; e < 8; ++e) yv[e] = second(yv[e], hv[e], wv[e], bv[e]);
+    store_unit(X, k, i * T + t, same, unit_pack<kBf16>(yv));
   }
+  if (k.extra >= 0)
+    X[k.extra] = to16<kBf16>(second(from16<kBf16>(extra[0]), from16<kBf16>(extra[1]),
+                                    from16<kBf16>(sums.we), from16<kBf16>(extra[2])));
 }
 
-// Rows of any length: one block per group of rows; the partial sums of dw live
+// Short rows: one warp per row, straight from global memory; the warps in
+// residence hide each other's latency.
+template <int NV>
+constexpr int kGradWarpBlocks = NV == 1 ? 6 : 4;  // per SM
+
+template <bool kBf16, int NV>
+__global__ void __launch_bounds__(128, kGradWarpBlocks<NV>)
+    rms_norm_grad_warp_kernel(const RmsGradCall c, float *part) {
+  const int t = static_cast<int>(threadIdx.x) & 31;
+  const int64_t slot = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int off = row_offset(c.dY + slot * c.lddy);
+  const RowWalk k = row_walk(c.dY + slot * c.lddy, c.cols, t);
+  GradSums<kBf16, NV> sums;
+  sums.template begin<32>(c, k, off, t);
+  for (int64_t r = slot; r < c.rows; r += static_cast<int64_t>(gridDim.x) * 4) {
+    const uint16_t *rows[3] = {c.dY + r * c.lddy, c.H + r * c.ldh,
+                               c.dH ? c.dH + r * c.lddh : nullptr};
+    uint4 v[3][NV];
+    uint32_t extra[3];
+#pragma unroll
+    for (int a = 0; a < 3; ++a) {
+      const bool same = row_offset(rows[a]) == off;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[a][i] = load_unit(rows[a], k, i * 32 + t, same);
+      extra[a] = load_extra(rows[a], k);
+    }
+    uint16_t *X = c.dX + r * c.lddx;
+    grad_row<kBf16, 32, NV>(X, c.cols, k, row_offset(X) == off, t, sums, c.rstd[r], extra, nullptr,
+                            [&](int a, int i) { return v[a][i]; }, [] {});
+  }
+  if (part != nullptr) sums.template end<32>(part + slot * c.cols, k, t);
+}
+
+// Longer rows: one block per row, rows brought by bulk copies into a ring of
+// `stages` rows of shared memory (the whole units of dY, H and dH, which must be
+// aligned alike, and dX with them), so stages - 1 rows are always in flight
+// whatever the threads do, and the values cost no registers between the two
+// passes over them. (Prefetching the next row into registers reached 96 us at
+// 8192 x 8192, and 143 us once the extra columns' loads shared their
+// scoreboards.) What bounds it beside memory is instructions, about 20 per
+// value: so no division for the ring's indexes and no 64-bit products per row.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+constexpr int kMaxGradStages = 4;
+
+template <bool kBf16, int T>
+__global__ void __launch_bounds__(T, 1024 / T)
+    rms_norm_grad_kernel(const RmsGradCall c, float *part, int stages, uint32_t *err_word) {
+  constexpr int NV = 2;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kMaxGradStages];
+  __shared__ __align__(16) float red[2][T / 32];
+  __shared__ int abort_flag;
+  volatile int *abort = &abort_flag;
+  const int t = static_cast<int>(threadIdx.x);
+  if (t == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full[i]), 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  // Pointers to this block's first row, advanced by a fixed number of elements.
+  const int64_t slot = blockIdx.x;
+  const int rows = static_cast<int>((c.rows - slot + gridDim.x - 1) / gridDim.x);
+  const uint16_t *Y = c.dY + slot * c.lddy, *H = c.H + slot * c.ldh;
+  const uint16_t *B = c.dH ? c.dH + slot * c.lddh : nullptr;
+  uint16_t *X = c.dX + slot * c.lddx;
+  const float *rstd = c.rstd + slot;
+  const int64_t step_y = gridDim.x * c.lddy, step_h = gridDim.x * c.ldh;
+  const int64_t step_b = gridDim.x * c.lddh, step_x = gridDim.x * c.lddx;
+  const RowWalk k = row_walk(Y, c.cols, t);
+  const bool ragged = c.cols != 8 * k.units;  // rows with a head or a tail
+  const uint32_t bytes = static_cast<uint32_t>(k.units) * 16u;
+  const uint32_t slab = (static_cast<uint32_t>(c.cols) / 8u) * 16u;  // one matrix's row
+  // The next row to copy (thread 0), and its stage.
+  const uint16_t *fy = Y + k.head, *fh = H + k.head, *fb = B ? B + k.head : nullptr;
+  int filled = 0, fstage = 0;
+  auto fill = [&] {
+    if (filled == rows || bytes == 0) return;
+    const uint32_t bar = smem_u32(&full[fstage]);
+    const uint32_t dst = smem_u32(ring) + static_cast<uint32_t>(fstage) * 3u * slab;
+    mbar_arrive_expect_tx(bar, fb ? 3u * bytes : 2u * bytes);
+    bulk_load(dst, fy, bytes, bar);
+    bulk_load(dst + slab, fh, bytes, bar);
+    if (fb) bulk_load(dst + 2 * slab, fb, bytes, bar);
+    fy += step_y, fh += step_h;
+    if (fb) fb += step_b;
+    ++filled;
+    if (++fstage == stages) fstage = 0;
+  };
+  if (t == 0)
+    for (int n = 0; n < stages - 1; ++n) fill();
+  GradSums<kBf16, NV> sums;
+  sums.template begin<T>(c, k, row_offset(Y), t);
+  uint32_t stage = 0, phase = 0;
+  float s = *rstd;
+  uint32_t extra[3] = {0, 0, 0};
+  for (int n = 0; n < rows; ++n) {
+    if (ragged) {
+      extra[0] = load_extra(Y, k);
+      extra[1] = load_extra(H, k);
+      extra[2] = load_extra(B, k);
+    }
+    float s2 = 0.f;
+    if (n + 1 < rows) s2 = rstd[gridDim.x];
+    if (bytes != 0)
+      mbar_wait_bounded(smem_u32(&full[stage]), phase, abort, err_word, kWaitFull);
+    const uint8_t *row = ring + stage * 3u * slab + t * 16;
+    grad_row<kBf16, T, NV>(
+        X, c.cols, k, true, t, sums, s, extra, red[n & 1],
+        [&](int a, int i) {
+          return i * T + t < k.units && (a < 2 || B != nullptr)
+                     ? *reinterpret_cast<const uint4 *>(row + a * slab + i * T * 16)
+                     : make_uint4(0, 0, 0, 0);
+        },
+        [&] {
+          // Behind the reduction's barrier every thread has left the previous
+          // row, whose stage takes the row stages - 1 ahead.
+          if (t == 0) fill();
+        });
+    s = s2;
+    Y += step_y, H += step_h, X += step_x, rstd += gridDim.x;
+    if (B) B += step_b;
+    if (++stage == static_cast<uint32_t>(stages)) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  // After a wait that gave up: never leave with a copy still writing.
+  if (t == 0 && *abort && bytes != 0) {
+    volatile int never = 0;
+    for (int i = rows > stages ? rows - stages : 0; i < rows; ++i)
+      mbar_wait_bounded(smem_u32(&full[i % stages]), static_cast<uint32_t>(i / stages) & 1u, &never,
+                        err_word, kWaitDrain);
+  }
+  if (part != nullptr) sums.template end<T>(part + slot * c.cols, k, t);
+}
+
+// Rows of any length and alignment: one block per group of rows; the partial sums of dw live
 // in the block's partial row in global memory.
 template <bool kBf16>
 __global__ void __launch_bounds__(1024)
     rms_norm_grad_long_kernel(const RmsGradCall c, float *part) {
-  __shared__ float2 red[2][32];
+  __shared__ __align__(16) float red[2][32];
   grid_dependency_wait();
   grid_launch_dependents();
   const float inv_n = 1.f / static_cast<float>(c.cols);
@@ -311,13 +535,13 @@ __global__ void __launch_bounds__(1024)
   for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
     const uint16_t *dY = c.dY + r * c.lddy, *H = c.H + r * c.ldh;
     const float s = c.rstd[r];
-    float dot = 0.f, unused = 0.f;
+    float dot = 0.f;
     for (int64_t j = threadIdx.x; j < c.cols; j += 1024) {
       const float d = from16<kBf16>(dY[j]), n = from16<kBf16>(H[j]) * s;
       dot = fmaf(c.W ? d * from16<kBf16>(c.W[j]) : d, n, dot);
       if (mine) mine[j] = first ? d * n : fmaf(d, n, mine[j]);  // this thread's own element
     }
-    row_reduce<1024>(dot, unused, red[flip]);
+    dot = row_sum<1024>(dot, red[flip]);
     flip ^= 1;
     const float mean = dot * inv_n;
     for (int64_t j = threadIdx.x; j < c.cols; j += 1024) {
@@ -331,11 +555,12 @@ __global__ void __launch_bounds__(1024)
 }
 
 template <typename... P, typename... A>
-cudaError_t launch_pdl(void (*kern)(P...), unsigned grid, unsigned block, cudaStream_t stream,
-                       A... args) {
+cudaError_t launch_pdl(void (*kern)(P...), unsigned grid, unsigned block, int smem,
+                       cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -345,38 +570,27 @@ cudaError_t launch_pdl(void (*kern)(P...), unsigned grid, unsigned block, cudaSt
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-bool vec_ok(const void *p, int64_t ld, int units) {
-  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % units == 0);
-}
-
-template <bool kBf16, int V>
+template <bool kBf16>
 cudaError_t launch_norm(const RmsCall &c, cudaStream_t stream) {
-  const int units = (c.cols + V - 1) / V;  // loads per row and array
+  const int units = c.cols / 8;  // at most, whatever the alignment
   const unsigned rows = static_cast<unsigned>(c.rows);
-  if (units <= 32) return launch_pdl(rms_norm_kernel<kBf16, 32, V, 1>, (rows + 3) / 4, 128, stream, c);
-  if (units <= 128) return launch_pdl(rms_norm_kernel<kBf16, 32, V, 4>, (rows + 3) / 4, 128, stream, c);
-  if (units <= 256) return launch_pdl(rms_norm_kernel<kBf16, 128, V, 2>, rows, 128, stream, c);
-  if (units <= 512) return launch_pdl(rms_norm_kernel<kBf16, 256, V, 2>, rows, 256, stream, c);
-  if (units <= 1024) return launch_pdl(rms_norm_kernel<kBf16, 512, V, 2>, rows, 512, stream, c);
-  if (units <= 2048) return launch_pdl(rms_norm_kernel<kBf16, 1024, V, 2>, rows, 1024, stream, c);
-  if (V == 1 && units <= 8192)
-    return launch_pdl(rms_norm_kernel<kBf16, 1024, V, 8 / V>, rows, 1024, stream, c);
-  return launch_pdl(rms_norm_long_kernel<kBf16>, rows, 1024, stream, c);
+  if (units <= 32) return launch_pdl(rms_norm_kernel<kBf16, 32, 1>, (rows + 3) / 4, 128, 0, stream, c);
+  if (units <= 64) return launch_pdl(rms_norm_kernel<kBf16, 32, 2>, (rows + 3) / 4, 128, 0, stream, c);
+  if (units <= 128) return launch_pdl(rms_norm_kernel<kBf16, 128, 1>, rows, 128, 0, stream, c);
+  if (units <= 256) return launch_pdl(rms_norm_kernel<kBf16, 128, 2>, rows, 128, 0, stream, c);
+  if (units <= 512) return launch_pdl(rms_norm_kernel<kBf16, 256, 2>, rows, 256, 0, stream, c);
+  if (units <= 1024) return launch_pdl(rms_norm_kernel<kBf16, 512, 2>, rows, 512, 0, stream, c);
+  if (units <= 2048) return launch_pdl(rms_norm_kernel<kBf16, 1024, 2>, rows, 1024, 0, stream, c);
+  return launch_pdl(rms_norm_long_kernel<kBf16>, rows, 1024, 0, stream, c);
 }
 
-template <bool kBf16, int T, int V, int NV>
-cudaError_t launch_grad_form(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_t stream) {
-  constexpr int kThreads = T < 128 ? 128 : T;
-  constexpr int kRows = kThreads / T;
-  // One wave: as many blocks as are resident at once, or one per row.
-  auto kern = rms_norm_grad_kernel<kBf16, T, V, NV>;
-  int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, 0);
-  if (e != cudaSuccess) return e;
-  const int64_t blocks = std::min<int64_t>(static_cast<int64_t>(std::max(per_sm, 1)) * dev.sm_count,
-                                           (static_cast<int64_t>(c.rows) + kRows - 1) / kRows);
-  const int64_t parts = blocks * kRows;
+// Runs launch(part) with a partial-sum matrix of `parts` rows when dW is wanted,
+// then adds its rows.
+template <typename F>
+cudaError_t with_partials(const DeviceInfo &dev, const RmsGradCall &c, int64_t parts,
+                          cudaStream_t stream, F &&launch) {
   void *part = nullptr;
+  cudaError_t e;
   if (c.dW != nullptr) {
     cudaMemPool_t pool;
     e = device_pool(dev, &pool);
@@ -384,8 +598,7 @@ cudaError_t launch_grad_form(const DeviceInfo &dev, const RmsGradCall &c, cudaSt
     e = cudaMallocFromPoolAsync(&part, static_cast<size_t>(parts) * c.cols * 4, pool, stream);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(kern, static_cast<unsigned>(blocks), kThreads, stream, c,
-                 static_cast<float *>(part));
+  e = launch(static_cast<float *>(part));
   if (part != nullptr) {
     if (e == cudaSuccess)
       e = launch_col_sums(c.bf16, static_cast<const float *>(part), static_cast<int>(parts),
@@ -396,39 +609,68 @@ cudaError_t launch_grad_form(const DeviceInfo &dev, const RmsGradCall &c, cudaSt
   return e;
 }
 
+// Blocks of one wave, `resident` per SM: fewer than the rows only as a multiple
+// of 8 (a block's rows must be a multiple of 8 apart).
+int64_t grad_blocks(const DeviceInfo &dev, int64_t rows, int resident) {
+  const int64_t wave = static_cast<int64_t>(std::max(resident, 1)) * dev.sm_count / 8 * 8;
+  return std::min<int64_t>(std::max<int64_t>(wave, 8), rows);
+}
+
+template <bool kBf16, int NV>
+cudaError_t launch_grad_warp(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_t stream) {
+  const int64_t blocks = grad_blocks(dev, (static_cast<int64_t>(c.rows) + 3) / 4,
+                                     kGradWarpBlocks<NV>);
+  return with_partials(dev, c, blocks * 4, stream, [&](float *part) {
+    return launch_pdl(rms_norm_grad_warp_kernel<kBf16, NV>, static_cast<unsigned>(blocks), 128, 0,
+                      stream, c, part);
+  });
+}
+
+template <bool kBf16, int T>
+cudaError_t launch_grad_ring(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_t stream) {
+  auto kern = rms_norm_grad_kernel<kBf16, T>;
+  // 1024 threads per SM share about 200 KB of rows in flight; the blocks beside
+  // each other hide each other's reductions.
+  const int stage = c.cols / 8 * 16 * 3;
+  const int room = 200 * T;
+  const int stages = std::max(2, std::min(kMaxGradStages, room / std::max(stage, 1)));
+  const int smem = stages * stage;
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem, dev.device);
+  if (e != cudaSuccess) return e;
+  int per_sm = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, T, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = grad_blocks(dev, c.rows, per_sm);
+  return with_partials(dev, c, blocks, stream, [&](float *part) {
+    return launch_pdl(kern, static_cast<unsigned>(blocks), T, smem, stream, c, part, stages,
+                      dev.err_word);
+  });
+}
+
 template <bool kBf16>
 cudaError_t launch_grad_long(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_t stream) {
   const int blocks = std::min(c.rows, 2 * dev.sm_count);
-  void *part = nullptr;
-  cudaError_t e = cudaSuccess;
-  if (c.dW != nullptr) {
-    cudaMemPool_t pool;
-    e = device_pool(dev, &pool);
-    if (e != cudaSuccess) return e;
-    e = cudaMallocFromPoolAsync(&part, static_cast<size_t>(blocks) * c.cols * 4, pool, stream);
-    if (e != cudaSuccess) return e;
-  }
-  e = launch_pdl(rms_norm_grad_long_kernel<kBf16>, static_cast<unsigned>(blocks), 1024, stream, c,
-                 static_cast<float *>(part));
-  if (part != nullptr) {
-    if (e == cudaSuccess)
-      e = launch_col_sums(c.bf16, static_cast<const float *>(part), blocks, c.cols, c.cols, c.dW,
-                          stream);
-    cudaError_t f = cudaFreeAsync(part, stream);
-    if (e == cudaSuccess) e = f;
-  }
-  return e;
+  return with_partials(dev, c, blocks, stream, [&](float *part) {
+    return launch_pdl(rms_norm_grad_long_kernel<kBf16>, static_cast<unsigned>(blocks), 1024, 0,
+                      stream, c, part);
+  });
 }
 
-template <bool kBf16, int V>
+template <bool kBf16>
 cudaError_t launch_grad(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_t stream) {
-  const int units = (c.cols + V - 1) / V;
-  if (units <= 32) return launch_grad_form<kBf16, 32, V, 1>(dev, c, stream);
-  if (units <= 128) return launch_grad_form<kBf16, 128, V, 1>(dev, c, stream);
-  if (units <= 256) return launch_grad_form<kBf16, 256, V, 1>(dev, c, stream);
-  if (units <= 512) return launch_grad_form<kBf16, 512, V, 1>(dev, c, stream);
-  if (units <= 1024) return launch_grad_form<kBf16, 1024, V, 1>(dev, c, stream);
-  if (V == 1 && units <= 8192) return launch_grad_form<kBf16, 1024, V, 8 / V>(dev, c, stream);
+  const int units = c.cols / 8;  // at most, whatever the alignment
+  auto alike = [&](const void *p, int64_t ld) {
+    return p == nullptr || ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(c.dY)) % 16 == 0 &&
+                            (ld - c.lddy) % 8 == 0);
+  };
+  if (units <= 32) return launch_grad_warp<kBf16, 1>(dev, c, stream);
+  if (units <= 64) return launch_grad_warp<kBf16, 2>(dev, c, stream);
+  if (!alike(c.H, c.ldh) || !alike(c.dH, c.lddh) || !alike(c.dX, c.lddx))
+    return launch_grad_long<kBf16>(dev, c, stream);
+  if (units <= 256) return launch_grad_ring<kBf16, 128>(dev, c, stream);
+  if (units <= 512) return launch_grad_ring<kBf16, 256>(dev, c, stream);
+  if (units <= 1024) return launch_grad_ring<kBf16, 512>(dev, c, stream);
+  if (units <= 2048) return launch_grad_ring<kBf16, 1024>(dev, c, stream);
   return launch_grad_long<kBf16>(dev, c, stream);
 }
 
@@ -436,23 +678,14 @@ cudaError_t launch_grad(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_
 
 cudaError_t launch_rms_norm(const DeviceInfo &dev, const RmsCall &c, cudaStream_t stream) {
   (void)dev;
-  // 16-byte loads need 16-byte aligned rows (8-byte ones for the e4m3 output)
-  // and whole groups of 8 columns.
-  const bool vec = c.cols % 8 == 0 && vec_ok(c.X, c.ldx, 8) && vec_ok(c.R, c.ldr, 8) &&
-                   vec_ok(c.H, c.ldh, 8) && vec_ok(c.Y, c.ldy, 8) && vec_ok(c.W, 8, 8);
-  if (c.bf16) return vec ? launch_norm<true, 8>(c, stream) : launch_norm<true, 1>(c, stream);
-  return vec ? launch_norm<false, 8>(c, stream) : launch_norm<false, 1>(c, stream);
+  return c.bf16 ? launch_norm<true>(c, stream) : launch_norm<false>(c, stream);
 }
 
 cudaError_t launch_rms_norm_grad(const DeviceInfo &dev, const RmsGradCall &c,
                                  cudaStream_t stream) {
   if (c.rows == 0)
     return c.dW ? launch_col_sums(c.bf16, nullptr, 0, c.cols, c.cols, c.dW, stream) : cudaSuccess;
-  const bool vec = c.cols % 8 == 0 && vec_ok(c.dY, c.lddy, 8) && vec_ok(c.H, c.ldh, 8) &&
-                   vec_ok(c.dH, c.lddh, 8) && vec_ok(c.dX, c.lddx, 8) && vec_ok(c.W, 8, 8);
-  if (c.bf16)
-    return vec ? launch_grad<true, 8>(dev, c, stream) : launch_grad<true, 1>(dev, c, stream);
-  return vec ? launch_grad<false, 8>(dev, c, stream) : launch_grad<false, 1>(dev, c, stream);
+  return c.bf16 ? launch_grad<true>(dev, c, stream) : launch_grad<false>(dev, c, stream);
 }
 
 }  // namespace dgr
