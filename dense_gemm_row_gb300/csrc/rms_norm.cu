@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const RmsCall c) {
 
 // Blocks walk rows blockIdx.x, + gridDim.x, ...; each thread keeps the sums of
 // dw for its columns over the block's rows and writes them once, as one partial
-// row per block (or per warp, where a warp has its own row). The launcher makes
+// row per block. The launcher makes
 // the stride between a block's rows a multiple of 8 rows, so that all of them
 // have the same alignment and a thread the same columns in each.
 template <bool kBf16, int NV>
@@ -403,7 +403,15 @@ __global__ void __launch_bounds__(128, kGradWarpBlocks<NV>)
     grad_row<kBf16, 32, NV>(X, c.cols, k, row_offset(X) == off, t, sums, c.rstd[r], extra, nullptr,
                             [&](int a, int i) { return v[a][i]; }, [] {});
   }
-  if (part != nullptr) sums.template end<32>(part + slot * c.cols, k, t);
+  if (part == nullptr) return;
+  // The block's warps add their sums in warp order (their rows may be aligned
+  // differently, so a column sits in different lanes).
+  __shared__ float mine[4][64 * NV * 4 + 8];
+  sums.template end<32>(mine[threadIdx.x >> 5], k, t);
+  __syncthreads();
+  for (int j = threadIdx.x; j < c.cols; j += 128)
+    part[blockIdx.x * static_cast<int64_t>(c.cols) + j] =
+        ((mine[0][j] + mine[1][j]) + mine[2][j]) + mine[3][j];
 }
 
 // Longer rows: one block per row, rows brought by bulk copies into a ring of
@@ -425,10 +433,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 constexpr int kMaxGradStages = 4;
 
-template <bool kBf16, int T>
+template <bool kBf16, int T, int NV>
 __global__ void __launch_bounds__(T, 1024 / T)
     rms_norm_grad_kernel(const RmsGradCall c, float *part, int stages, uint32_t *err_word) {
-  constexpr int NV = 2;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kMaxGradStages];
   __shared__ __align__(16) float red[2][T / 32];
@@ -609,10 +616,12 @@ cudaError_t with_partials(const DeviceInfo &dev, const RmsGradCall &c, int64_t p
   return e;
 }
 
-// Blocks of one wave, `resident` per SM: fewer than the rows only as a multiple
-// of 8 (a block's rows must be a multiple of 8 apart).
+// Blocks of one wave, `resident` per SM but at most 4 (each costs a partial row
+// to write and add): fewer than the rows only as a multiple of 8 (a block's rows
+// must be a multiple of 8 apart).
 int64_t grad_blocks(const DeviceInfo &dev, int64_t rows, int resident) {
-  const int64_t wave = static_cast<int64_t>(std::max(resident, 1)) * dev.sm_count / 8 * 8;
+  const int64_t wave =
+      static_cast<int64_t>(std::min(std::max(resident, 1), 4)) * dev.sm_count / 8 * 8;
   return std::min<int64_t>(std::max<int64_t>(wave, 8), rows);
 }
 
@@ -620,15 +629,15 @@ template <bool kBf16, int NV>
 cudaError_t launch_grad_warp(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_t stream) {
   const int64_t blocks = grad_blocks(dev, (static_cast<int64_t>(c.rows) + 3) / 4,
                                      kGradWarpBlocks<NV>);
-  return with_partials(dev, c, blocks * 4, stream, [&](float *part) {
+  return with_partials(dev, c, blocks, stream, [&](float *part) {
     return launch_pdl(rms_norm_grad_warp_kernel<kBf16, NV>, static_cast<unsigned>(blocks), 128, 0,
                       stream, c, part);
   });
 }
 
-template <bool kBf16, int T>
+template <bool kBf16, int T, int NV = 2>
 cudaError_t launch_grad_ring(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_t stream) {
-  auto kern = rms_norm_grad_kernel<kBf16, T>;
+  auto kern = rms_norm_grad_kernel<kBf16, T, NV>;
   // 1024 threads per SM share about 200 KB of rows in flight; the blocks beside
   // each other hide each other's reductions.
   const int stage = c.cols / 8 * 16 * 3;
@@ -667,6 +676,7 @@ cudaError_t launch_grad(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_
   if (units <= 64) return launch_grad_warp<kBf16, 2>(dev, c, stream);
   if (!alike(c.H, c.ldh) || !alike(c.dH, c.lddh) || !alike(c.dX, c.lddx))
     return launch_grad_long<kBf16>(dev, c, stream);
+  if (units <= 128) return launch_grad_ring<kBf16, 128, 1>(dev, c, stream);
   if (units <= 256) return launch_grad_ring<kBf16, 128>(dev, c, stream);
   if (units <= 512) return launch_grad_ring<kBf16, 256>(dev, c, stream);
   if (units <= 1024) return launch_grad_ring<kBf16, 512>(dev, c, stream);
