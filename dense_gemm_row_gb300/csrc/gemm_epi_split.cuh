@@ -32,6 +32,16 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// True in one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(p)
+               :
+               : "memory");
+  return p != 0;
+}
+
 __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t cluster_addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
@@ -188,7 +198,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   extern __shared__ uint8_t smem_raw[];
   SplitSmem<kMP> &sm = *reinterpret_cast<SplitSmem<kMP> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int *abort = &sm.abort;
   const int cl = p.cl;
   const int rank = cl > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -235,13 +245,15 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   SplitRow first;
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint32_t bytes = Cf::kBBytes + static_cast<uint32_t>(p.mp) * kRowBytes;
-      uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(smem_u32(&sm.empty[stage]), phase ^ 1u, abort, p.err_word,
-                               kWaitEmpty))
-          break;
+    // The whole warp runs the loop and one elected lane issues: control flow and
+    // operands are then uniform to the compiler, which keeps the TMA's and the
+    // MMA's operands in uniform registers.
+    const uint32_t bytes = Cf::kBBytes + static_cast<uint32_t>(p.mp) * kRowBytes;
+    uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait_bounded(smem_u32(&sm.empty[stage]), phase ^ 1u, abort, p.err_word, kWaitEmpty))
+        break;
+      if (elect_one()) {
         const uint32_t bar = smem_u32(&sm.full[stage]);
         mbar_arrive_expect_tx(bar, bytes);
         const int k0 = kb * kBK;
@@ -252,40 +264,40 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
           tma_load_3d(smem_u32(sm.b[stage]) + kRowBytes * 64, &tmB, bar, n0 + 64, k0, 0);
         }
         tma_load_3d(smem_u32(sm.a[stage]), &tmA, bar, k0, m0, 0);
-        issued |= 1u << stage;
-        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-        if (++stage == Cf::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
-      // Never leave with a copy still writing into shared memory.
-      for (int s = 0; s < Cf::kStages; ++s)
-        if (issued & (1u << s))
-          drain_wait(smem_u32(&sm.full[s]), (issued_parity >> s) & 1u, p.err_word);
+      __syncwarp();
+      issued |= 1u << stage;
+      issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+      if (++stage == Cf::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
+    // Never leave with a copy still writing into shared memory.
+    for (int s = 0; s < Cf::kStages; ++s)
+      if (issued & (1u << s))
+        drain_wait(smem_u32(&sm.full[s]), (issued_parity >> s) & 1u, p.err_word);
     __syncwarp();
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
-    if (lane == 0) {
-      const bool kmajor = kE4m3 || p.b_t;
-      // The MMA's A operand is the weights' tile: K-major rows of n, or N-major
-      // rows of k (LBO = one 64-column box, 16 k-rows per MMA).
-      const uint64_t wdesc = kmajor
-                                 ? smem_desc(smem_u32(sm.b[0]), 16, kAtomBytes, 2u)
-                                 : smem_desc(smem_u32(sm.b[0]), kRowBytes * 64, kAtomBytes, 2u);
-      const uint64_t xdesc = smem_desc(smem_u32(sm.a[0]), 16, kAtomBytes, 2u);
-      const uint32_t wstep = (kmajor ? 32u : kRowBytes * 16) >> 4;
-      uint32_t stage = 0, phase = 0;
-      bool ok = true, any = false;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(smem_u32(&sm.full[stage]), phase, abort, p.err_word, kWaitFull)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint64_t wd = wdesc + stage * (Cf::kBBytes >> 4);
-        const uint64_t xd = xdesc + stage * (Cf::kABytes >> 4);
+    const bool kmajor = kE4m3 || p.b_t;
+    // The MMA's A operand is the weights' tile: K-major rows of n, or N-major
+    // rows of k (LBO = one 64-column box, 16 k-rows per MMA).
+    const uint64_t wdesc = kmajor ? smem_desc(smem_u32(sm.b[0]), 16, kAtomBytes, 2u)
+                                  : smem_desc(smem_u32(sm.b[0]), kRowBytes * 64, kAtomBytes, 2u);
+    const uint64_t xdesc = smem_desc(smem_u32(sm.a[0]), 16, kAtomBytes, 2u);
+    const uint32_t wstep = (kmajor ? 32u : kRowBytes * 16) >> 4;
+    uint32_t stage = 0, phase = 0;
+    bool ok = true, any = false;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait_bounded(smem_u32(&sm.full[stage]), phase, abort, p.err_word, kWaitFull)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint64_t wd = wdesc + stage * (Cf::kBBytes >> 4);
+      const uint64_t xd = xdesc + stage * (Cf::kABytes >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           const uint32_t acc = kk > 0 || kb > kb0 ? 1u : 0u;
@@ -295,19 +307,24 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
             tc_mma_f16(tmem_base, wd + kk * wstep, xd + kk * 2, p.idesc, acc);
           }
         }
-        any = true;
         tc_commit(smem_u32(&sm.empty[stage]));
-        if (++stage == Cf::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
-      if (ok) tc_commit(smem_u32(&sm.done));
-      if (any) {  // never leave with an MMA still reading shared memory or writing TMEM
-        tc_commit(smem_u32(&sm.drain));
-        drain_wait(smem_u32(&sm.drain), 0, p.err_word);
+      __syncwarp();
+      any = true;
+      if (++stage == Cf::kStages) {
+        stage = 0;
+        phase ^= 1u;
       }
     }
+    // A commit covers the MMAs of the lane that issues it: the same lane is
+    // elected each time (the lowest of a full warp).
+    if (elect_one()) {
+      if (ok) tc_commit(smem_u32(&sm.done));
+      if (any) tc_commit(smem_u32(&sm.drain));
+    }
+    __syncwarp();
+    // Never leave with an MMA still reading shared memory or writing TMEM.
+    if (any) drain_wait(smem_u32(&sm.drain), 0, p.err_word);
     __syncwarp();
   } else {
     // ------------------------------------------- accumulator -> partial sums
