@@ -19,6 +19,7 @@
 
 #include "epi.cuh"
 #include "gemm_tc_kernel.cuh"
+#include "tc_issue.cuh"
 
 namespace dgr {
 namespace {
@@ -30,16 +31,6 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-// True in one lane of the (converged) warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n"
-               : "=r"(p)
-               :
-               : "memory");
-  return p != 0;
 }
 
 __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t cluster_addr) {
@@ -198,7 +189,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   extern __shared__ uint8_t smem_raw[];
   SplitSmem<kMP> &sm = *reinterpret_cast<SplitSmem<kMP> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   volatile int *abort = &sm.abort;
   const int cl = p.cl;
   const int rank = cl > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -223,9 +214,9 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = sm.tmem_base;
-  // Launched as a programmatic dependent: the set-up above overlaps the previous
-  // kernel's tail; nothing in global memory is touched before this.
-  grid_dependency_wait();
+  // Launched as a programmatic dependent: the set-up overlaps the previous
+  // kernel's tail. Each role that touches global memory waits for that kernel
+  // just before it does, with its loop's code already fetched.
   grid_launch_dependents();
 
   // Token tiles of one column block are neighbours, so its weights are read
@@ -245,14 +236,12 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   SplitRow first;
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    // The whole warp runs the loop and one elected lane issues: control flow and
-    // operands are then uniform to the compiler, which keeps the TMA's and the
-    // MMA's operands in uniform registers.
     const uint32_t bytes = Cf::kBBytes + static_cast<uint32_t>(p.mp) * kRowBytes;
     uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (!mbar_wait_bounded(smem_u32(&sm.empty[stage]), phase ^ 1u, abort, p.err_word, kWaitEmpty))
+      if (!mbar_wait_lazy(smem_u32(&sm.empty[stage]), phase ^ 1u, abort, p.err_word, kWaitEmpty))
         break;
+      if (kb == kb0) grid_dependency_wait();
       if (elect_one()) {
         const uint32_t bar = smem_u32(&sm.full[stage]);
         mbar_arrive_expect_tx(bar, bytes);
@@ -290,7 +279,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     uint32_t stage = 0, phase = 0;
     bool ok = true, any = false;
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (!mbar_wait_bounded(smem_u32(&sm.full[stage]), phase, abort, p.err_word, kWaitFull)) {
+      if (!mbar_wait_lazy(smem_u32(&sm.full[stage]), phase, abort, p.err_word, kWaitFull)) {
         ok = false;
         break;
       }
@@ -329,6 +318,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   } else {
     // ------------------------------------------- accumulator -> partial sums
     const int quarter = warp & 3;
+    grid_dependency_wait();
     split_load_cols<kGrad>(p, col, cols);
     split_load_row<kGrad>(p, m0 + t / wq, col, first);
     int got = 0;

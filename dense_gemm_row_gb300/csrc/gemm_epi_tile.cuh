@@ -10,7 +10,7 @@
 // A CTA pair (cta_group::2) owns a 256 x kBN tile; persistent, ten warps per CTA:
 //   warp 0      TMA producer: 128 rows of A and kBN / 2 columns of B per CTA and
 //               stage, 128 bytes of k (64 16-bit or 128 8-bit values)
-//   warp 1      one thread of the leader issues the pair's MMAs into one of two
+//   warp 1      the leader's issues the pair's MMAs into one of two
 //               accumulators, so a tile's epilogue overlaps the next main loop
 //   warps 2..9  epilogue: each owns 32 rows x kBN / 2 columns, in units of 64
 //               columns (one 128-byte row of 16-bit output per lane)
@@ -36,6 +36,7 @@
 
 #include "epi.cuh"
 #include "gemm_tc_kernel.cuh"
+#include "tc_issue.cuh"
 
 namespace dgr {
 namespace {
@@ -252,30 +253,34 @@ __device__ __forceinline__ void epi_produce(const CUtensorMap &tmA, const CUtens
     const int m0 = tm * Cf::kTileM + static_cast<int>(rank) * kBM;
     const int n0 = tn * kN + static_cast<int>(rank) * Cf::kBNLoad;
     for (int kb = 0; kb < KB; ++kb) {
-      if (!mbar_wait_bounded(smem_u32(&sm.empty[stage]), phase ^ 1u, abort, p.err_word,
-                             kWaitEmpty)) {
+      if (!mbar_wait_lazy(smem_u32(&sm.empty[stage]), phase ^ 1u, abort, p.err_word,
+                          kWaitEmpty)) {
         ok = false;
         break;
       }
-      const uint32_t full_bar = smem_u32(&sm.full[stage]);
-      if (rank == 0) mbar_arrive_expect_tx(full_bar, Cf::kTxBytes);
-      const uint32_t bar = mapa_shared(full_bar, 0);
-      const int k0 = kb * kBK;
-      if constexpr (!kAT) {
-        tma_load_3d_pair_hint(smem_u32(sm.a[stage]), &tmA, bar, k0, m0, 0, keep);
-      } else {
+      if (elect_one()) {
+        const uint32_t full_bar = smem_u32(&sm.full[stage]);
+        if (rank == 0) mbar_arrive_expect_tx(full_bar, Cf::kTxBytes);
+        const uint32_t bar = mapa_shared(full_bar, 0);
+        const int k0 = kb * kBK;
+        if constexpr (!kAT) {
+          tma_load_3d_pair_hint(smem_u32(sm.a[stage]), &tmA, bar, k0, m0, 0, keep);
+        } else {
 #pragma unroll
-        for (int j = 0; j < kBM / 64; ++j)
-          tma_load_3d_pair_hint(smem_u32(sm.a[stage] + j * kMNBoxBytes), &tmA, bar, m0 + 64 * j,
-                                k0, 0, keep);
-      }
-      if constexpr (!kBT) {
+          for (int j = 0; j < kBM / 64; ++j)
+            tma_load_3d_pair_hint(smem_u32(sm.a[stage] + j * kMNBoxBytes), &tmA, bar, m0 + 64 * j,
+                                  k0, 0, keep);
+        }
+        if constexpr (!kBT) {
 #pragma unroll
-        for (int j = 0; j < Cf::kBNLoad / 64; ++j)
-          tma_load_3d_pair(smem_u32(sm.b[stage] + j * kMNBoxBytes), &tmB, bar, n0 + 64 * j, k0, 0);
-      } else {
-        tma_load_3d_pair(smem_u32(sm.b[stage]), &tmB, bar, k0, n0, 0);
+          for (int j = 0; j < Cf::kBNLoad / 64; ++j)
+            tma_load_3d_pair(smem_u32(sm.b[stage] + j * kMNBoxBytes), &tmB, bar, n0 + 64 * j, k0,
+                             0);
+        } else {
+          tma_load_3d_pair(smem_u32(sm.b[stage]), &tmB, bar, k0, n0, 0);
+        }
       }
+      __syncwarp();
       issued |= 1u << stage;
       issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
       if (++stage == Cf::kStages) {
@@ -314,40 +319,44 @@ __device__ __forceinline__ void epi_multiply(const EpiArgs &p, EpiSmem<kN> &sm,
   bool ok = true, any = false;
   for (int t = unit; ok && t < p.tiles; t += units, ++n) {
     const uint32_t buf = n & 1u, use = (n >> 1) & 1u;
-    if (!mbar_wait_bounded_cluster(smem_u32(&sm.tmem_empty[buf]), use ^ 1u, abort, p.err_word,
-                                   kWaitTmemEmpty))
+    if (!mbar_wait_lazy<true>(smem_u32(&sm.tmem_empty[buf]), use ^ 1u, abort, p.err_word,
+                              kWaitTmemEmpty))
       break;
     tc_fence_after_sync();
     const uint32_t d_tmem = tmem_base + buf * kN;
     for (int kb = 0; kb < KB; ++kb) {
-      if (!mbar_wait_bounded(smem_u32(&sm.full[stage]), phase, abort, p.err_word, kWaitFull)) {
+      if (!mbar_wait_lazy(smem_u32(&sm.full[stage]), phase, abort, p.err_word, kWaitFull)) {
         ok = false;
         break;
       }
       tc_fence_after_sync();
       const uint64_t ad = adesc0 + stage * kAStage, bd = bdesc0 + stage * kBStage;
+      if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint32_t acc = kk > 0 || kb > 0 ? 1u : 0u;
-        if constexpr (kE4m3) {
-          tc_mma_f8_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, p.idesc, acc);
-        } else {
-          tc_mma_f16_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, p.idesc, acc);
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint32_t acc = kk > 0 || kb > 0 ? 1u : 0u;
+          if constexpr (kE4m3) {
+            tc_mma_f8_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, p.idesc, acc);
+          } else {
+            tc_mma_f16_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, p.idesc, acc);
+          }
         }
+        tc_commit_pair_mc(smem_u32(&sm.empty[stage]), 0x3);
+        if (kb == KB - 1) tc_commit_pair_mc(smem_u32(&sm.tmem_full[buf]), 0x3);
       }
+      __syncwarp();
       any = true;
-      tc_commit_pair_mc(smem_u32(&sm.empty[stage]), 0x3);
       if (++stage == Cf::kStages) {
         stage = 0;
         phase ^= 1u;
       }
     }
-    if (!ok) break;
-    tc_commit_pair_mc(smem_u32(&sm.tmem_full[buf]), 0x3);
   }
-  // Never leave with an MMA still reading shared memory or writing TMEM.
+  // Never leave with an MMA still reading shared memory or writing TMEM. (The
+  // same lane is elected each time, so its commit covers them all.)
   if (any) {
-    tc_commit_pair_mc(smem_u32(&sm.drain), 0x1);
+    if (elect_one()) tc_commit_pair_mc(smem_u32(&sm.drain), 0x1);
+    __syncwarp();
     drain_wait(smem_u32(&sm.drain), 0, p.err_word);
   }
 }
@@ -483,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Same offset in both CTAs of the pair, as the pair MMA needs.
   EpiSmem<kN> &sm = *reinterpret_cast<EpiSmem<kN> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int unit = static_cast<int>(blockIdx.x >> 1), units = static_cast<int>(gridDim.x >> 1);
 
@@ -517,24 +526,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_launch_dependents();
 
   if (warp == 0) {
-    if (lane == 0) {
-      if constexpr (kE4m3) {
-        epi_produce<true, kN, false, true>(tmA, tmB, p, sm, rank, unit, units);
-      } else if (p.a_t) {
-        if (p.b_t) {
-          epi_produce<false, kN, true, true>(tmA, tmB, p, sm, rank, unit, units);
-        } else {
-          epi_produce<false, kN, true, false>(tmA, tmB, p, sm, rank, unit, units);
-        }
-      } else if (p.b_t) {
-        epi_produce<false, kN, false, true>(tmA, tmB, p, sm, rank, unit, units);
+    if constexpr (kE4m3) {
+      epi_produce<true, kN, false, true>(tmA, tmB, p, sm, rank, unit, units);
+    } else if (p.a_t) {
+      if (p.b_t) {
+        epi_produce<false, kN, true, true>(tmA, tmB, p, sm, rank, unit, units);
       } else {
-        epi_produce<false, kN, false, false>(tmA, tmB, p, sm, rank, unit, units);
+        epi_produce<false, kN, true, false>(tmA, tmB, p, sm, rank, unit, units);
       }
+    } else if (p.b_t) {
+      epi_produce<false, kN, false, true>(tmA, tmB, p, sm, rank, unit, units);
+    } else {
+      epi_produce<false, kN, false, false>(tmA, tmB, p, sm, rank, unit, units);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       if constexpr (kE4m3) {
         epi_multiply<true, kN, false, true>(p, sm, tmem_base, unit, units);
       } else if (p.a_t) {
