@@ -132,16 +132,24 @@ __device__ __forceinline__ void load_block(const uint16_t *p, int64_t ld, bool v
       w[4 * u] = v.x, w[4 * u + 1] = v.y, w[4 * u + 2] = v.z, w[4 * u + 3] = v.w;
     }
   } else {
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r) {
-      const uint16_t *q = p + (row0 + r) * ld + col;
+    // 16 rows' loads (two per lane) are in flight together.
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = lane + 32 * h;
-        const uint16_t v = row0 + r < M && col + j < N ? q[j] : 0;
-        asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(stage_elem(stage, r, j)), "h"(v)
-                     : "memory");
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+      uint16_t v[16][2];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint16_t *q = p + (row0 + r0 + i) * ld + col + lane;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[i][h] = row0 + r0 + i < M && col + lane + 32 * h < N ? q[32 * h] : 0;
       }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(stage_elem(stage, r0 + i, lane + 32 * h)),
+                       "h"(v[i][h])
+                       : "memory");
     }
     __syncwarp();
 #pragma unroll
@@ -178,17 +186,15 @@ __device__ __forceinline__ void store_block(const void *tm, bool tma, uint16_t *
     }
   } else {
     __syncwarp();
-#pragma unroll 4
+#pragma unroll 8
     for (int r = 0; r < 32; ++r) {
-      if (row0 + r >= M) break;
-      uint16_t *q = p + (row0 + r) * ld + col;
+      uint16_t *q = p + (row0 + r) * ld + col + lane;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int j = lane + 32 * h;
         uint16_t v;
-        asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(stage_elem(stage, r, j))
+        asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(stage_elem(stage, r, lane + 32 * h))
                      : "memory");
-        if (col + j < N) q[j] = v;
+        if (row0 + r < M && col + lane + 32 * h < N) q[32 * h] = v;
       }
     }
     __syncwarp();
