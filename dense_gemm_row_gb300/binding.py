@@ -59,7 +59,6 @@ EXPORTED = ("gemm_f32", "gemm_bf16", "gemm_f16", "gemm_s8", "gemm_u8", "gemm_f16
             "gemm_rms_norm_f16_e4m3", "gemm_rms_norm_grad_bf16", "gemm_rms_norm_grad_f16")
 
 OP_N, OP_T = 0, 1  # gemm_op_t
-ACTS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}  # gemm_act_t
 
 
 class GemmError(RuntimeError):
@@ -356,97 +355,26 @@ def gemm_batched(A, B, C, alpha=1.0, beta=0.0, trans_a=False, trans_b=False, str
 
 # ------------------------------------------------------ linear-layer operators
 
-def _torch():
-    import torch
-    return torch
+_layers = None
 
 
-def _current(stream, device) -> int:
-    """The raw stream of a call on CUDA device `device` (an index); torch's
-    current stream of that device by default."""
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(device)
-    return stream if isinstance(stream, int) else int(stream.cuda_stream)
-
-
-def _device(t, name) -> int:
-    """Index of the CUDA device `t` is on; it has to be the current device,
-    where the library enqueues its work."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != _torch().cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, not on the current CUDA device")
-    return dev
-
-
-def _matrix(t, name, shape, dtype, dev):
-    """(address, row stride) of a matrix of that shape, dtype and device with
-    unit column stride; (None, 0) for None."""
-    if t is None:
-        return None, 0
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {shape[0]} x {shape[1]}, not {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}")
-    ld, step = t.stride()
-    if step != 1 and shape[1] > 1 and shape[0] > 0:
-        raise ValueError(f"{name} needs unit column stride (row-major)")
-    if shape[0] <= 1:
-        ld = max(shape[1], 1)  # one row: the stride has no meaning
-    elif ld < shape[1]:
-        raise ValueError(f"{name}: rows overlap (row stride {ld}, {shape[1]} columns)")
-    return t.data_ptr(), ld
-
-
-def _operand(t, name, shape, dtype, dev, unit):
-    """_matrix for a tensor-core operand: a single row's stride counts as the
-    next multiple of `unit` (the layout rule is about addresses that are read)."""
-    p, ld = _matrix(t, name, shape, dtype, dev)
-    return p, (-(-ld // unit) * unit if shape[0] <= 1 else ld)
-
-
-def _vector(t, name, n, dtype, dev):
-    """Address of a contiguous vector of n values; None for None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous vector of {n} values")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _act(act) -> int:
-    try:
-        return ACTS[act]
-    except KeyError:
-        raise ValueError(f"act must be one of {[a for a in ACTS if a]}, not {act!r}") from None
-
-
-def _fmt(dtype, what) -> str:
-    torch = _torch()
-    if dtype is torch.bfloat16:
-        return "bf16"
-    if dtype is torch.float16:
-        return "f16"
-    raise TypeError(f"{what} must be bfloat16 or float16, not {dtype}")
-
-
-def _product_shape(A, B, trans_a, trans_b, what):
-    if A.dim() != 2 or B.dim() != 2:
-        raise ValueError(f"{what}: A and B must be 2-D")
-    if A.dtype is not B.dtype:
-        raise TypeError(f"{what}: A and B must share a dtype")
-    k, m = A.shape if trans_a else A.shape[::-1]
-    n, k2 = B.shape if trans_b else B.shape[::-1]
-    if k != k2:
-        raise ValueError(f"{what}: shapes do not chain")
-    return m, n, k
+def _load_layers():
+    """The marshalling module of the linear-layer operators, bound to the library.
+    Loaded by the first call: it links against torch, which the raw entry points
+    above do not need."""
+    global _layers
+    import importlib
+    if not os.path.exists(os.path.join(_PKG, "_layers.so")):
+        raise ImportError(
+            "dense_gemm_row_gb300/_layers.so is missing: build it with "
+            "`python -m dense_gemm_row_gb300.build` (or __graft_entry__.build()).")
+    import torch  # noqa: F401  (the module links against torch's libraries)
+    mod = importlib.import_module("dense_gemm_row_gb300._layers")
+    for name in EXPORTED:
+        if "_epi" in name or "dact" in name or "act_grad" in name or "rms_norm" in name:
+            mod.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
+    _layers = mod
+    return mod
 
 
 def gemm_epilogue(A, B, D, *, alpha=1.0, bias=None, act=None, residual=None, preact=None,
@@ -461,37 +389,10 @@ def gemm_epilogue(A, B, D, *, alpha=1.0, bias=None, act=None, residual=None, pre
     itself) and act ("relu", "gelu", "gelu_tanh", "silu" or None) may be left
     out; preact (M x N), when given, receives Z for gemm_dact or act_grad.
     A and B start on 16-byte boundaries with row strides in whole 16-byte units."""
-    torch = _torch()
-    m, n, k = _product_shape(A, B, trans_a, trans_b, "gemm_epilogue")
-    dev = _device(A, "A")
-    e4m3 = A.dtype is torch.float8_e4m3fn
-    dtype = D.dtype if e4m3 else A.dtype
-    fmt = _fmt(dtype, "D" if e4m3 else "A")
-    unit = 16 if e4m3 else 8
-    pa, lda = _operand(A, "A", tuple(A.shape), A.dtype, dev, unit)
-    pb, ldb = _operand(B, "B", tuple(B.shape), A.dtype, dev, unit)
-    pd, ldd = _matrix(D, "D", (m, n), dtype, dev)
-    pr, ldr = _matrix(residual, "residual", (m, n), dtype, dev)
-    pz, ldz = _matrix(preact, "preact", (m, n), dtype, dev)
-    pbias = _vector(bias, "bias", n, dtype, dev)
-    a = _act(act)
-    s = _current(stream, dev)
-    if e4m3:
-        if trans_a or not trans_b:
-            raise ValueError("gemm_epilogue: float8_e4m3fn takes A as M x K and B as N x K "
-                             "(trans_b=True)")
-        sa = _vector(scale_a, "scale_a", m, torch.float32, dev)
-        sb = _vector(scale_b, "scale_b", n, torch.float32, dev)
-        name = "gemm_e4m3_bf16_epi" if fmt == "bf16" else "gemm_e4m3_f16_epi"
-        st = getattr(lib, name)(m, n, k, alpha, pa, lda, sa, pb, ldb, sb, a, pbias, pr, ldr, pz,
-                                ldz, pd, ldd, s)
-    else:
-        if scale_a is not None or scale_b is not None:
-            raise ValueError("gemm_epilogue: scales go with float8_e4m3fn operands")
-        name = "gemm_bf16_epi" if fmt == "bf16" else "gemm_f16_epi"
-        st = getattr(lib, name)(trans_a, trans_b, m, n, k, alpha, pa, lda, pb, ldb, a, pbias, pr,
-                                ldr, pz, ldz, pd, ldd, s)
-    _check(st, name)
+    st = (_layers or _load_layers()).gemm_epilogue(A, B, D, alpha, bias, act, residual, preact,
+                                                   trans_a, trans_b, scale_a, scale_b, stream)
+    if st:
+        _check(st, "gemm_epilogue")
     return D
 
 
@@ -503,17 +404,10 @@ def gemm_dact(A, B, Z, dZ, *, act=None, alpha=1.0, dbias=None, trans_a=False, tr
     layer, B its weights) with the activation's derivative at the stored
     pre-activation Z (M x N; None without an activation) in its epilogue. dbias
     (N values of the same dtype) may be None. dZ may be Z itself."""
-    m, n, k = _product_shape(A, B, trans_a, trans_b, "gemm_dact")
-    dev = _device(A, "A")
-    dtype = A.dtype
-    name = "gemm_bf16_dact" if _fmt(dtype, "A") == "bf16" else "gemm_f16_dact"
-    pa, lda = _operand(A, "A", tuple(A.shape), dtype, dev, 8)
-    pb, ldb = _operand(B, "B", tuple(B.shape), dtype, dev, 8)
-    pz, ldz = _matrix(Z, "Z", (m, n), dtype, dev)
-    pd, ldd = _matrix(dZ, "dZ", (m, n), dtype, dev)
-    pbias = _vector(dbias, "dbias", n, dtype, dev)
-    _check(getattr(lib, name)(trans_a, trans_b, m, n, k, alpha, pa, lda, pb, ldb, _act(act), pz,
-                              ldz, pd, ldd, pbias, _current(stream, dev)), name)
+    st = (_layers or _load_layers()).gemm_dact(A, B, Z, dZ, act, alpha, dbias, trans_a, trans_b,
+                                               stream)
+    if st:
+        _check(st, "gemm_dact")
     return dZ
 
 
@@ -523,18 +417,9 @@ def act_grad(dD, Z, dZ, *, act=None, dbias=None, stream=None):
     gemm_dact for an output gradient that is already in memory. Without an
     activation Z may be None, and dZ too when only dbias is wanted. dZ may be
     dD or Z itself."""
-    if dD.dim() != 2:
-        raise ValueError("act_grad: dD must be 2-D")
-    m, n = shape = tuple(dD.shape)
-    dev = _device(dD, "dD")
-    dtype = dD.dtype
-    name = "gemm_act_grad_bf16" if _fmt(dtype, "dD") == "bf16" else "gemm_act_grad_f16"
-    pd, ldd = _matrix(dD, "dD", shape, dtype, dev)
-    pz, ldz = _matrix(Z, "Z", shape, dtype, dev)
-    po, ldo = _matrix(dZ, "dZ", shape, dtype, dev)
-    pbias = _vector(dbias, "dbias", n, dtype, dev)
-    _check(getattr(lib, name)(m, n, _act(act), pd, ldd, pz, ldz, po, ldo, pbias,
-                              _current(stream, dev)), name)
+    st = (_layers or _load_layers()).act_grad(dD, Z, dZ, act, dbias, stream)
+    if st:
+        _check(st, "act_grad")
     return dZ
 
 
@@ -547,33 +432,9 @@ def rms_norm(X, Y, *, weight=None, residual=None, h=None, scale=None, rstd=None,
     one scale per row written to scale (float32, required then): Y stands for
     Y * scale[:, None], which gemm_epilogue takes as A and scale_a. rstd
     (float32, rows values), when given, receives 1 / rms for rms_norm_grad."""
-    torch = _torch()
-    if X.dim() != 2:
-        raise ValueError("rms_norm: X must be 2-D")
-    m, n = shape = tuple(X.shape)
-    dev = _device(X, "X")
-    dtype = X.dtype
-    fmt = _fmt(dtype, "X")
-    e4m3 = Y.dtype is torch.float8_e4m3fn
-    px, ldx = _matrix(X, "X", shape, dtype, dev)
-    pr, ldr = _matrix(residual, "residual", shape, dtype, dev)
-    ph, ldh = _matrix(h, "h", shape, dtype, dev)
-    py, ldy = _matrix(Y, "Y", shape, torch.float8_e4m3fn if e4m3 else dtype, dev)
-    pw = _vector(weight, "weight", n, dtype, dev)
-    ps = _vector(scale, "scale", m, torch.float32, dev)
-    pq = _vector(rstd, "rstd", m, torch.float32, dev)
-    s = _current(stream, dev)
-    if e4m3:
-        if scale is None:
-            raise ValueError("rms_norm: a float8_e4m3fn Y needs scale")
-        name = "gemm_rms_norm_bf16_e4m3" if fmt == "bf16" else "gemm_rms_norm_f16_e4m3"
-        st = getattr(lib, name)(m, n, eps, px, ldx, pr, ldr, pw, ph, ldh, py, ldy, ps, pq, s)
-    else:
-        if scale is not None:
-            raise ValueError("rms_norm: scale goes with a float8_e4m3fn Y")
-        name = "gemm_rms_norm_bf16" if fmt == "bf16" else "gemm_rms_norm_f16"
-        st = getattr(lib, name)(m, n, eps, px, ldx, pr, ldr, pw, ph, ldh, py, ldy, pq, s)
-    _check(st, name)
+    st = (_layers or _load_layers()).rms_norm(X, Y, weight, residual, h, scale, rstd, eps, stream)
+    if st:
+        _check(st, "rms_norm")
     return Y
 
 
@@ -582,21 +443,7 @@ def rms_norm_grad(dY, H, rstd, dX, *, weight=None, dh=None, dweight=None, stream
     the gradient that reaches H past the norm; dweight (cols values) receives
     the weight's gradient. H and rstd are those of the forward call. dX may be
     dY or dh itself. Returns dX."""
-    torch = _torch()
-    if dY.dim() != 2:
-        raise ValueError("rms_norm_grad: dY must be 2-D")
-    m, n = shape = tuple(dY.shape)
-    dev = _device(dY, "dY")
-    dtype = dY.dtype
-    fmt = _fmt(dtype, "dY")
-    name = "gemm_rms_norm_grad_bf16" if fmt == "bf16" else "gemm_rms_norm_grad_f16"
-    py, ldy = _matrix(dY, "dY", shape, dtype, dev)
-    ph, ldh = _matrix(H, "H", shape, dtype, dev)
-    pb, ldb = _matrix(dh, "dh", shape, dtype, dev)
-    px, ldx = _matrix(dX, "dX", shape, dtype, dev)
-    pw = _vector(weight, "weight", n, dtype, dev)
-    pg = _vector(dweight, "dweight", n, dtype, dev)
-    pq = _vector(rstd, "rstd", m, torch.float32, dev)
-    _check(getattr(lib, name)(m, n, py, ldy, ph, ldh, pq, pw, pb, ldb, px, ldx, pg,
-                              _current(stream, dev)), name)
+    st = (_layers or _load_layers()).rms_norm_grad(dY, H, rstd, dX, weight, dh, dweight, stream)
+    if st:
+        _check(st, "rms_norm_grad")
     return dX

@@ -3,7 +3,9 @@
 Each translation unit is compiled in parallel to an object file under
 ``_build/``, then linked into a shared library with the CUDA runtime linked
 statically, so the library needs no libcudart at load time and resolves the
-driver only when a GPU call is made.
+driver only when a GPU call is made. Beside it, csrc/py_layers.cpp becomes the
+Python module ``_layers`` (argument marshalling of the linear-layer operators;
+needs the headers of Python and torch).
 
     python -m dense_gemm_row_gb300.build [--force] [--ptxas-verbose]
 """
@@ -23,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB_NAME = "libdense_gemm_row.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
+LAYERS_PATH = os.path.join(PKG, "_layers.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -45,6 +48,23 @@ def _deps():
     hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     hdrs.append(os.path.join(INCLUDE, "dense_gemm_row.h"))
     return hdrs
+
+
+def _layers_command(out: str):
+    """g++ command that builds the _layers module against the running Python and torch."""
+    import importlib.util
+    import sysconfig
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc = os.path.join(torch_dir, "include")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    return ["g++", "-O2", "-std=c++20", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
+            "-I", INCLUDE, "-isystem", inc,
+            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"],
+            "-isystem", os.path.join(cuda, "include"),
+            os.path.join(CSRC, "py_layers.cpp"), "-o", out,
+            "-L", os.path.join(torch_dir, "lib"), "-Wl,-rpath," + os.path.join(torch_dir, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def _stale(target: str, inputs) -> bool:
@@ -70,15 +90,23 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = False)
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
+    layers_tmp = LAYERS_PATH + f".tmp{os.getpid()}"
+    layers = force or _stale(LAYERS_PATH, [os.path.join(CSRC, "py_layers.cpp"),
+                                           os.path.join(INCLUDE, "dense_gemm_row.h")])
+    if layers:
+        jobs.insert(0, _layers_command(layers_tmp))
+
     def run(cmd):
         return cmd, subprocess.run(cmd, capture_output=True, text=True)
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
         for cmd, res in ex.map(run, jobs):
             if res.returncode != 0:
-                raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stderr)
+                raise RuntimeError("compiling failed:\n" + " ".join(cmd) + "\n" + res.stderr)
             if (ptxas_verbose or res.stderr.strip()) and not quiet:
                 sys.stderr.write(res.stderr)
+    if layers:
+        os.replace(layers_tmp, LAYERS_PATH)
     if force or jobs or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
