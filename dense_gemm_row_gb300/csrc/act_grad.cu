@@ -89,10 +89,11 @@ __device__ __forceinline__ void act_grad_body(int M, int N, const uint16_t *dD, 
         float a, b;
         unpack16<kBf16>(dw[e], a, b);
         if constexpr (kAct != kActNone) {
-          float za, zb;
+          float za, zb, sa, sb;
           unpack16<kBf16>(zw[e], za, zb);
-          a *= act_slope<kAct>(za);
-          b *= act_slope<kAct>(zb);
+          act_slope2<kAct>(za, zb, sa, sb);
+          a *= sa;
+          b *= sb;
         }
         sum[2 * e] += a;
         sum[2 * e + 1] += b;

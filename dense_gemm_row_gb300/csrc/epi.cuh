@@ -85,18 +85,15 @@ constexpr float kGeluA = 0.044715f;
 constexpr float kInvSqrt2 = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
-// The normal distribution function Phi(z), with e = exp(-z^2 / 2) returned for
-// its density. Phi(-x sqrt 2) = erfc(x) / 2, and erfc(x) = exp(-x^2) t P(t)
+// The normal distribution function Phi(z). Phi(-x sqrt 2) = erfc(x) / 2, and erfc(x) = exp(-x^2) t P(t)
 // with t = 1 / (1 + x / 2): P is the degree-6 polynomial that minimises the
 // largest relative error over 0 <= x <= 9.3 (iteratively reweighted least
 // squares against a double-precision erfc; 1.5e-6 with fp32 coefficients).
-// The relative error holds in the lower tail too, where 1 + erf cancels, and
-// the exponential is the one the density needs: two MUFU operations in all,
-// so an element-wise pass stays bound by memory.
-__device__ __forceinline__ float normal_cdf(float z, float &e) {
+// The relative error holds in the lower tail too, where 1 + erf cancels.
+__device__ __forceinline__ float normal_cdf(float z) {
   const float x = fabsf(z) * kInvSqrt2;
   const float t = rcp_fast(fmaf(0.5f, x, 1.f));
-  e = exp_fast(-0.5f * z * z);
+  const float e = exp_fast(-0.5f * z * z);
   float p = 0.08912812918424606f;
   p = fmaf(p, t, -0.35999614000320435f);
   p = fmaf(p, t, 0.39379453659057617f);
@@ -113,8 +110,7 @@ __device__ __forceinline__ float act_value(float z) {
   if constexpr (kAct == kActRelu) {
     return z < 0.f ? 0.f : z;
   } else if constexpr (kAct == kActGelu) {
-    float e;
-    return z * normal_cdf(z, e);
+    return z * normal_cdf(z);
   } else if constexpr (kAct == kActGeluTanh) {
     return z * logistic(2.f * kGeluC * (z + kGeluA * z * z * z));
   } else if constexpr (kAct == kActSilu) {
@@ -125,24 +121,103 @@ __device__ __forceinline__ float act_value(float z) {
 }
 
 template <int kAct>
+__device__ __forceinline__ void act_slope2(float z0, float z1, float &s0, float &s1);
+
+// The derivative. gelu: Phi(z) + z phi(z); gelu_tanh: s + z s (1 - s) 2u', where
+// for |z| > 100 s (1 - s) is 0 and a bound on z^2 keeps a finite z from making it
+// 0 * inf; silu: s + z s (1 - s).
+template <int kAct>
 __device__ __forceinline__ float act_slope(float z) {
   if constexpr (kAct == kActRelu) {
     return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);  // NaN stays NaN
-  } else if constexpr (kAct == kActGelu) {
-    float e;  // Phi(z) + z phi(z)
-    const float cdf = normal_cdf(z, e);
-    return fmaf(z * kInvSqrt2Pi, e, cdf);
-  } else if constexpr (kAct == kActGeluTanh) {
-    // s + z s (1 - s) 2u'. For |z| > 100 s (1 - s) is 0; the bound on z^2
-    // keeps a finite z from making it 0 * inf.
-    const float zz = fminf(z * z, 1e4f);
-    const float s = logistic(2.f * kGeluC * (z + kGeluA * z * z * z));
-    return fmaf(z * s * (1.f - s), 2.f * kGeluC * fmaf(3.f * kGeluA, zz, 1.f), s);
-  } else if constexpr (kAct == kActSilu) {
-    const float s = logistic(z);
-    return fmaf(z * s, 1.f - s, s);
+  } else if constexpr (kAct == kActGelu || kAct == kActGeluTanh || kAct == kActSilu) {
+    float s0, s1;
+    act_slope2<kAct>(z, z, s0, s1);
+    return s0;
   } else {
     return 1.f;
+  }
+}
+
+// Two fp32 values in one register pair, and the packed operations on them: one
+// instruction for two values, which is what keeps the slopes below the cost of
+// the memory traffic in the element-wise gradient.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void split(F2 p, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+// 2^x and 1 / x of both values (exp_fast and rcp_fast's instructions).
+__device__ __forceinline__ F2 exp2_fast2(F2 x) {
+  float a, b;
+  split(x, a, b);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return f2(a, b);
+}
+__device__ __forceinline__ F2 rcp_fast2(F2 x) {
+  float a, b;
+  split(x, a, b);
+  return f2(rcp_fast(a), rcp_fast(b));
+}
+
+// act_slope of two values. gelu takes Phi as 1/2 + sign(z) (1/2 - erfc / 2): the
+// slope needs it to an absolute 2^-24 only.
+template <int kAct>
+__device__ __forceinline__ void act_slope2(float z0, float z1, float &s0, float &s1) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const F2 z = f2(z0, z1);
+  if constexpr (kAct == kActGelu) {
+    const F2 e = exp2_fast2(mul2(mul2(z, z), f2(-0.5f * kLog2e)));
+    const F2 t = rcp_fast2(fma2(f2(fabsf(z0), fabsf(z1)), f2(0.5f * kInvSqrt2), f2(1.f)));
+    F2 p = f2(0.5f * 0.08912812918424606f);  // normal_cdf's polynomial, halved
+    p = fma2(p, t, f2(0.5f * -0.35999614000320435f));
+    p = fma2(p, t, f2(0.5f * 0.39379453659057617f));
+    p = fma2(p, t, f2(0.5f * 0.03464719280600548f));
+    p = fma2(p, t, f2(0.5f * 0.28272417187690735f));
+    p = fma2(p, t, f2(0.5f * 0.2773527503013611f));
+    p = fma2(p, t, f2(0.5f * 0.2823481559753418f));
+    float a, b;
+    split(fma2(mul2(e, t), mul2(p, f2(-1.f)), f2(0.5f)), a, b);
+    const F2 cdf = add2(f2(copysignf(a, z0), copysignf(b, z1)), f2(0.5f));
+    split(fma2(mul2(z, f2(kInvSqrt2Pi)), e, cdf), s0, s1);
+  } else if constexpr (kAct == kActGeluTanh) {
+    const F2 zz = mul2(z, z);
+    const F2 arg = mul2(z, fma2(zz, f2(-2.f * kGeluC * kLog2e * kGeluA), f2(-2.f * kGeluC * kLog2e)));
+    const F2 s = rcp_fast2(add2(exp2_fast2(arg), f2(1.f)));
+    float a, b;
+    split(zz, a, b);
+    const F2 poly = fma2(f2(fminf(a, 1e4f), fminf(b, 1e4f)), f2(6.f * kGeluC * kGeluA),
+                         f2(2.f * kGeluC));
+    split(fma2(mul2(mul2(z, s), fma2(s, f2(-1.f), f2(1.f))), poly, s), s0, s1);
+  } else if constexpr (kAct == kActSilu) {
+    const F2 s = rcp_fast2(add2(exp2_fast2(mul2(z, f2(-kLog2e))), f2(1.f)));
+    split(fma2(mul2(z, s), fma2(s, f2(-1.f), f2(1.f)), s), s0, s1);
+  } else {
+    s0 = act_slope<kAct>(z0);
+    s1 = act_slope<kAct>(z1);
   }
 }
 

@@ -168,9 +168,12 @@ __device__ __forceinline__ void split_finish(const SplitArgs &p, uint32_t red, i
         for (int e = 0; e < 4; ++e) v[e] += r[e];
       }
     } else {
+      float slope[4];
+      act_slope2<kAct>(r[0], r[1], slope[0], slope[1]);
+      act_slope2<kAct>(r[2], r[3], slope[2], slope[3]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] *= sa * act_slope<kAct>(r[e]);
+        v[e] *= sa * slope[e];
         sum[e] += v[e];
       }
     }
