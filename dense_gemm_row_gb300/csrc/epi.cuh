@@ -120,25 +120,6 @@ __device__ __forceinline__ float act_value(float z) {
   }
 }
 
-template <int kAct>
-__device__ __forceinline__ void act_slope2(float z0, float z1, float &s0, float &s1);
-
-// The derivative. gelu: Phi(z) + z phi(z); gelu_tanh: s + z s (1 - s) 2u', where
-// for |z| > 100 s (1 - s) is 0 and a bound on z^2 keeps a finite z from making it
-// 0 * inf; silu: s + z s (1 - s).
-template <int kAct>
-__device__ __forceinline__ float act_slope(float z) {
-  if constexpr (kAct == kActRelu) {
-    return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);  // NaN stays NaN
-  } else if constexpr (kAct == kActGelu || kAct == kActGeluTanh || kAct == kActSilu) {
-    float s0, s1;
-    act_slope2<kAct>(z, z, s0, s1);
-    return s0;
-  } else {
-    return 1.f;
-  }
-}
-
 // Two fp32 values in one register pair, and the packed operations on them: one
 // instruction for two values, which is what keeps the slopes below the cost of
 // the memory traffic in the element-wise gradient.
@@ -183,26 +164,30 @@ __device__ __forceinline__ F2 rcp_fast2(F2 x) {
   return f2(rcp_fast(a), rcp_fast(b));
 }
 
-// act_slope of two values. gelu takes Phi as 1/2 + sign(z) (1/2 - erfc / 2): the
-// slope needs it to an absolute 2^-24 only.
+// The derivatives at two values. gelu: Phi(z) + z phi(z), with Phi as 1/2 +
+// sign(z) (1/2 - erfc / 2), as the slope needs it to an absolute 2^-24 only;
+// gelu_tanh: s + z s (1 - s) 2u', where for |z| > 100 s (1 - s) is 0 and a bound
+// on z^2 keeps a finite z from making it 0 * inf; silu: s + z s (1 - s).
 template <int kAct>
-__device__ __forceinline__ void act_slope2(float z0, float z1, float &s0, float &s1) {
+__device__ __forceinline__ F2 act_slope2(float z0, float z1) {
   constexpr float kLog2e = 1.4426950408889634f;
   const F2 z = f2(z0, z1);
-  if constexpr (kAct == kActGelu) {
+  if constexpr (kAct == kActRelu) {  // NaN stays NaN
+    return f2(z0 > 0.f ? 1.f : (z0 <= 0.f ? 0.f : z0), z1 > 0.f ? 1.f : (z1 <= 0.f ? 0.f : z1));
+  } else if constexpr (kAct == kActGelu) {
     const F2 e = exp2_fast2(mul2(mul2(z, z), f2(-0.5f * kLog2e)));
     const F2 t = rcp_fast2(fma2(f2(fabsf(z0), fabsf(z1)), f2(0.5f * kInvSqrt2), f2(1.f)));
-    F2 p = f2(0.5f * 0.08912812918424606f);  // normal_cdf's polynomial, halved
-    p = fma2(p, t, f2(0.5f * -0.35999614000320435f));
-    p = fma2(p, t, f2(0.5f * 0.39379453659057617f));
-    p = fma2(p, t, f2(0.5f * 0.03464719280600548f));
-    p = fma2(p, t, f2(0.5f * 0.28272417187690735f));
-    p = fma2(p, t, f2(0.5f * 0.2773527503013611f));
-    p = fma2(p, t, f2(0.5f * 0.2823481559753418f));
+    F2 p = f2(-0.5f * 0.08912812918424606f);  // normal_cdf's polynomial, times -1/2
+    p = fma2(p, t, f2(-0.5f * -0.35999614000320435f));
+    p = fma2(p, t, f2(-0.5f * 0.39379453659057617f));
+    p = fma2(p, t, f2(-0.5f * 0.03464719280600548f));
+    p = fma2(p, t, f2(-0.5f * 0.28272417187690735f));
+    p = fma2(p, t, f2(-0.5f * 0.2773527503013611f));
+    p = fma2(p, t, f2(-0.5f * 0.2823481559753418f));
     float a, b;
-    split(fma2(mul2(e, t), mul2(p, f2(-1.f)), f2(0.5f)), a, b);
+    split(fma2(mul2(e, t), p, f2(0.5f)), a, b);
     const F2 cdf = add2(f2(copysignf(a, z0), copysignf(b, z1)), f2(0.5f));
-    split(fma2(mul2(z, f2(kInvSqrt2Pi)), e, cdf), s0, s1);
+    return fma2(mul2(z, f2(kInvSqrt2Pi)), e, cdf);
   } else if constexpr (kAct == kActGeluTanh) {
     const F2 zz = mul2(z, z);
     const F2 arg = mul2(z, fma2(zz, f2(-2.f * kGeluC * kLog2e * kGeluA), f2(-2.f * kGeluC * kLog2e)));
@@ -211,13 +196,12 @@ __device__ __forceinline__ void act_slope2(float z0, float z1, float &s0, float 
     split(zz, a, b);
     const F2 poly = fma2(f2(fminf(a, 1e4f), fminf(b, 1e4f)), f2(6.f * kGeluC * kGeluA),
                          f2(2.f * kGeluC));
-    split(fma2(mul2(mul2(z, s), fma2(s, f2(-1.f), f2(1.f))), poly, s), s0, s1);
+    return fma2(mul2(mul2(z, s), fma2(s, f2(-1.f), f2(1.f))), poly, s);
   } else if constexpr (kAct == kActSilu) {
     const F2 s = rcp_fast2(add2(exp2_fast2(mul2(z, f2(-kLog2e))), f2(1.f)));
-    split(fma2(mul2(z, s), fma2(s, f2(-1.f), f2(1.f)), s), s0, s1);
+    return fma2(mul2(z, s), fma2(s, f2(-1.f), f2(1.f)), s);
   } else {
-    s0 = act_slope<kAct>(z0);
-    s1 = act_slope<kAct>(z1);
+    return f2(1.f);
   }
 }
 

@@ -168,14 +168,12 @@ __device__ __forceinline__ void split_finish(const SplitArgs &p, uint32_t red, i
         for (int e = 0; e < 4; ++e) v[e] += r[e];
       }
     } else {
-      float slope[4];
-      act_slope2<kAct>(r[0], r[1], slope[0], slope[1]);
-      act_slope2<kAct>(r[2], r[3], slope[2], slope[3]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] *= sa * slope[e];
-        sum[e] += v[e];
-      }
+      for (int e = 0; e < 4; e += 2)
+        split(mul2(mul2(f2(v[e], v[e + 1]), f2(sa)), act_slope2<kAct>(r[e], r[e + 1])), v[e],
+              v[e + 1]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += v[e];
     }
     store4(p.c.D + row * p.c.ldd + col, p.d_vec, left,
            make_uint2(pack16<kBf16>(v[0], v[1]), pack16<kBf16>(v[2], v[3])));

@@ -463,11 +463,11 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
         with_act(p.c.act, [&](auto a) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float lo = 0.f, hi = 0.f, s0, s1;
+            float lo = 0.f, hi = 0.f;
             if constexpr (decltype(a)::value != kActNone) unpack16<kBf16>(r[16 * h + j], lo, hi);
-            act_slope2<decltype(a)::value>(lo, hi, s0, s1);
-            v[2 * j] = __uint_as_float(acc[2 * j]) * row_scale * s0;
-            v[2 * j + 1] = __uint_as_float(acc[2 * j + 1]) * row_scale * s1;
+            const F2 d = mul2(f2(__uint_as_float(acc[2 * j]), __uint_as_float(acc[2 * j + 1])),
+                              f2(row_scale));
+            split(mul2(d, act_slope2<decltype(a)::value>(lo, hi)), v[2 * j], v[2 * j + 1]);
           }
         });
       }
