@@ -121,6 +121,16 @@ def test_empty_problems_are_no_ops(gemm_mod, name):
     assert call(lib, name, M=0, A=None, D=None, **none) == OK
 
 
+def test_wrong_arguments_of_the_marshalling_module(gemm_mod):
+    mod = gemm_mod._load_layers()
+    with pytest.raises(TypeError):
+        mod.rms_norm(1, 2)                      # too few
+    with pytest.raises(TypeError):
+        mod.act_grad(1, None, None, None, None, None)  # not a tensor
+    with pytest.raises(KeyError):
+        mod.bind("gemm_f32", 0)
+
+
 def test_cpu_tensors_are_refused(gemm_mod):
     import torch
     x = torch.zeros(8, 16, dtype=torch.bfloat16)

@@ -206,6 +206,27 @@ def test_same_bits_every_call_and_on_another_stream(gemm_mod, m):
     assert torch.equal(D[0], D[1]) and torch.equal(D[0], D[2])
 
 
+def test_output_past_2_to_31_elements(gemm_mod):
+    """Offsets of D, Z and R pass 32 bits: the last rows of a tall output, against
+    the same rows computed alone."""
+    m, n, k = 70000, 32768, 64
+    A = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+    A[-300:] = normal((300, k), torch.bfloat16, 1)
+    B = normal((n, k), torch.bfloat16, 2)
+    D, R = (torch.empty(m, n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    R[:-300].zero_()
+    R[-300:] = normal((300, n), torch.bfloat16, 3)
+    gemm_mod.gemm_epilogue(A, B, D, residual=R, act="silu", trans_b=True)
+    tail = torch.empty(300, n, dtype=torch.bfloat16, device="cuda")
+    gemm_mod.gemm_epilogue(A[-300:], B, tail, residual=R[-300:], act="silu", trans_b=True)
+    assert torch.equal(D[-300:], tail)
+    assert not D[:-300].any()
+    gemm_mod.act_grad(D, R, D, act="relu")
+    want = torch.empty_like(tail)
+    gemm_mod.act_grad(tail, R[-300:], want, act="relu")
+    assert torch.equal(D[-300:], want)
+
+
 def test_captured_in_a_graph(gemm_mod):
     A = normal((24, 512), torch.bfloat16, 1)
     B = normal((768, 512), torch.bfloat16, 2)
