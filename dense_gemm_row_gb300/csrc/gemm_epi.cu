@@ -106,7 +106,10 @@ cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t
     return mp ? launch_split_fwd(dev, mp, b_t, M, N, K, A, lda, B, ldb, epi, nullptr, stream)
               : launch_epi_fwd(dev, tile_n, a_t, b_t, M, N, K, A, lda, B, ldb, epi, stream);
   }
-  // Gradient: partial column sums, one row per token tile or per 32 rows of D.
+  // Gradient: partial column sums, one row per token tile or per 32 rows of D. A
+  // single token tile's kernel writes dbias itself.
+  if (mp && M <= mp)
+    return launch_split_grad(dev, mp, b_t, M, N, K, A, lda, B, ldb, epi, nullptr, stream);
   const int parts = static_cast<int>((static_cast<int64_t>(M) + (mp ? mp : 32) - 1) / (mp ? mp : 32));
   void *part = nullptr;
   if (epi.dbias != nullptr) {

@@ -77,7 +77,7 @@ struct SplitArgs {
   bool r_vec, d_vec, z_vec;  // rows of R / D / Z in whole 8-byte units
   uint32_t idesc;
   uint32_t *err_word;
-  float *part;  // gradient: column sums per token tile [tiles_m][N], or null
+  float *part;  // gradient, several token tiles: column sums of each [tiles_m][N]
   EpiCall c;
 };
 
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   }
 
   if constexpr (kGrad) {
-    if (p.part != nullptr) {
+    if (p.c.dbias != nullptr) {
       // Column sums of this CTA's columns: the threads of a column in row order.
       // The stages are free: every read of the partial sums is behind the barrier.
       static_assert(Cf::kStages * Cf::kABytes >= kSplitFinish * 16, "room for the sums");
@@ -394,7 +394,12 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
         float s = 0.f;
         for (int i = t / 4; i < kSplitFinish; i += wq)
           s += reinterpret_cast<const float *>(slots + i)[t & 3];
-        p.part[static_cast<int64_t>(tile % p.tiles_m) * p.N + at] = s;
+        // All rows in one token tile: the sum is complete.
+        if (p.part != nullptr) {
+          p.part[static_cast<int64_t>(tile % p.tiles_m) * p.N + at] = s;
+        } else {
+          p.c.dbias[at] = p.c.bf16 ? to16<true>(s) : to16<false>(s);
+        }
       }
     }
   }

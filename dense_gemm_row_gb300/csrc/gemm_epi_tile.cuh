@@ -591,8 +591,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             warp, lane, ok);
       }
     }
-    // Never leave with a TMA store still reading the staging buffer.
-    if (lane == 0) bulk_wait_all();
+    // Never leave with a TMA store still reading the staging buffer (its writes
+    // are complete when the grid is).
+    if (lane == 0) bulk_wait_read_all();
     __syncwarp();
   }
 
