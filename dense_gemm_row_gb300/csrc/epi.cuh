@@ -150,6 +150,19 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+// Two 16-bit values of a word, widened.
+template <bool kBf16>
+__device__ __forceinline__ F2 unpack2(uint32_t w) {
+  float a, b;
+  unpack16<kBf16>(w, a, b);
+  return f2(a, b);
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(F2 v) {
+  float a, b;
+  split(v, a, b);
+  return pack16<kBf16>(a, b);
+}
 // 2^x and 1 / x of both values (exp_fast and rcp_fast's instructions).
 __device__ __forceinline__ F2 exp2_fast2(F2 x) {
   float a, b;

@@ -294,7 +294,8 @@ template <bool kBf16, int NV>
 struct GradSums {
   uint4 w[NV];
   uint32_t we;
-  float dw[NV][8], dwe;
+  F2 dw[NV][4];
+  float dwe;
 
   template <int T>
   __device__ __forceinline__ void begin(const RmsGradCall &c, const RowWalk &k, int off, int t) {
@@ -304,7 +305,7 @@ struct GradSums {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+      for (int q = 0; q < 4; ++q) dw[i][q] = f2(0.f);
       w[i] = c.W ? load_unit(c.W, k, i * T + t, row_offset(c.W) == off)
                  : make_uint4(one, one, one, one);
     }
@@ -314,61 +315,82 @@ struct GradSums {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (i * T + t >= k.units) continue;
+      float *p = out + k.head + 8 * (i * T + t);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) out[k.head + 8 * (i * T + t) + e] = dw[i][e];
+      for (int q = 0; q < 4; ++q) split(dw[i][q], p[2 * q], p[2 * q + 1]);
     }
     if (k.extra >= 0) out[k.extra] = dwe;
   }
 };
 
+// The gain's packed values, widened again for every row: hoisted out of the row
+// loop, the widened ones would take twice the registers and spill.
+__device__ __forceinline__ uint4 per_row(uint4 w) {
+  asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w));
+  return w;
+}
+
 // One row by T threads. get(a, i): packed unit i of this thread of matrix a (0:
-// dY, 1: H, 2: dH); extra[a]: its extra value. Units are read twice, before and
-// after the reduction, instead of being held in registers over it. between() runs
-// behind the reduction. X: the row of dX.
+// dY, 1: H, 2: dH), called for units inside the row; extra[a]: its extra value.
+// Units are read twice, before and after the reduction, instead of being held in
+// registers over it. between() runs behind the reduction. X: the row of dX; back:
+// whether there is a dH; inv_n: 1 / cols.
+//
+// With t = dy s: dw += t h and sum(g n) = sum(t w h), so that
+// dx = s (dy w) - h (s^2 mean(g n)) + dh takes three operations per value, on
+// packed pairs.
 template <bool kBf16, int T, int NV, typename Get, typename Between>
-__device__ __forceinline__ void grad_row(uint16_t *X, int cols, const RowWalk &k, bool same,
-                                         int t, GradSums<kBf16, NV> &sums, float s,
+__device__ __forceinline__ void grad_row(uint16_t *X, const RowWalk &k, bool same, bool past,
+                                         int t, GradSums<kBf16, NV> &sums, float s, float inv_n,
                                          const uint32_t (&extra)[3], float *red, Get &&get,
                                          Between &&between) {
-  // With t = dy s: dw += t h and sum(g n) = sum(t w h), so that
-  // dx = s (dy w) - h (s^2 mean(g n)) + dh takes three operations per value.
-  float dot = 0.f;
-  auto first = [&](float yv, float hv, float wv, float &acc) {
-    const float ts = yv * s;
-    acc = fmaf(ts, hv, acc);
-    dot = fmaf(ts * wv, hv, dot);
-  };
+  const F2 s2 = f2(s);
+  F2 dots = f2(0.f);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float yv[8], hv[8], wv[8];
-    unit_values<kBf16>(get(0, i), yv);
-    unit_values<kBf16>(get(1, i), hv);
-    unit_values<kBf16>(sums.w[i], wv);
+    if (i * T + t < k.units) {
+      const uint4 y = get(0, i), h = get(1, i), w = per_row(sums.w[i]);
+      const uint32_t yw[4] = {y.x, y.y, y.z, y.w}, hw[4] = {h.x, h.y, h.z, h.w};
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) first(yv[e], hv[e], wv[e], sums.dw[i][e]);
+      for (int q = 0; q < 4; ++q) {
+        const F2 ts = mul2(unpack2<kBf16>(yw[q]), s2), hv = unpack2<kBf16>(hw[q]);
+        sums.dw[i][q] = fma2(ts, hv, sums.dw[i][q]);
+        dots = fma2(mul2(ts, unpack2<kBf16>(ww[q])), hv, dots);
+      }
+    }
   }
-  if (k.extra >= 0)
-    first(from16<kBf16>(extra[0]), from16<kBf16>(extra[1]), from16<kBf16>(sums.we), sums.dwe);
+  float dot, dot1;
+  split(dots, dot, dot1);
+  dot += dot1;
+  const float ye = from16<kBf16>(extra[0]), he = from16<kBf16>(extra[1]);
+  const float we = from16<kBf16>(sums.we);
+  if (k.extra >= 0) {
+    sums.dwe = fmaf(ye * s, he, sums.dwe);
+    dot = fmaf(ye * s * we, he, dot);
+  }
   dot = row_sum<T>(dot, red);
   between();
-  const float back = -s * s * (dot / static_cast<float>(cols));
-  auto second = [&](float yv, float hv, float wv, float bv) {
-    return fmaf(yv * wv, s, fmaf(hv, back, bv));
-  };
+  const float back = -s * s * (dot * inv_n);
+  const F2 back2 = f2(back);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float yv[8], hv[8], wv[8], bv[8];
-    unit_values<kBf16>(get(0, i), yv);
-    unit_values<kBf16>(get(1, i), hv);
-    unit_values<kBf16>(sums.w[i], wv);
-    unit_values<kBf16>(get(2, i), bv);
+    if (i * T + t < k.units) {
+      const uint4 y = get(0, i), h = get(1, i), w = per_row(sums.w[i]);
+      const uint4 b = past ? get(2, i) : make_uint4(0, 0, 0, 0);
+      const uint32_t yw[4] = {y.x, y.y, y.z, y.w}, hw[4] = {h.x, h.y, h.z, h.w};
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w}, bw[4] = {b.x, b.y, b.z, b.w};
+      uint32_t out[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) yv[e] = second(yv[e], hv[e], wv[e], bv[e]);
-    store_unit(X, k, i * T + t, same, unit_pack<kBf16>(yv));
+      for (int q = 0; q < 4; ++q)
+        out[q] = pack2<kBf16>(
+            fma2(mul2(unpack2<kBf16>(yw[q]), unpack2<kBf16>(ww[q])), s2,
+                 fma2(unpack2<kBf16>(hw[q]), back2, unpack2<kBf16>(bw[q]))));
+      store_unit(X, k, i * T + t, same, make_uint4(out[0], out[1], out[2], out[3]));
+    }
   }
   if (k.extra >= 0)
-    X[k.extra] = to16<kBf16>(second(from16<kBf16>(extra[0]), from16<kBf16>(extra[1]),
-                                    from16<kBf16>(sums.we), from16<kBf16>(extra[2])));
+    X[k.extra] = to16<kBf16>(fmaf(ye * we, s, fmaf(he, back, from16<kBf16>(extra[2]))));
 }
 
 // Short rows: one warp per row, straight from global memory; the warps in
@@ -400,7 +422,8 @@ __global__ void __launch_bounds__(128, kGradWarpBlocks<NV>)
       extra[a] = load_extra(rows[a], k);
     }
     uint16_t *X = c.dX + r * c.lddx;
-    grad_row<kBf16, 32, NV>(X, c.cols, k, row_offset(X) == off, t, sums, c.rstd[r], extra, nullptr,
+    grad_row<kBf16, 32, NV>(X, k, row_offset(X) == off, c.dH != nullptr, t, sums, c.rstd[r],
+                            1.f / static_cast<float>(c.cols), extra, nullptr,
                             [&](int a, int i) { return v[a][i]; }, [] {});
   }
   if (part == nullptr) return;
@@ -420,8 +443,8 @@ __global__ void __launch_bounds__(128, kGradWarpBlocks<NV>)
 // whatever the threads do, and the values cost no registers between the two
 // passes over them. (Prefetching the next row into registers reached 96 us at
 // 8192 x 8192, and 143 us once the extra columns' loads shared their
-// scoreboards.) What bounds it beside memory is instructions, about 20 per
-// value: so no division for the ring's indexes and no 64-bit products per row.
+// scoreboards.) What bounds it beside memory is instructions: packed pairs, no
+// division for the ring's indexes and no 64-bit products per row.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
                                           uint32_t bar) {
   asm volatile(
@@ -484,6 +507,7 @@ __global__ void __launch_bounds__(T, 1024 / T)
   GradSums<kBf16, NV> sums;
   sums.template begin<T>(c, k, row_offset(Y), t);
   uint32_t stage = 0, phase = 0;
+  const float inv_n = 1.f / static_cast<float>(c.cols);
   float s = *rstd;
   uint32_t extra[3] = {0, 0, 0};
   for (int n = 0; n < rows; ++n) {
@@ -498,11 +522,9 @@ __global__ void __launch_bounds__(T, 1024 / T)
       mbar_wait_bounded(smem_u32(&full[stage]), phase, abort, err_word, kWaitFull);
     const uint8_t *row = ring + stage * 3u * slab + t * 16;
     grad_row<kBf16, T, NV>(
-        X, c.cols, k, true, t, sums, s, extra, red[n & 1],
+        X, k, true, B != nullptr, t, sums, s, inv_n, extra, red[n & 1],
         [&](int a, int i) {
-          return i * T + t < k.units && (a < 2 || B != nullptr)
-                     ? *reinterpret_cast<const uint4 *>(row + a * slab + i * T * 16)
-                     : make_uint4(0, 0, 0, 0);
+          return *reinterpret_cast<const uint4 *>(row + a * slab + i * T * 16);
         },
         [&] {
           // Behind the reduction's barrier every thread has left the previous
