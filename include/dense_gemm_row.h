@@ -2,7 +2,7 @@
  * dense_gemm_row.h -- C ABI of the GB300 (sm_103a) row-major dense GEMM library
  * (libdense_gemm_row.so).
  *
- * Every entry point computes
+ * Every GEMM entry point computes
  *
  *     C = alpha * A * B + beta * C
  *
