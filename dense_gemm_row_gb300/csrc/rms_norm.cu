@@ -546,7 +546,26 @@ __global__ void __launch_bounds__(T, 1024 / T)
       mbar_wait_bounded(smem_u32(&full[i % stages]), static_cast<uint32_t>(i / stages) & 1u, &never,
                         err_word, kWaitDrain);
   }
-  if (part != nullptr) sums.template end<T>(part + slot * c.cols, k, t);
+  if (part == nullptr) return;
+  // The block's partial row goes out in whole lines: through shared memory (the
+  // ring is free), value e of unit u at e * pitch + u, with a pitch that spreads
+  // the 32 consecutive columns a warp reads back over the banks. Written from
+  // the threads directly, 8 columns apart per lane, it took longer than a row.
+  __syncthreads();
+  float *out = part + slot * c.cols, *sums8 = reinterpret_cast<float *>(ring);
+  const int pitch = (k.units + 27) / 32 * 32 + 4;  // 4 modulo 32, at least units
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int u = i * T + t;
+    if (u >= k.units) continue;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      split(sums.dw[i][q], sums8[2 * q * pitch + u], sums8[(2 * q + 1) * pitch + u]);
+  }
+  if (k.extra >= 0) out[k.extra] = sums.dwe;
+  __syncthreads();
+  for (int j = t; j < 8 * k.units; j += T)
+    out[k.head + j] = sums8[(j & 7) * pitch + (j >> 3)];
 }
 
 // Rows of any length and alignment: one block per group of rows; the partial sums of dw live
@@ -661,11 +680,11 @@ template <bool kBf16, int T, int NV = 2>
 cudaError_t launch_grad_ring(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_t stream) {
   auto kern = rms_norm_grad_kernel<kBf16, T, NV>;
   // 1024 threads per SM share about 200 KB of rows in flight; the blocks beside
-  // each other hide each other's reductions.
-  const int stage = c.cols / 8 * 16 * 3;
+  // each other hide each other's reductions. At the end the ring holds the sums.
+  const int units = c.cols / 8, stage = units * 16 * 3;
   const int room = 200 * T;
   const int stages = std::max(2, std::min(kMaxGradStages, room / std::max(stage, 1)));
-  const int smem = stages * stage;
+  const int smem = std::max(stages * stage, ((units + 27) / 32 * 32 + 4) * 8 * 4);
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem, dev.device);
   if (e != cudaSuccess) return e;
   int per_sm = 0;
