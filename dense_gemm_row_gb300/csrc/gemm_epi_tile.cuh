@@ -20,10 +20,12 @@
 // kernel, none per k-block) and the epilogue, most of the code, is shared.
 //
 // Epilogue data: the tile's bias and column scales are put in shared memory once
-// per tile (read back as broadcasts); R or Zin is read straight from
-// global memory, 16 bytes per lane, issued before the accumulator is waited for;
-// results are packed and staged in the warp's 4 KiB buffer in the layout of a
-// 128-byte swizzle and stored by TMA. Matrices that TMA cannot address (rows not
+// per tile (read back as broadcasts); R or Zin comes by TMA into the warp's 4 KiB
+// buffer, requested before the accumulator is waited for; results are packed and
+// staged in the same buffer in the layout of a 128-byte swizzle and stored by
+// TMA. (R read straight from global memory, a row per lane, cost 2.3 us per unit
+// in L1 lookups, which showed for short k. Blocks of 32 columns with two half
+// buffers, R a block ahead, were slower: twice the fences and stores.) Matrices that TMA cannot address (rows not
 // in whole 16-byte units) go through the same buffer with coalesced 2-byte
 // accesses, a row of 64 columns per two warp instructions: a lane per row would
 // touch 32 rows per instruction.
@@ -72,6 +74,7 @@ struct __align__(1024) EpiSmem {
   uint64_t empty[EpiCfg<kN>::kStages];
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
+  uint64_t arrived[kEpiWarps];  // R is in a warp's buffer
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -82,7 +85,7 @@ struct EpiArgs {
   int tiles_m, tiles_n, tiles;
   bool a_t, b_t;
   bool d_tma, z_tma;  // D / Z written through their tensor maps
-  bool r_vec;         // R (Zin) read in 16-byte units
+  bool r_tma;         // R (Zin) read through its tensor map
   uint32_t idesc;
   uint32_t *err_word;
   float *part;        // gradient: partial column sums [ceil(M / 32)][N], or null
@@ -105,59 +108,42 @@ __device__ __forceinline__ uint32_t stage_elem(uint32_t stage, int row, int j) {
   return stage_unit(stage, row, j >> 3) + static_cast<uint32_t>(j & 7) * 2u;
 }
 
-// 64 16-bit values of row `row`, columns col.. of a row-major matrix, as packed
-// words; zeros outside it. Aligned matrices: the lane's own row, in 16-byte
-// loads. Others: the warp reads its 32 rows one by one, coalesced, through the
-// staging buffer (which must be free).
-__device__ __forceinline__ void load_block(const uint16_t *p, int64_t ld, bool vec, int row0,
-                                           int col, int M, int N, uint32_t stage, int lane,
-                                           uint32_t (&w)[32]) {
-  if (vec) {
-    const int row = row0 + lane;
-    const uint16_t *q = p + row * ld + col;
+// The lane's row of a staged block, packed.
+__device__ __forceinline__ void read_staged(uint32_t stage, int lane, uint32_t (&w)[32]) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (row < M) {
-        if (col + 8 * u + 7 < N) {
-          v = *reinterpret_cast<const uint4 *>(q + 8 * u);
-        } else if (col + 8 * u < N) {  // the last, partial unit
-          uint32_t h[8];
+  for (int u = 0; u < 8; ++u)
+    ld_shared_v4(stage_unit(stage, lane, u), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+}
+// Stages 32 rows x 64 columns of a matrix that TMA cannot read, row by row,
+// coalesced; zeros outside it.
+__device__ __forceinline__ void stage_block(const uint16_t *p, int64_t ld, int row0, int col,
+                                            int M, int N, uint32_t stage, int lane) {
+  // 16 rows' loads (two per lane) are in flight together.
 #pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = col + 8 * u + e < N ? q[8 * u + e] : 0;
-          v = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
-                         h[6] | (h[7] << 16));
-        }
-      }
-      w[4 * u] = v.x, w[4 * u + 1] = v.y, w[4 * u + 2] = v.z, w[4 * u + 3] = v.w;
+  for (int r0 = 0; r0 < 32; r0 += 16) {
+    uint16_t v[16][2];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint16_t *q = p + (row0 + r0 + i) * ld + col + lane;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        v[i][h] = row0 + r0 + i < M && col + lane + 32 * h < N ? q[32 * h] : 0;
     }
-  } else {
-    // 16 rows' loads (two per lane) are in flight together.
 #pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += 16) {
-      uint16_t v[16][2];
+    for (int i = 0; i < 16; ++i)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint16_t *q = p + (row0 + r0 + i) * ld + col + lane;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          v[i][h] = row0 + r0 + i < M && col + lane + 32 * h < N ? q[32 * h] : 0;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(stage_elem(stage, r0 + i, lane + 32 * h)),
-                       "h"(v[i][h])
-                       : "memory");
-    }
-    __syncwarp();
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      ld_shared_v4(stage_unit(stage, lane, u), w[4 * u], w[4 * u + 1], w[4 * u + 2],
-                   w[4 * u + 3]);
-    __syncwarp();
+      for (int h = 0; h < 2; ++h)
+        asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(stage_elem(stage, r0 + i, lane + 32 * h)),
+                     "h"(v[i][h])
+                     : "memory");
   }
+  __syncwarp();
+}
+
+// Waits (bounded) for a copy of R that is in flight, whatever else has failed.
+__device__ __forceinline__ void wait_copy(uint32_t bar, uint32_t parity, uint32_t *err_word) {
+  volatile int never = 0;
+  mbar_wait_lazy(bar, parity, &never, err_word, kWaitDrain);
 }
 
 // The staging buffer's three steps: wait until the last store has left it, put
@@ -374,9 +360,10 @@ __device__ __forceinline__ void epi_multiply(const EpiArgs &p, EpiSmem<kN> &sm,
 // One tile's epilogue by one warp (32 rows x kN / 2 columns).
 template <bool kE4m3, bool kGrad, bool kBf16, int kN>
 __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorMap &tmZ,
-                                         const EpiArgs &p, EpiSmem<kN> &sm, uint32_t tmem_base,
-                                         uint32_t n, int tm, int tn, uint32_t rank, int warp,
-                                         int lane, bool &ok) {
+                                         const CUtensorMap &tmR, const EpiArgs &p,
+                                         EpiSmem<kN> &sm, uint32_t tmem_base, uint32_t n, int tm,
+                                         int tn, uint32_t rank, int warp, int lane,
+                                         uint32_t &rphase, bool &ok) {
   const int e = warp - 2, quarter = warp & 3, half = e >> 2;
   const uint32_t stage = smem_u32(sm.stage[e]);
   const uint32_t buf = n & 1u, use = (n >> 1) & 1u;
@@ -396,18 +383,33 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
   float row_scale = p.c.alpha;
   if (kE4m3 && p.c.scale_a && row < p.M) row_scale *= __ldg(p.c.scale_a + row);
   uint32_t r[32];
-  // The staging buffer is free for load_block once the last store has left it.
-  auto load_r = [&](int col) {
-    if (p.c.R == nullptr) return;
-    if (!p.r_vec) stage_free(lane);
-    load_block(p.c.R, p.c.ldr, p.r_vec, row0, col, p.M, p.N, stage, lane, r);
+  const bool have_r = p.c.R != nullptr;
+  // Requests the unit's R into the staging buffer, and takes it from there.
+  const uint32_t rbar = smem_u32(&sm.arrived[e]);
+  auto request_r = [&](int col) {
+    stage_free(lane);
+    if (p.r_tma) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(rbar, kStageCBytes);
+        tma_load_3d(stage, &tmR, rbar, col, row0, 0);
+      }
+    } else {
+      stage_block(p.c.R, p.c.ldr, row0, col, p.M, p.N, stage, lane);
+    }
   };
-  load_r(col0);
-  int got = 0;
-  if (lane == 0)
-    got = mbar_wait_bounded(smem_u32(&sm.tmem_full[buf]), use, abort, p.err_word, kWaitTmemFull);
-  got = __shfl_sync(0xffffffffu, got, 0);
-  if (!got) {
+  auto take_r = [&] {
+    if (p.r_tma) {
+      wait_copy(rbar, rphase, p.err_word);
+      rphase ^= 1u;
+    }
+    read_staged(stage, lane, r);
+    __syncwarp();
+  };
+  if (have_r) request_r(col0);
+  const bool got = mbar_wait_lazy(smem_u32(&sm.tmem_full[buf]), use, abort, p.err_word,
+                                  kWaitTmemFull);
+  if (have_r) take_r();
+  if (!__all_sync(0xffffffffu, got)) {
     ok = false;
     return;
   }
@@ -485,7 +487,10 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
       }
     }
     store_block(&tmD, p.d_tma, p.c.D, p.c.ldd, row0, col0 + c, p.M, p.N, stage, lane);
-    if (c + 64 < kN / 2) load_r(col0 + c + 64);
+    if (have_r && c + 64 < kN / 2) {
+      request_r(col0 + c + 64);
+      take_r();
+    }
   }
 }
 
@@ -495,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmD,
                          const __grid_constant__ CUtensorMap tmZ,
+                         const __grid_constant__ CUtensorMap tmR,
                          const __grid_constant__ EpiArgs p) {
   using Cf = EpiCfg<kN>;
   extern __shared__ uint8_t smem_raw[];
@@ -515,11 +521,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sm.tmem_empty[i]), 2 * kEpiWarps);
     }
     mbar_init(smem_u32(&sm.drain), 1);
+    for (int i = 0; i < kEpiWarps; ++i) mbar_init(smem_u32(&sm.arrived[i]), 1);
     sm.abort = 0;
     fence_mbar_init();
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
     if (p.d_tma) prefetch_tmap(&tmD);
+    if (p.r_tma) prefetch_tmap(&tmR);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(&sm.tmem_base), Cf::kTmem);
@@ -571,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // barriers; after a wait that gave up it skips the work, not the barriers.
     grid_dependency_wait();
     bool ok = true;
-    uint32_t n = 0;
+    uint32_t n = 0, rphase = 0;
     for (int t = unit; t < p.tiles; t += units, ++n) {
       int tm, tn;
       tile_coords<kEpiGroupM>(t, p.tiles_m, p.tiles_n, tm, tn);
@@ -584,11 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       if (p.c.bf16) {
-        epi_tile<kE4m3, kGrad, true, kN>(tmD, tmZ, p, sm, tmem_base, n, tm, tn, rank,
-                                            warp, lane, ok);
+        epi_tile<kE4m3, kGrad, true, kN>(tmD, tmZ, tmR, p, sm, tmem_base, n, tm, tn, rank, warp,
+                                          lane, rphase, ok);
       } else {
-        epi_tile<kE4m3, kGrad, false, kN>(tmD, tmZ, p, sm, tmem_base, n, tm, tn, rank,
-                                            warp, lane, ok);
+        epi_tile<kE4m3, kGrad, false, kN>(tmD, tmZ, tmR, p, sm, tmem_base, n, tm, tn, rank, warp,
+                                          lane, rphase, ok);
       }
     }
     // Never leave with a TMA store still reading the staging buffer (its writes
@@ -605,13 +613,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// A 16-bit output matrix as a tensor map of 32 x 64 blocks, where TMA can write
-// it: 16-byte aligned rows of whole 16-byte units (a store box is clipped at the
-// right edge in such units only).
-inline bool out_tmap(CUtensorMap *tm, bool bf16, uint16_t *p, int64_t ld, int M, int N) {
-  return p != nullptr && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && N % 8 == 0 &&
+// A 16-bit matrix as a tensor map of 32 x 64 blocks, where TMA can address it
+// (16-byte aligned rows). An output's rows also have to be whole 16-byte units
+// long: a store box is clipped at the right edge in such units only.
+inline bool block_tmap(CUtensorMap *tm, bool bf16, const uint16_t *p, int64_t ld, int M, int N) {
+  return p != nullptr && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 &&
          make_tmap(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                    p, M, N, ld, 1, 0, 32, 64, false);
+}
+inline bool out_tmap(CUtensorMap *tm, bool bf16, const uint16_t *p, int64_t ld, int M, int N) {
+  return N % 8 == 0 && block_tmap(tm, bf16, p, ld, M, N);
 }
 
 template <bool kE4m3, int kN, bool kGrad>
@@ -629,9 +640,10 @@ cudaError_t launch_epi_tile(const DeviceInfo &dev, bool a_t, bool b_t, int M, in
   const CUtensorMapDataType dt = kE4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                  : epi.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  CUtensorMap tmA, tmB, tmD, tmZ;
+  CUtensorMap tmA, tmB, tmD, tmZ, tmR;
   std::memset(&tmD, 0, sizeof tmD);
   std::memset(&tmZ, 0, sizeof tmZ);
+  std::memset(&tmR, 0, sizeof tmR);
   if (!(a_t ? make_tmap(&tmA, dt, kEs, A, K, M, lda, 1, 0, 64, 64)
             : make_tmap(&tmA, dt, kEs, A, M, K, lda, 1, 0, kBM, kBK)) ||
       !(b_t ? make_tmap(&tmB, dt, kEs, B, N, K, ldb, 1, 0, Cf::kBNLoad, kBK)
@@ -647,7 +659,7 @@ cudaError_t launch_epi_tile(const DeviceInfo &dev, bool a_t, bool b_t, int M, in
   p.a_t = a_t, p.b_t = b_t;
   p.d_tma = out_tmap(&tmD, epi.bf16, epi.D, epi.ldd, M, N);
   p.z_tma = out_tmap(&tmZ, epi.bf16, epi.Z, epi.ldz, M, N);
-  p.r_vec = reinterpret_cast<uintptr_t>(epi.R) % 16 == 0 && epi.ldr % 8 == 0;
+  p.r_tma = block_tmap(&tmR, epi.bf16, epi.R, epi.ldr, M, N);
   p.idesc = idesc_mma(kE4m3 || !epi.bf16 ? 0u : kFmtBF16, a_t, !b_t, Cf::kTileM, kN);
   p.err_word = dev.err_word;
   p.part = part;
@@ -667,7 +679,7 @@ cudaError_t launch_epi_tile(const DeviceInfo &dev, bool a_t, bool b_t, int M, in
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, tmZ, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, tmZ, tmR, p);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
