@@ -66,16 +66,20 @@ cudaError_t launch_empty(int M, int N, const EpiCall &epi, cudaStream_t stream) 
 //   256 x 256 tiles   5.2 + waves * KB * 0.28
 //   256 x 128 tiles   4.2 + waves * KB * 0.165 (dearer per output, fewer idle SMs)
 //   few-rows kernel   up to 64 rows always: 64 x 4096 x 4096 9.9 against 15.2,
-//                     64 x 1024 x 512 4.5 against 5.2; above, where the 256 x 128
-//                     tiles would fill the GPU `idle` >= 2 times over and leave a
-//                     long k range to one pair each: KB * idle >= 128
-//                     (128 x 1024 x 4096 7.6 against 14.5, 256 x 4096 x 4096 15.1
-//                     against 15.8; not 256 x 1024 x 512, 8.4 against 5.6).
+//                     64 x 1024 x 512 4.5 against 5.2; up to 128 where D's rows
+//                     are not whole 16-byte units, which the tiles' epilogue
+//                     writes 2 bytes at a time: 100 x 1023 x 513 6.4 against 7.7;
+//                     above, where the 256 x 128 tiles would fill the GPU `idle`
+//                     >= 2 times over and leave a long k range to one pair each:
+//                     KB >= 16 and KB * idle >= 128 (128 x 1024 x 4096 7.6 against
+//                     14.5, 256 x 4096 x 4096 15.1 against 15.8; not
+//                     256 x 1024 x 512, 8.4 against 5.6, nor 300 x 95 x 93, 8.1
+//                     against 6.4).
 struct EpiPlan {
   int split_rows;  // rows per token tile of the few-rows kernel, or 0
   int tile_n;      // columns per tile otherwise
 };
-EpiPlan plan_epi(const DeviceInfo &dev, bool a_t, int M, int N, int KB) {
+EpiPlan plan_epi(const DeviceInfo &dev, bool a_t, int M, int N, int KB, bool ragged) {
   const int64_t pairs = std::max(dev.sm_count / 2, 1);
   const int64_t rows = (static_cast<int64_t>(M) + 255) / 256;
   const int64_t t256 = rows * ((static_cast<int64_t>(N) + 255) / 256);
@@ -83,7 +87,7 @@ EpiPlan plan_epi(const DeviceInfo &dev, bool a_t, int M, int N, int KB) {
   const int64_t idle = pairs / t128;
   EpiPlan plan{0, 256};
   // The few-rows kernel's token tiles are K-major.
-  if (!a_t && (M <= 64 || (idle >= 2 && KB * idle >= 128)))
+  if (!a_t && (M <= (ragged ? 128 : 64) || (idle >= 2 && KB >= 16 && KB * idle >= 128)))
     plan.split_rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   const double w256 = static_cast<double>((t256 + pairs - 1) / pairs);
   const double w128 = static_cast<double>((t128 + pairs - 1) / pairs);
@@ -97,7 +101,9 @@ cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t
                             int K, const void *A, int64_t lda, const void *B, int64_t ldb,
                             const EpiCall &epi, cudaStream_t stream) {
   if (K == 0) return launch_empty(M, N, epi, stream);
-  const EpiPlan plan = plan_epi(dev, a_t, M, N, (K + (e4m3 ? 127 : 63)) / (e4m3 ? 128 : 64));
+  const bool ragged = N % 8 != 0 || epi.ldd % 8 != 0 || reinterpret_cast<uintptr_t>(epi.D) % 16 != 0;
+  const EpiPlan plan =
+      plan_epi(dev, a_t, M, N, (K + (e4m3 ? 127 : 63)) / (e4m3 ? 128 : 64), ragged);
   const int mp = plan.split_rows, tile_n = plan.tile_n;
   if (!epi.grad) {
     if (e4m3)
