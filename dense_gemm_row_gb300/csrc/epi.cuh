@@ -61,68 +61,16 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   }
 }
 
-// The hardware's exponential and reciprocal, subnormals taken as zero: a few
-// 2^-22 (relative), far below one 16-bit rounding (2^-9 for bf16, 2^-12 for
-// fp16). One instruction each; __expf and __fdividef add the handling of
-// subnormals around them, which an element-wise pass pays for.
-__device__ __forceinline__ float exp_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
-  return y;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 1 / (1 + exp(-x)). exp(-x) overflows to +inf for x < -88, where the quotient
-// is 0, its limit.
-__device__ __forceinline__ float logistic(float x) { return rcp_fast(1.f + exp_fast(-x)); }
-
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 constexpr float kInvSqrt2 = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
-
-// The normal distribution function Phi(z). Phi(-x sqrt 2) = erfc(x) / 2, and erfc(x) = exp(-x^2) t P(t)
-// with t = 1 / (1 + x / 2): P is the degree-6 polynomial that minimises the
-// largest relative error over 0 <= x <= 9.3 (iteratively reweighted least
-// squares against a double-precision erfc; 1.5e-6 with fp32 coefficients).
-// The relative error holds in the lower tail too, where 1 + erf cancels.
-__device__ __forceinline__ float normal_cdf(float z) {
-  const float x = fabsf(z) * kInvSqrt2;
-  const float t = rcp_fast(fmaf(0.5f, x, 1.f));
-  const float e = exp_fast(-0.5f * z * z);
-  float p = 0.08912812918424606f;
-  p = fmaf(p, t, -0.35999614000320435f);
-  p = fmaf(p, t, 0.39379453659057617f);
-  p = fmaf(p, t, 0.03464719280600548f);
-  p = fmaf(p, t, 0.28272417187690735f);
-  p = fmaf(p, t, 0.2773527503013611f);
-  p = fmaf(p, t, 0.2823481559753418f);
-  const float q = 0.5f * e * t * p;
-  return z < 0.f ? q : 1.f - q;
-}
-
-template <int kAct>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (kAct == kActRelu) {
-    return z < 0.f ? 0.f : z;
-  } else if constexpr (kAct == kActGelu) {
-    return z * normal_cdf(z);
-  } else if constexpr (kAct == kActGeluTanh) {
-    return z * logistic(2.f * kGeluC * (z + kGeluA * z * z * z));
-  } else if constexpr (kAct == kActSilu) {
-    return z * logistic(z);
-  } else {
-    return z;
-  }
-}
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Two fp32 values in one register pair, and the packed operations on them: one
-// instruction for two values, which is what keeps the slopes below the cost of
-// the memory traffic in the element-wise gradient.
+// instruction for two values. It keeps the element-wise gradient near the cost of
+// its memory traffic, and an epilogue's gelu short: 64 columns by eight warps took
+// 1.9 us of a 7.2 us call (300 x 1024 x 512) with one value per instruction.
 struct F2 {
   uint64_t v;
 };
@@ -163,7 +111,10 @@ __device__ __forceinline__ uint32_t pack2(F2 v) {
   split(v, a, b);
   return pack16<kBf16>(a, b);
 }
-// 2^x and 1 / x of both values (exp_fast and rcp_fast's instructions).
+// 2^x and 1 / x of both values: the hardware's approximations, subnormals taken
+// as zero. They are a few 2^-22 (relative) off, far below one 16-bit rounding
+// (2^-9 for bf16, 2^-12 for fp16). 1 / (1 + 2^x) needs no care at the ends: 2^x
+// overflows to infinity, whose reciprocal is 0, the limit.
 __device__ __forceinline__ F2 exp2_fast2(F2 x) {
   float a, b;
   split(x, a, b);
@@ -174,7 +125,60 @@ __device__ __forceinline__ F2 exp2_fast2(F2 x) {
 __device__ __forceinline__ F2 rcp_fast2(F2 x) {
   float a, b;
   split(x, a, b);
-  return f2(rcp_fast(a), rcp_fast(b));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return f2(a, b);
+}
+
+// -erfc(|z| / sqrt 2) / 2, i.e. -Phi(-|z|), and e = exp(-z^2 / 2), for two z.
+// With x = |z| / sqrt 2: erfc(x) = exp(-x^2) t P(t), t = 1 / (1 + x / 2), where P
+// is the degree-6 polynomial that minimises the largest relative error over
+// 0 <= x <= 9.3 (iteratively reweighted least squares against a double-precision
+// erfc; 1.5e-6 with fp32 coefficients). Relative: it holds in the tail, where
+// 1 + erf would cancel.
+__device__ __forceinline__ F2 minus_tail2(F2 z, F2 mag, F2 &e) {
+  e = exp2_fast2(mul2(mul2(z, z), f2(-0.5f * kLog2e)));
+  const F2 t = rcp_fast2(fma2(mag, f2(0.5f * kInvSqrt2), f2(1.f)));
+  F2 p = f2(-0.5f * 0.08912812918424606f);
+  p = fma2(p, t, f2(-0.5f * -0.35999614000320435f));
+  p = fma2(p, t, f2(-0.5f * 0.39379453659057617f));
+  p = fma2(p, t, f2(-0.5f * 0.03464719280600548f));
+  p = fma2(p, t, f2(-0.5f * 0.28272417187690735f));
+  p = fma2(p, t, f2(-0.5f * 0.2773527503013611f));
+  p = fma2(p, t, f2(-0.5f * 0.2823481559753418f));
+  return mul2(mul2(e, t), p);
+}
+// The logistic functions of the tanh form and of silu: s(2u) and s(z).
+__device__ __forceinline__ F2 tanh_gate2(F2 z, F2 zz) {
+  const F2 arg =
+      mul2(z, fma2(zz, f2(-2.f * kGeluC * kLog2e * kGeluA), f2(-2.f * kGeluC * kLog2e)));
+  return rcp_fast2(add2(exp2_fast2(arg), f2(1.f)));
+}
+__device__ __forceinline__ F2 logistic2(F2 z) {
+  return rcp_fast2(add2(exp2_fast2(mul2(z, f2(-kLog2e))), f2(1.f)));
+}
+
+// The activations of two values. gelu: z Phi(z) = max(z, 0) - |z| Phi(-|z|).
+template <int kAct>
+__device__ __forceinline__ F2 act_value2(F2 z) {
+  if constexpr (kAct == kActNone) return z;
+  if constexpr (kAct == kActSilu) return mul2(z, logistic2(z));
+  if constexpr (kAct == kActGeluTanh) return mul2(z, tanh_gate2(z, mul2(z, z)));
+  float z0, z1;
+  split(z, z0, z1);
+  if constexpr (kAct == kActRelu) {  // NaN stays NaN
+    return f2(z0 < 0.f ? 0.f : z0, z1 < 0.f ? 0.f : z1);
+  } else {
+    const F2 mag = f2(fabsf(z0), fabsf(z1));
+    F2 e;
+    return fma2(mag, minus_tail2(z, mag, e), f2(fmaxf(z0, 0.f), fmaxf(z1, 0.f)));
+  }
+}
+template <int kAct>
+__device__ __forceinline__ float act_value(float z) {
+  float a, b;
+  split(act_value2<kAct>(f2(z)), a, b);
+  return a;
 }
 
 // The derivatives at two values. gelu: Phi(z) + z phi(z), with Phi as 1/2 +
@@ -183,35 +187,24 @@ __device__ __forceinline__ F2 rcp_fast2(F2 x) {
 // on z^2 keeps a finite z from making it 0 * inf; silu: s + z s (1 - s).
 template <int kAct>
 __device__ __forceinline__ F2 act_slope2(float z0, float z1) {
-  constexpr float kLog2e = 1.4426950408889634f;
   const F2 z = f2(z0, z1);
   if constexpr (kAct == kActRelu) {  // NaN stays NaN
     return f2(z0 > 0.f ? 1.f : (z0 <= 0.f ? 0.f : z0), z1 > 0.f ? 1.f : (z1 <= 0.f ? 0.f : z1));
   } else if constexpr (kAct == kActGelu) {
-    const F2 e = exp2_fast2(mul2(mul2(z, z), f2(-0.5f * kLog2e)));
-    const F2 t = rcp_fast2(fma2(f2(fabsf(z0), fabsf(z1)), f2(0.5f * kInvSqrt2), f2(1.f)));
-    F2 p = f2(-0.5f * 0.08912812918424606f);  // normal_cdf's polynomial, times -1/2
-    p = fma2(p, t, f2(-0.5f * -0.35999614000320435f));
-    p = fma2(p, t, f2(-0.5f * 0.39379453659057617f));
-    p = fma2(p, t, f2(-0.5f * 0.03464719280600548f));
-    p = fma2(p, t, f2(-0.5f * 0.28272417187690735f));
-    p = fma2(p, t, f2(-0.5f * 0.2773527503013611f));
-    p = fma2(p, t, f2(-0.5f * 0.2823481559753418f));
+    F2 e;
     float a, b;
-    split(fma2(mul2(e, t), p, f2(0.5f)), a, b);
+    split(add2(minus_tail2(z, f2(fabsf(z0), fabsf(z1)), e), f2(0.5f)), a, b);
     const F2 cdf = add2(f2(copysignf(a, z0), copysignf(b, z1)), f2(0.5f));
     return fma2(mul2(z, f2(kInvSqrt2Pi)), e, cdf);
   } else if constexpr (kAct == kActGeluTanh) {
-    const F2 zz = mul2(z, z);
-    const F2 arg = mul2(z, fma2(zz, f2(-2.f * kGeluC * kLog2e * kGeluA), f2(-2.f * kGeluC * kLog2e)));
-    const F2 s = rcp_fast2(add2(exp2_fast2(arg), f2(1.f)));
+    const F2 zz = mul2(z, z), s = tanh_gate2(z, zz);
     float a, b;
     split(zz, a, b);
     const F2 poly = fma2(f2(fminf(a, 1e4f), fminf(b, 1e4f)), f2(6.f * kGeluC * kGeluA),
                          f2(2.f * kGeluC));
     return fma2(mul2(mul2(z, s), fma2(s, f2(-1.f), f2(1.f))), poly, s);
   } else if constexpr (kAct == kActSilu) {
-    const F2 s = rcp_fast2(add2(exp2_fast2(mul2(z, f2(-kLog2e))), f2(1.f)));
+    const F2 s = logistic2(z);
     return fma2(mul2(z, s), fma2(s, f2(-1.f), f2(1.f)), s);
   } else {
     return f2(1.f);

@@ -162,7 +162,7 @@ __device__ __forceinline__ void split_finish(const SplitArgs &p, uint32_t red, i
         store4(p.c.Z + row * p.c.ldz + col, p.z_vec, left,
                make_uint2(pack16<kBf16>(v[0], v[1]), pack16<kBf16>(v[2], v[3])));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = act_value<kAct>(v[e]);
+      for (int e = 0; e < 4; e += 2) split(act_value2<kAct>(f2(v[e], v[e + 1])), v[e], v[e + 1]);
       if (p.c.R) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += r[e];

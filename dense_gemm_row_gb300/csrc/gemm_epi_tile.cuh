@@ -201,25 +201,24 @@ __device__ __forceinline__ float warp_column_sums(float (&v)[32], int lane) {
   return v[0];
 }
 
-// z of 32 columns of one row from the accumulator (forward).
+// z of 32 columns of one row from the accumulator (forward), in pairs.
 template <bool kE4m3, bool kBf16>
 __device__ __forceinline__ void epi_preact(const uint16_t *bias, const float *scale,
                                            float row_scale, const uint32_t (&acc)[32],
-                                           float (&v)[32]) {
+                                           F2 (&v)[16]) {
 #pragma unroll
-  for (int j = 0; j < 32; j += 8) {
-    const uint4 q = *reinterpret_cast<const uint4 *>(bias + j);
+  for (int j = 0; j < 16; j += 4) {
+    const uint4 q = *reinterpret_cast<const uint4 *>(bias + 2 * j);
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int h = 0; h < 8; h += 2) {
-      float b0, b1, s0 = row_scale, s1 = row_scale;
-      unpack16<kBf16>(w[h / 2], b0, b1);
+    for (int h = 0; h < 4; ++h) {
+      F2 s = f2(row_scale);
       if constexpr (kE4m3) {
-        s0 *= scale[j + h];
-        s1 *= scale[j + h + 1];
+        const float2 c = *reinterpret_cast<const float2 *>(scale + 2 * (j + h));
+        s = mul2(s, f2(c.x, c.y));
       }
-      v[j + h] = fmaf(__uint_as_float(acc[j + h]), s0, b0);
-      v[j + h + 1] = fmaf(__uint_as_float(acc[j + h + 1]), s1, b1);
+      v[j + h] = fma2(f2(__uint_as_float(acc[2 * (j + h)]), __uint_as_float(acc[2 * (j + h) + 1])),
+                      s, unpack2<kBf16>(w[h]));
     }
   }
 }
@@ -423,13 +422,13 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t acc[32], w[16];
-        float v[32];
+        F2 v[16];
         tmem_ld_32x32b_x32(taddr + c + 32 * h, acc);
         tmem_ld_wait();
         epi_preact<kE4m3, kBf16>(&sm.bias[local0 + c + 32 * h], &sm.scale[local0 + c + 32 * h],
                                  row_scale, acc, v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) w[j] = pack16<kBf16>(v[2 * j], v[2 * j + 1]);
+        for (int j = 0; j < 16; ++j) w[j] = pack2<kBf16>(v[j]);
         stage_half(stage, lane, h, w);
       }
       store_block(&tmZ, p.z_tma, p.c.Z, p.c.ldz, row0, col0 + c, p.M, p.N, stage, lane);
@@ -437,7 +436,7 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t acc[32], w[16];
-      float v[32];
+      F2 v[16];
       tmem_ld_32x32b_x32(taddr + c + 32 * h, acc);
       tmem_ld_wait();
       if (c + 32 * h + 32 == kN / 2) {  // all in registers: the next tile may have it
@@ -450,16 +449,11 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
                                  row_scale, acc, v);
         with_act(p.c.act, [&](auto a) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
+          for (int j = 0; j < 16; ++j) v[j] = act_value2<decltype(a)::value>(v[j]);
         });
-        if (p.c.R != nullptr) {
+        if (have_r) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float lo, hi;
-            unpack16<kBf16>(r[16 * h + j], lo, hi);
-            v[2 * j] += lo;
-            v[2 * j + 1] += hi;
-          }
+          for (int j = 0; j < 16; ++j) v[j] = add2(v[j], unpack2<kBf16>(r[16 * h + j]));
         }
       } else {
         with_act(p.c.act, [&](auto a) {
@@ -469,18 +463,21 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
             if constexpr (decltype(a)::value != kActNone) unpack16<kBf16>(r[16 * h + j], lo, hi);
             const F2 d = mul2(f2(__uint_as_float(acc[2 * j]), __uint_as_float(acc[2 * j + 1])),
                               f2(row_scale));
-            split(mul2(d, act_slope2<decltype(a)::value>(lo, hi)), v[2 * j], v[2 * j + 1]);
+            v[j] = mul2(d, act_slope2<decltype(a)::value>(lo, hi));
           }
         });
       }
 #pragma unroll
-      for (int j = 0; j < 16; ++j) w[j] = pack16<kBf16>(v[2 * j], v[2 * j + 1]);
+      for (int j = 0; j < 16; ++j) w[j] = pack2<kBf16>(v[j]);
       if (h == 0) stage_free(lane);
       stage_half(stage, lane, h, w);
       if constexpr (kGrad) {
         // Rows beyond M hold zeros (zero-filled operands), so they add nothing.
         if (p.part != nullptr && row0 < p.M) {
-          const float s = warp_column_sums(v, lane);
+          float u[32];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) split(v[j], u[2 * j], u[2 * j + 1]);
+          const float s = warp_column_sums(u, lane);
           const int col = col0 + c + 32 * h + lane;
           if (col < p.N) p.part[static_cast<int64_t>(row0 / 32) * p.N + col] = s;
         }
