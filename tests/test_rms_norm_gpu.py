@@ -72,6 +72,26 @@ def test_norm(gemm_mod, shape, dtype, out8):
     Y.check_guards()
 
 
+@pytest.mark.parametrize("n", [1, 3, 7, 9, 13, 101, 1001, 2049, 2056, 4095, 6001, 7777, 16383])
+def test_8_bit_rows_padded_for_the_product(gemm_mod, n):
+    """Y in rows of whole 16-byte units, X in packed rows: the two are aligned
+    differently in most rows. Every value, and nothing else, is written."""
+    m = 19
+    X, R = normal((m, n), torch.bfloat16, n), normal((m, n), torch.bfloat16, n + 1)
+    W = vector(n, torch.bfloat16, n)
+    Y = Out(m, n, torch.float8_e4m3fn, pad=-n % 16)
+    scale = torch.empty(m, device="cuda")
+    gemm_mod.rms_norm(X, Y.t, weight=W, residual=R, scale=scale, eps=EPS)
+    torch.cuda.synchronize()
+    y, _, _ = L.rms_norm(L.to64(X), L.to64(W), L.to64(R), EPS)
+    q, qs = L.quantise_e4m3(y)
+    step = qs[:, None] * 2.0 ** -10
+    assert_close(L.to64(Y.t) * L.to64(scale)[:, None], y,
+                 (2.0 ** -4 + 2.0 ** -16) * np.abs(y) + step * (1 + 2.0 ** -16), "Y")
+    assert (L.to64(Y.t) == q).mean() >= 0.99
+    Y.check_guards()
+
+
 @pytest.mark.parametrize("dtype", DTYPES.values(), ids=list(DTYPES))
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
 def test_grad(gemm_mod, shape, dtype):
