@@ -21,7 +21,7 @@ constexpr int kSlots = 32;
 
 template <bool kBf16>
 __global__ void __launch_bounds__(32 * kSlots)
-    col_sums_kernel(const float *__restrict__ part, int parts, int n, int64_t ld, uint16_t *out) {
+    col_sums_kernel(const float *part, int parts, int n, int64_t ld, uint16_t *out) {
   __shared__ float red[kSlots][32];
   grid_dependency_wait();
   const int j = blockIdx.x * 32 + threadIdx.x;

@@ -114,8 +114,8 @@ template <bool kGrad>
 __device__ __forceinline__ void split_load_cols(const SplitArgs &p, int col, SplitCols &k) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    k.bias[e] = !kGrad && p.c.bias && col + e < p.N ? __ldg(p.c.bias + col + e) : 0;
-    k.scale[e] = !kGrad && p.c.scale_b && col + e < p.N ? __ldg(p.c.scale_b + col + e) : 1.f;
+    k.bias[e] = !kGrad && p.c.bias && col + e < p.N ? p.c.bias[col + e] : 0;
+    k.scale[e] = !kGrad && p.c.scale_b && col + e < p.N ? p.c.scale_b[col + e] : 1.f;
   }
 }
 template <bool kGrad>
@@ -125,7 +125,7 @@ __device__ __forceinline__ void split_load_row(const SplitArgs &p, int64_t row, 
   k.scale = 1.f;
   if (row >= p.M || col >= p.N) return;
   if (p.c.R) k.r = load4(p.c.R + row * p.c.ldr + col, p.r_vec, p.N - col);
-  if (!kGrad && p.c.scale_a) k.scale = __ldg(p.c.scale_a + row);
+  if (!kGrad && p.c.scale_a) k.scale = p.c.scale_a[row];
 }
 
 // Adds the partial sums of this CTA's columns over the cluster and writes them.

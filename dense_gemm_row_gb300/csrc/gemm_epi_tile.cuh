@@ -374,13 +374,13 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
     epilogue_sync();  // every warp has read the previous tile's
     for (int i = threadIdx.x - 64; i < kN; i += 32 * kEpiWarps) {
       const int col = tn * kN + i;
-      sm.bias[i] = p.c.bias && col < p.N ? __ldg(p.c.bias + col) : 0;
-      if constexpr (kE4m3) sm.scale[i] = p.c.scale_b && col < p.N ? __ldg(p.c.scale_b + col) : 1.f;
+      sm.bias[i] = p.c.bias && col < p.N ? p.c.bias[col] : 0;
+      if constexpr (kE4m3) sm.scale[i] = p.c.scale_b && col < p.N ? p.c.scale_b[col] : 1.f;
     }
     epilogue_sync();
   }
   float row_scale = p.c.alpha;
-  if (kE4m3 && p.c.scale_a && row < p.M) row_scale *= __ldg(p.c.scale_a + row);
+  if (kE4m3 && p.c.scale_a && row < p.M) row_scale *= p.c.scale_a[row];
   uint32_t r[32];
   const bool have_r = p.c.R != nullptr;
   // Requests the unit's R into the staging buffer, and takes it from there.

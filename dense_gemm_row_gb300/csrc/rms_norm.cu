@@ -412,8 +412,8 @@ __device__ __forceinline__ void grad_row(uint16_t *X, const RowWalk &k, bool sam
     X[k.extra] = to16<kBf16>(fmaf(ye * we, s, fmaf(he, back, from16<kBf16>(extra[2]))));
 }
 
-// Short rows: one warp per row, straight from global memory; the warps in
-// residence hide each other's latency.
+// Short rows of matrices that are aligned differently: one warp per row, straight
+// from global memory; the warps in residence hide each other's latency.
 template <int NV>
 constexpr int kGradWarpBlocks = NV == 1 ? 6 : 4;  // per SM
 
@@ -587,6 +587,133 @@ __global__ void __launch_bounds__(T, 1024 / T)
     out[k.head + j] = sums8[(j & 7) * pitch + (j >> 3)];
 }
 
+// Rows of up to 2048 columns whose matrices are aligned alike: one warp per row.
+// Every lane copies its own units of the warp's next rows into shared memory
+// (asynchronous 16-byte copies), so that no row waits for a block's barrier, no
+// lane for another's copies, and the next rows are in flight whatever the warp
+// does. (Bulk copies instead, three of 512 bytes per row, took 25 us against 19
+// at 32768 x 256.) The block's warps add their sums of dw at the end: one partial
+// row per block. Memory bounds it: 32768 x 1024 with dh 47.5 us, 5.7 TB/s.
+template <int NV>
+constexpr int kGradRowStages = NV == 8 ? 2 : 8 / NV;
+template <int NV>
+constexpr int kGradRowWarps = NV == 8 ? 8 : 16;  // at most: 192 KB of rows per SM
+
+// Where column j of a warp's sums is kept: lanes 8 columns apart hit all banks.
+__device__ __forceinline__ int sums_at(int j) { return j + (j >> 5); }
+
+template <bool kBf16, int NV>
+__global__ void __launch_bounds__(32 * kGradRowWarps<NV>, 1)
+    rms_norm_grad_rows_kernel(const RmsGradCall c, float *part) {
+  constexpr int kStages = kGradRowStages<NV>;
+  constexpr uint32_t kSlab = NV * 512;  // one matrix's row
+  extern __shared__ __align__(128) uint8_t ring[];
+  const int t = static_cast<int>(threadIdx.x) & 31, warp = static_cast<int>(threadIdx.x) >> 5;
+  const int warps = static_cast<int>(blockDim.x) >> 5;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t slot = static_cast<int64_t>(blockIdx.x) * warps + warp;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * warps;
+  const int rows = slot < c.rows ? static_cast<int>((c.rows - slot + step - 1) / step) : 0;
+  const uint16_t *Y = c.dY + slot * c.lddy, *H = c.H + slot * c.ldh;
+  const uint16_t *B = c.dH ? c.dH + slot * c.lddh : nullptr;
+  uint16_t *X = c.dX + slot * c.lddx;
+  const float *rstd = c.rstd + slot;
+  const int64_t step_y = step * c.lddy, step_h = step * c.ldh;
+  const int64_t step_b = step * c.lddh, step_x = step * c.lddx;
+  const RowWalk k = row_walk(Y, c.cols, t);
+  uint8_t *mine = ring + static_cast<uint32_t>(warp) * kStages * 3 * kSlab + t * 16;
+  // The warp's next row to copy: this lane's units, rstd and extra values.
+  const uint16_t *fy = Y + k.head + 8 * t, *fh = H + k.head + 8 * t;
+  const uint16_t *fb = B ? B + k.head + 8 * t : nullptr;
+  int filled = 0;
+  auto fill = [&](uint32_t stage) {
+    if (filled < rows) {
+      const uint32_t dst = smem_u32(mine) + stage * 3 * kSlab;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (i * 32 + t >= k.units) continue;
+        cp_async_16(dst + i * 512, fy + i * 256, 16);
+        cp_async_16(dst + kSlab + i * 512, fh + i * 256, 16);
+        if (fb) cp_async_16(dst + 2 * kSlab + i * 512, fb + i * 256, 16);
+      }
+      fy += step_y, fh += step_h;
+      if (fb) fb += step_b;
+      ++filled;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int n = 0; n < kStages; ++n) fill(n);
+  GradSums<kBf16, NV> sums;
+  sums.template begin<32>(c, k, row_offset(Y), t);
+  uint32_t stage = 0;
+  const float inv_n = 1.f / static_cast<float>(c.cols);
+  float s = 0.f;
+  uint32_t extra[3] = {0, 0, 0};
+  if (rows > 0) {
+    s = *rstd;
+    extra[0] = load_extra(Y, k), extra[1] = load_extra(H, k), extra[2] = load_extra(B, k);
+  }
+  for (int n = 0; n < rows; ++n) {
+    Y += step_y, H += step_h, rstd += step;
+    if (B) B += step_b;
+    float s2 = 0.f;
+    uint32_t extra2[3] = {0, 0, 0};
+    if (n + 1 < rows) {
+      s2 = *rstd;
+      extra2[0] = load_extra(Y, k), extra2[1] = load_extra(H, k), extra2[2] = load_extra(B, k);
+    }
+    cp_async_wait<kStages - 1>();
+    const uint8_t *row = mine + stage * 3 * kSlab;
+    grad_row<kBf16, 32, NV>(X, k, true, c.dH != nullptr, t, sums, s, inv_n, extra, nullptr,
+                            [&](int a, int i) {
+                              return *reinterpret_cast<const uint4 *>(row + a * kSlab + i * 512);
+                            },
+                            [] {});
+    fill(stage);
+    X += step_x;
+    s = s2;
+    extra[0] = extra2[0], extra[1] = extra2[1], extra[2] = extra2[2];
+    if (++stage == kStages) stage = 0;
+  }
+  if (part == nullptr) return;
+  __syncthreads();  // the ring is free
+  const int pitch = sums_at(c.cols) + 1;
+  float *all = reinterpret_cast<float *>(ring), *own = all + warp * pitch;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (i * 32 + t >= k.units) continue;
+    const int j = k.head + 8 * (i * 32 + t);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      split(sums.dw[i][q], own[sums_at(j + 2 * q)], own[sums_at(j + 2 * q + 1)]);
+  }
+  if (k.extra >= 0) own[sums_at(k.extra)] = sums.dwe;
+  __syncthreads();
+  // Eight loads in flight per thread; the adds are in warp order.
+  const int stride = 32 * warps;
+  for (int j = threadIdx.x; j < c.cols; j += 2 * stride) {
+    const bool two = j + stride < c.cols;
+    const int at0 = sums_at(j), at1 = sums_at(two ? j + stride : j);
+    float v0 = 0.f, v1 = 0.f;
+    for (int w = 0; w < warps; w += 4) {
+      float a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float *from = all + min(w + i, warps - 1) * pitch;
+        a[i] = from[at0], b[i] = from[at1];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (w + i < warps) v0 += a[i], v1 += b[i];
+    }
+    float *out = part + blockIdx.x * static_cast<int64_t>(c.cols) + j;
+    out[0] = v0;
+    if (two) out[stride] = v1;
+  }
+}
+
 // Rows of any length and alignment: one block per group of rows; the partial sums of dw live
 // in the block's partial row in global memory.
 template <bool kBf16>
@@ -716,6 +843,27 @@ cudaError_t launch_grad_ring(const DeviceInfo &dev, const RmsGradCall &c, cudaSt
   });
 }
 
+template <bool kBf16, int NV>
+cudaError_t launch_grad_rows(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_t stream) {
+  auto kern = rms_norm_grad_rows_kernel<kBf16, NV>;
+  // As few rows per warp as kGradRowWarps warps per SM allow, then as few warps as
+  // that takes. A warp's rows are a multiple of 8 apart, or it has one row.
+  const int sms = std::max(dev.sm_count / 8 * 8, 8);
+  const int per_warp = (c.rows - 1) / (sms * kGradRowWarps<NV>) + 1;
+  int warps = (c.rows - 1) / (sms * per_warp) + 1;
+  // One row each: at least 8 warps a block, for fewer partial rows and more threads
+  // to add them (333 x 1001 7.0 -> 6.4 us).
+  if (per_warp == 1) warps = std::max(warps, 8);
+  const int64_t blocks = per_warp > 1 ? sms : (c.rows - 1) / warps + 1;
+  const int smem = std::max(warps * kGradRowStages<NV> * 3 * NV * 512,
+                            warps * (c.cols + c.cols / 32 + 1) * 4);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem, dev.device);
+  if (e != cudaSuccess) return e;
+  return with_partials(dev, c, blocks, stream, [&](float *part) {
+    return launch_pdl(kern, static_cast<unsigned>(blocks), 32u * warps, smem, stream, c, part);
+  });
+}
+
 template <bool kBf16>
 cudaError_t launch_grad_long(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_t stream) {
   const int blocks = std::min(c.rows, 2 * dev.sm_count);
@@ -732,11 +880,23 @@ cudaError_t launch_grad(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_
     return p == nullptr || ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(c.dY)) % 16 == 0 &&
                             (ld - c.lddy) % 8 == 0);
   };
-  if (units <= 32) return launch_grad_warp<kBf16, 1>(dev, c, stream);
-  if (units <= 64) return launch_grad_warp<kBf16, 2>(dev, c, stream);
-  if (!alike(c.H, c.ldh) || !alike(c.dH, c.lddh) || !alike(c.dX, c.lddx))
+  const bool same = alike(c.H, c.ldh) && alike(c.dH, c.lddh) && alike(c.dX, c.lddx);
+  if (!same) {
+    if (units <= 32) return launch_grad_warp<kBf16, 1>(dev, c, stream);
+    if (units <= 64) return launch_grad_warp<kBf16, 2>(dev, c, stream);
     return launch_grad_long<kBf16>(dev, c, stream);
+  }
+  // A warp per row, or a block per row? The warp form keeps more rows in flight
+  // (32768 x 1024 47.5 against 62.3 us, 32768 x 1536 65.3 against 85.7, 8192 x 512
+  // 10.1 against 12.4 for a warp per row without the copies ahead); the block form
+  // has the shorter row where there are few (256 x 1024 4.7 against 5.2 us but
+  // 400 x 1024 6.2 against 5.5; 256 x 2048 5.4 against 7.4, 1300 x 2048 9.1 against
+  // 10.8, 2048 x 2048 11.2 against 11.1).
+  if (units <= 32) return launch_grad_rows<kBf16, 1>(dev, c, stream);
+  if (units <= 64) return launch_grad_rows<kBf16, 2>(dev, c, stream);
+  if (units <= 128 && c.rows > 2 * dev.sm_count) return launch_grad_rows<kBf16, 4>(dev, c, stream);
   if (units <= 128) return launch_grad_ring<kBf16, 128, 1>(dev, c, stream);
+  if (units <= 256 && c.rows > 10 * dev.sm_count) return launch_grad_rows<kBf16, 8>(dev, c, stream);
   if (units <= 256) return launch_grad_ring<kBf16, 128>(dev, c, stream);
   if (units <= 512) return launch_grad_ring<kBf16, 256>(dev, c, stream);
   if (units <= 1024) return launch_grad_ring<kBf16, 512>(dev, c, stream);

@@ -122,6 +122,33 @@ def test_grad(gemm_mod, shape, dtype):
     dW.check_guards()
 
 
+@pytest.mark.parametrize("dtype", DTYPES.values(), ids=list(DTYPES))
+@pytest.mark.parametrize("shape", [(6001, 64), (5000, 255), (2433, 500), (4867, 512), (305, 1001),
+                                   (2600, 1000), (4870, 1024), (1521, 1500), (2600, 2047),
+                                   (1530, 2055)], ids=lambda s: "x".join(map(str, s)))
+def test_grad_of_several_rows_per_warp(gemm_mod, shape, dtype):
+    """Rows enough that a warp walks over several, with rings shorter and longer
+    than its rows; dX in place of dY, as dY's and dh's rows are walked ahead."""
+    m, n = shape
+    W, D = vector(n, dtype, n), Out(1, n, dtype)
+    H, dH = normal(shape, dtype, m, 2.0), normal(shape, dtype, m + 1)
+    X = Out(m, n, dtype)
+    X.t.copy_(normal(shape, dtype, m + 2))
+    y64, h64, d64, w64 = L.to64(X.t), L.to64(H), L.to64(dH), L.to64(W)
+    rstd = torch.from_numpy(1 / np.sqrt((h64 * h64).mean(1) + EPS)).float().cuda()
+    s64 = L.to64(rstd)
+    gemm_mod.rms_norm_grad(X.t, H, rstd, X.t, weight=W, dh=dH, dweight=D.t[0])
+    torch.cuda.synchronize()
+    dx, dw = L.rms_norm_grad(y64, h64, s64, w64, d64)
+    nrm, g = h64 * s64[:, None], np.abs(y64 * w64)
+    terms = s64[:, None] * (g + np.abs(nrm) * (g * np.abs(nrm)).mean(1, keepdims=True)) + np.abs(d64)
+    assert_close(L.to64(X.t), dx, rounded_bound(dx, 2.0 ** -17 * terms, dtype), "dX")
+    ew = (m + 20) * 2.0 ** -24 * np.abs(y64 * nrm).sum(0)
+    assert_close(L.to64(D.t[0]), dw, rounded_bound(dw, ew, dtype), "dW")
+    X.check_guards()
+    D.check_guards()
+
+
 def test_in_place(gemm_mod):
     for n in (1000, 1001, 20000):
         X, R = normal((6, n), torch.bfloat16, 1), normal((6, n), torch.bfloat16, 2)
