@@ -12,11 +12,12 @@
 //
 //     dx_j = s (g_j - n_j mean_k(g_k n_k)) + dh_j,    dw_j = sum_i dy_ij n_ij
 //
-// Both are bound by memory: every value is read once, kept in registers and
-// written once. A row belongs to one block, or (short rows) to one warp of a
-// block. The largest |h w|
-// is reduced together with the sum of squares, so the 8-bit form has one block
-// reduction too: max |y| = s max |h w| up to rounding.
+// Both are bound by memory: every value is read once and written once. A row
+// belongs to one block, or to one warp of a block; while few rows are to be done
+// a thread holds its values in registers and a block ends with its row, with many
+// rows blocks walk over them with the next rows' copies in flight. The largest
+// |h w| is reduced together with the sum of squares, so the 8-bit form has one
+// block reduction too: max |y| = s max |h w| up to rounding.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -36,12 +37,13 @@ constexpr float kE4m3Max = 448.f;
 // must not overflow.
 constexpr float kE4m3Least = 1e-30f;
 
-// 1 / scale of a row, and its scale; NaN and infinity stay visible in both the
-// scale and the values (0 * inf and NaN).
-__device__ __forceinline__ void e4m3_scale(float most, float &scale, float &inv) {
-  const bool zeros = most < kE4m3Least;
-  scale = zeros ? 0.f : most / kE4m3Max;
-  inv = zeros ? 0.f : kE4m3Max / most;
+// The scale of a row whose largest |y| is `most`, and its inverse; NaN and infinity
+// stay visible in both the scale and the values (0 * inf and NaN).
+__device__ __forceinline__ float e4m3_scale(float most) {
+  return most < kE4m3Least ? 0.f : most / kE4m3Max;
+}
+__device__ __forceinline__ float e4m3_inverse(float most) {
+  return most < kE4m3Least ? 0.f : kE4m3Max / most;
 }
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
@@ -119,10 +121,9 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 template <int T>
 __device__ __forceinline__ void row_reduce(float &a, float &m, float2 *red) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  }
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  // m >= 0 or NaN, whose bits order like its values (NaN last).
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
   if constexpr (T > 32) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, m);
     __syncthreads();
@@ -147,15 +148,42 @@ __device__ __forceinline__ float row_sum(float a, float *red) {
     __syncthreads();
     a = 0.f;
 #pragma unroll
-    for (int i = 0; i < T / 32; i += 4) {
-      const float4 v = *reinterpret_cast<const float4 *>(red + i);
+    for (int i = 0; i < T / 32; i += 2) {
+      const float2 v = *reinterpret_cast<const float2 *>(red + i);
       a += v.x;
       a += v.y;
-      a += v.z;
-      a += v.w;
     }
   }
   return a;
+}
+
+// Writes a row's units of 8 8-bit values where they lie `head` bytes off Y's 8-byte
+// boundaries: the aligned 8 bytes number a are the last `head` values of unit
+// a - 1 and the first 8 - head of unit a. unit(u): unit u, behind a barrier.
+// (16384 rows of 7777 values 265 -> 204 us against byte stores, of 4095 102 -> 91;
+// in the one-row form of shorter rows the byte stores are the faster ones, 26
+// against 29 us at 1001.)
+template <typename Unit>
+__device__ __forceinline__ void store_shifted(uint8_t *Y, const RowWalk &k, int t, int threads,
+                                              Unit &&unit) {
+  const int sh = 8 * k.head;
+  for (int a = t; a <= k.units; a += threads) {
+    const uint64_t below = a > 0 ? unit(a - 1) : 0, above = a < k.units ? unit(a) : 0;
+    const uint64_t w = (below >> (64 - sh)) | (above << sh);
+    if (a > 0 && a < k.units) {
+      *reinterpret_cast<uint64_t *>(Y + 8 * a) = w;
+    } else {
+      const int e0 = a == 0 ? k.head : 0, e1 = a == 0 ? 8 : k.head;
+      for (int e = e0; e < e1; ++e) Y[8 * a + e] = static_cast<uint8_t>(w >> (8 * e));
+    }
+  }
+}
+
+// The gain's packed values, widened again for every row: hoisted out of the row
+// loop, the widened ones would take twice the registers and spill.
+__device__ __forceinline__ uint4 per_row(uint4 w) {
+  asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w));
+  return w;
 }
 
 // T threads per row, at most NV units per thread and array: rows of up to T * NV
@@ -210,9 +238,8 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) rms_norm_kernel(const RmsCa
   const float s = rsqrtf(sum / static_cast<float>(cols) + c.eps);
   if (t == 0 && c.rstd) c.rstd[r] = s;
   if (c.scale) {
-    float scale, inv;
-    e4m3_scale(top * s, scale, inv);
-    if (t == 0) c.scale[r] = scale;
+    const float inv = e4m3_inverse(top * s);
+    if (t == 0) c.scale[r] = e4m3_scale(top * s);
     uint8_t *Y = static_cast<uint8_t *>(c.Y) + r * c.ldy;
     const uint32_t lead = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(Y) & 7);
 #pragma unroll
@@ -235,23 +262,8 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) rms_norm_kernel(const RmsCa
       }
     }
     if (T >= 256 && lead == 0 && k.head != 0 && k.units > 0) {
-      // Units of 8 values lie `head` bytes off Y's 8-byte boundaries: the aligned
-      // 8 bytes number a are the last `head` values of unit a - 1 and the first
-      // 8 - head of unit a, put together from shared memory (16384 rows of 7777
-      // values 265 -> 204 us, of 4095 102 -> 91; for shorter rows the byte stores
-      // are the faster ones, 26 against 29 us at 1001).
       __syncthreads();
-      const int sh = 8 * k.head;
-      for (int a = t; a <= k.units; a += T) {
-        const uint64_t below = a > 0 ? packed[a - 1] : 0, above = a < k.units ? packed[a] : 0;
-        const uint64_t w = (below >> (64 - sh)) | (above << sh);
-        if (a > 0 && a < k.units) {
-          *reinterpret_cast<uint64_t *>(Y + 8 * a) = w;
-        } else {
-          const int e0 = a == 0 ? k.head : 0, e1 = a == 0 ? 8 : k.head;
-          for (int e = e0; e < e1; ++e) Y[8 * a + e] = static_cast<uint8_t>(w >> (8 * e));
-        }
-      }
+      store_shifted(Y, k, t, T, [&](int u) { return packed[u]; });
     }
     if (k.extra >= 0) Y[k.extra] = static_cast<uint8_t>(e4m3x2(ge * s * inv, 0.f));
   } else {
@@ -264,6 +276,235 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) rms_norm_kernel(const RmsCa
       store_unit(Y, k, i * T + t, same, unit_pack<kBf16>(g[i]));
     }
     if (k.extra >= 0) Y[k.extra] = to16<kBf16>(ge * s);
+  }
+}
+
+// A lane's extra value of a coming row, copied to shared memory asynchronously like
+// the units: a plain load in flight shares a scoreboard with the shared-memory loads
+// and stalls them (16384 x 5279 88 -> 67 us). The copy takes the aligned pair of
+// values that the extra one is in; past the row's end nothing is read, before its
+// start the end of the previous row (`first`: there is none).
+__device__ __forceinline__ void copy_extra(uint32_t dst, const uint16_t *row, const RowWalk &k,
+                                           int cols, bool first) {
+  if (k.extra < 0) return;
+  const uint16_t *p = row + k.extra;
+  const uint32_t odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) >> 1) & 1u;
+  if (first && odd && k.extra == 0) {
+    asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(dst + 2), "h"(*p) : "memory");
+  } else {
+    cp_async_4(dst, p - odd, !odd && k.extra + 1 == cols ? 2u : 4u);
+  }
+}
+// Where in its four bytes the extra value is.
+__device__ __forceinline__ uint32_t extra_at(const void *row, const RowWalk &k) {
+  return static_cast<uint32_t>((reinterpret_cast<uintptr_t>(row) >> 1) + (k.extra & 1)) & 1u;
+}
+
+// Many rows: blocks walk rows blockIdx.x, + gridDim.x, ... (T = 32: one warp per
+// row, the block's warps on rows of their own), and every thread copies its own
+// units of the next rows into shared memory, `stages` rows deep, so that memory is
+// busy during the reductions and the stores and no thread waits for another's
+// copies. X and R must be aligned alike; the stride between a block's rows is a
+// multiple of 8 rows, so that all have the same alignment and a thread the same
+// columns of W in each.
+//
+// 512 threads per SM with 4 units of 8 values each: what a row costs a thread beside
+// its values (the reduction, the scale, addresses) is as much as some 20 values, and
+// 1024 threads with 2 units took 94 us, not 63, at 16384 x 6144 and 128, not 76, with
+// 8-bit output.
+constexpr int kNormThreads = 512, kNormUnits = 4;
+
+template <bool kBf16, bool kOut8, int T>
+__global__ void __launch_bounds__(T > 32 ? T : kNormThreads, T > 32 ? kNormThreads / T : 1)
+    rms_norm_ring_kernel(const RmsCall c, int stages) {
+  constexpr int NV = kNormUnits;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(16) float2 red[2][T / 32];
+  constexpr uint32_t kSlab = NV * T * 16;  // one matrix's row, unit u at 16 u
+  const int t = static_cast<int>(threadIdx.x) % T, group = static_cast<int>(threadIdx.x) / T;
+  const int groups = T > 32 ? 1 : static_cast<int>(blockDim.x) / T;
+  auto sync = [] {
+    if constexpr (T > 32) {
+      __syncthreads();
+    } else {
+      __syncwarp();
+    }
+  };
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t slot = static_cast<int64_t>(blockIdx.x) * groups + group;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const int rows = slot < c.rows ? static_cast<int>((c.rows - slot + step - 1) / step) : 0;
+  if (rows == 0) return;  // a whole group
+  const int mats = c.R ? 2 : 1;
+  const uint16_t *X = c.X + slot * c.ldx, *R = c.R ? c.R + slot * c.ldr : nullptr;
+  uint16_t *H = c.H ? c.H + slot * c.ldh : nullptr;
+  constexpr int kSize = kOut8 ? 1 : 2;
+  uint8_t *out = static_cast<uint8_t *>(c.Y) + slot * c.ldy * kSize;
+  float *rstd = c.rstd ? c.rstd + slot : nullptr, *scales = kOut8 ? c.scale + slot : nullptr;
+  const int64_t step_x = step * c.ldx, step_r = step * c.ldr, step_h = step * c.ldh;
+  const int64_t step_y = step * c.ldy * kSize;
+  const int off = row_offset(X);
+  const RowWalk k = row_walk(X, c.cols, t);
+  const bool ragged = c.cols != 8 * k.units;  // rows with a head or a tail
+  const float inv_n = 1.f / static_cast<float>(c.cols);
+  uint8_t *mine = ring + static_cast<uint32_t>(group * stages * mats) * kSlab;
+  // The extra values: 16 lanes' words per row and matrix, behind the units.
+  uint8_t *side = ring + static_cast<uint32_t>(groups * stages * mats) * kSlab +
+                  static_cast<uint32_t>(group * stages * mats) * 64u + t * 4;
+  const uint32_t side_at = 2 * extra_at(X, k);
+  const uint16_t *fx = X, *fr = R;
+  const int first_unit = k.head + 8 * t;
+  int filled = 0;
+  auto fill = [&](int stage) {
+    if (filled < rows) {
+      const uint32_t dst = smem_u32(mine) + static_cast<uint32_t>(stage * mats) * kSlab + t * 16;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (i * T + t >= k.units) continue;
+        cp_async_16(dst + i * T * 16, fx + first_unit + i * T * 8, 16);
+        if (fr) cp_async_16(dst + kSlab + i * T * 16, fr + first_unit + i * T * 8, 16);
+      }
+      if (ragged) {
+        const uint32_t to = smem_u32(side) + static_cast<uint32_t>(stage * mats) * 64u;
+        const bool top_row = slot == 0 && filled == 0;
+        copy_extra(to, fx, k, c.cols, top_row);
+        if (fr) copy_extra(to + 64, fr, k, c.cols, top_row);
+      }
+      fx += step_x;
+      if (fr) fr += step_r;
+      ++filled;
+    }
+    cp_async_commit();
+  };
+  for (int n = 0; n < stages; ++n) fill(n);
+  const uint32_t one = kBf16 ? 0x3f803f80u : 0x3c003c00u;  // no gain: ones
+  uint4 w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    w[i] = c.W ? load_unit(c.W, k, i * T + t, row_offset(c.W) == off)
+               : make_uint4(one, one, one, one);
+  const float we = c.W ? from16<kBf16>(load_extra(c.W, k)) : 1.f;
+  int stage = 0;
+  for (int n = 0; n < rows; ++n) {
+    const bool same_h = row_offset(H) == off;
+    switch (stages) {  // all but the newest stages - 1 rows are there
+      case 2: cp_async_wait<1>(); break;
+      case 3: cp_async_wait<2>(); break;
+      default: cp_async_wait<3>(); break;
+    }
+    uint8_t *row = mine + static_cast<uint32_t>(stage * mats) * kSlab;
+    float he = 0.f, ge = 0.f;
+    if (ragged && k.extra >= 0) {
+      const uint8_t *from = side + static_cast<uint32_t>(stage * mats) * 64u + side_at;
+      he = from16<kBf16>(*reinterpret_cast<const uint16_t *>(from));
+      if (R) he += from16<kBf16>(*reinterpret_cast<const uint16_t *>(from + 64));
+      ge = he * we;
+    }
+    F2 g[NV][4], sums = f2(0.f);
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int u = i * T + t;
+      if (u >= k.units) continue;
+      const uint4 x = *reinterpret_cast<const uint4 *>(row + 16 * u), wi = per_row(w[i]);
+      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, ww[4] = {wi.x, wi.y, wi.z, wi.w};
+      F2 h[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) h[q] = unpack2<kBf16>(xw[q]);
+      if (R) {
+        const uint4 b = *reinterpret_cast<const uint4 *>(row + kSlab + 16 * u);
+        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[q] = add2(h[q], unpack2<kBf16>(bw[q]));
+      }
+      if (H)
+        store_unit(H, k, u, same_h, make_uint4(pack2<kBf16>(h[0]), pack2<kBf16>(h[1]),
+                                               pack2<kBf16>(h[2]), pack2<kBf16>(h[3])));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        sums = fma2(h[q], h[q], sums);
+        g[i][q] = mul2(h[q], unpack2<kBf16>(ww[q]));
+        if constexpr (kOut8) {
+          float a, b;
+          split(g[i][q], a, b);
+          top = max_nan(top, max_nan(fabsf(a), fabsf(b)));
+        }
+      }
+    }
+    float sum, sum1;
+    split(sums, sum, sum1);
+    sum += sum1;
+    if (ragged && k.extra >= 0) {
+      sum = fmaf(he, he, sum);
+      if (kOut8) top = max_nan(top, fabsf(ge));
+      if (H) H[k.extra] = to16<kBf16>(he);
+    }
+    if constexpr (kOut8) {
+      row_reduce<T>(sum, top, red[n & 1]);
+    } else {
+      sum = row_sum<T>(sum, reinterpret_cast<float *>(red[n & 1]));
+    }
+    const float s = rsqrtf(sum * inv_n + c.eps);
+    if (t == 0 && rstd) rstd[0] = s;
+    const F2 s2 = f2(s);
+    if constexpr (kOut8) {
+      const float inv = e4m3_inverse(top * s);
+      if (t == 0) scales[0] = e4m3_scale(top * s);
+      uint8_t *Y = out;
+      const uint32_t lead = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(Y) & 7);
+      const bool whole = ((lead + k.head) & 7) == 0, shifted = !whole && lead == 0 && k.units > 0;
+      const F2 inv2 = f2(inv);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int u = i * T + t;
+        if (u >= k.units) continue;
+        uint32_t b[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float y0, y1;
+          split(mul2(mul2(g[i][q], s2), inv2), y0, y1);
+          b[q] = e4m3x2(y0, y1);
+        }
+        const uint64_t v =
+            static_cast<uint64_t>(b[2] | (b[3] << 16)) << 32 | (b[0] | (b[1] << 16));
+        uint8_t *p = Y + k.head + 8 * u;
+        if (whole) {
+          *reinterpret_cast<uint64_t *>(p) = v;
+        } else if (shifted) {
+          *reinterpret_cast<uint64_t *>(row + 16 * u) = v;  // in place of X's unit
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = static_cast<uint8_t>(v >> (8 * e));
+        }
+      }
+      if (k.extra >= 0) Y[k.extra] = static_cast<uint8_t>(e4m3x2(ge * s * inv, 0.f));
+      if (shifted) {
+        sync();
+        store_shifted(Y, k, t, T, [&](int u) {
+          return *reinterpret_cast<const uint64_t *>(row + 16 * u);
+        });
+        sync();  // before the next row is copied over the units
+      }
+    } else {
+      uint16_t *Y = reinterpret_cast<uint16_t *>(out);
+      const bool same_y = row_offset(Y) == off;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int u = i * T + t;
+        if (u >= k.units) continue;
+        store_unit(Y, k, u, same_y,
+                   make_uint4(pack2<kBf16>(mul2(g[i][0], s2)), pack2<kBf16>(mul2(g[i][1], s2)),
+                              pack2<kBf16>(mul2(g[i][2], s2)), pack2<kBf16>(mul2(g[i][3], s2))));
+      }
+      if (k.extra >= 0) Y[k.extra] = to16<kBf16>(ge * s);
+    }
+    fill(stage);
+    if (++stage == stages) stage = 0;
+    if (H) H += step_h;
+    out += step_y;
+    if (rstd) rstd += step;
+    if (kOut8) scales += step;
   }
 }
 
@@ -286,9 +527,8 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const RmsCall c) {
   row_reduce<1024>(sum, top, red);
   const float s = rsqrtf(sum / static_cast<float>(c.cols) + c.eps);
   if (threadIdx.x == 0 && c.rstd) c.rstd[r] = s;
-  float scale, inv;
-  e4m3_scale(top * s, scale, inv);
-  if (threadIdx.x == 0 && c.scale) c.scale[r] = scale;
+  const float inv = e4m3_inverse(top * s);
+  if (threadIdx.x == 0 && c.scale) c.scale[r] = e4m3_scale(top * s);
   for (int64_t j = threadIdx.x; j < c.cols; j += 1024) {
     float h = from16<kBf16>(X[j]);
     if (R) h += from16<kBf16>(R[j]);
@@ -341,13 +581,6 @@ struct GradSums {
     if (k.extra >= 0) out[k.extra] = dwe;
   }
 };
-
-// The gain's packed values, widened again for every row: hoisted out of the row
-// loop, the widened ones would take twice the registers and spill.
-__device__ __forceinline__ uint4 per_row(uint4 w) {
-  asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w));
-  return w;
-}
 
 // One row by T threads. get(a, i): packed unit i of this thread of matrix a (0:
 // dY, 1: H, 2: dH), called for units inside the row; extra[a]: its extra value.
@@ -764,9 +997,57 @@ cudaError_t launch_pdl(void (*kern)(P...), unsigned grid, unsigned block, int sm
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+template <bool kBf16, int T>
+cudaError_t launch_norm_ring(const DeviceInfo &dev, const RmsCall &c, cudaStream_t stream) {
+  auto kern = c.scale ? rms_norm_ring_kernel<kBf16, true, T>
+                      : rms_norm_ring_kernel<kBf16, false, T>;
+  const int mats = c.R ? 2 : 1;
+  const int sms = std::max(dev.sm_count / 8 * 8, 8);
+  int threads = T;
+  int64_t blocks;
+  if (T > 32) {
+    blocks = std::min(c.rows, sms * (kNormThreads / T));
+  } else {
+    const int most = kNormThreads / 32;
+    const int per_warp = (c.rows - 1) / (sms * most) + 1, warps = (c.rows - 1) / (sms * per_warp) + 1;
+    threads = 32 * warps;
+    blocks = per_warp > 1 ? sms : (c.rows - 1) / warps + 1;
+  }
+  // Rows in flight or in work: about 64 KB per SM. (16384 x 8192 without a residual:
+  // 64 KB 83 us, 192 KB 94 us; 16384 x 5280 with one: 42 KB 130 us, 84 KB 115 us,
+  // 126 KB 125 us.)
+  const int layer = kNormThreads / T * mats * c.cols * 2;
+  const int stages = std::min(std::max((65536 + layer / 2) / layer, 2), 4);
+  const int smem = threads / T * stages * mats * (kNormUnits * T * 16 + 64);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem, dev.device);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, static_cast<unsigned>(blocks), static_cast<unsigned>(threads), smem,
+                    stream, c, stages);
+}
+
 template <bool kBf16>
-cudaError_t launch_norm(const RmsCall &c, cudaStream_t stream) {
+cudaError_t launch_norm(const DeviceInfo &dev, const RmsCall &c, cudaStream_t stream) {
   const int units = c.cols / 8;  // at most, whatever the alignment
+  const bool alike =
+      c.R == nullptr || ((reinterpret_cast<uintptr_t>(c.R) ^ reinterpret_cast<uintptr_t>(c.X)) % 16 == 0 &&
+                         (c.ldr - c.ldx) % 8 == 0);
+  // Blocks that walk rows, or a block per row? A block per row while about all rows
+  // are in residence at once (1024 x 4096: 5.2 against 4.4 us, but 304 x 4096 2.3
+  // against 2.8), and for rows of up to 512 columns (16384 x 512 8.0 against 7.7).
+  // With a residual, whose reads and writes keep memory busy enough, also where the
+  // row fills most of the block (16384 rows: 2048 40 against 45 us, 4096 78 against
+  // 87; but 2560 58 against 54, 5280 139 against 115 and 12288, of half as many
+  // rows, 185 against 131).
+  const int slots = units <= 128 ? 128 : units <= 256 ? 256 : 512;
+  const bool full = units > 128 && units <= 512 && 4 * units > 3 * slots;
+  if (alike && units > 64 && static_cast<int64_t>(c.rows) * c.cols > 10240LL * dev.sm_count &&
+      !(c.R != nullptr && full)) {
+    if (units <= 128) return launch_norm_ring<kBf16, 32>(dev, c, stream);
+    if (units <= 256) return launch_norm_ring<kBf16, 64>(dev, c, stream);
+    if (units <= 512) return launch_norm_ring<kBf16, 128>(dev, c, stream);
+    if (units <= 1024) return launch_norm_ring<kBf16, 256>(dev, c, stream);
+    if (units <= 2048) return launch_norm_ring<kBf16, 512>(dev, c, stream);
+  }
   const unsigned rows = static_cast<unsigned>(c.rows);
   if (units <= 32) return launch_pdl(rms_norm_kernel<kBf16, 32, 1>, (rows + 3) / 4, 128, 0, stream, c);
   if (units <= 64) return launch_pdl(rms_norm_kernel<kBf16, 32, 2>, (rows + 3) / 4, 128, 0, stream, c);
@@ -907,8 +1188,7 @@ cudaError_t launch_grad(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_
 }  // namespace
 
 cudaError_t launch_rms_norm(const DeviceInfo &dev, const RmsCall &c, cudaStream_t stream) {
-  (void)dev;
-  return c.bf16 ? launch_norm<true>(c, stream) : launch_norm<false>(c, stream);
+  return c.bf16 ? launch_norm<true>(dev, c, stream) : launch_norm<false>(dev, c, stream);
 }
 
 cudaError_t launch_rms_norm_grad(const DeviceInfo &dev, const RmsGradCall &c,

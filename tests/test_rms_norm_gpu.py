@@ -72,6 +72,51 @@ def test_norm(gemm_mod, shape, dtype, out8):
     Y.check_guards()
 
 
+@pytest.mark.parametrize("residual", [False, True], ids=["plain", "residual"])
+@pytest.mark.parametrize("out8", [False, True], ids=["out16", "e4m3"])
+@pytest.mark.parametrize("shape", [(2600, 1000), (1601, 1031), (1000, 2047), (700, 2500), (500, 4095),
+                                   (400, 5280), (250, 8191), (200, 10001), (160, 16384)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_norm_of_many_rows(gemm_mod, shape, out8, residual):
+    """Rows enough for blocks that walk over several; X one value off a 16-byte
+    boundary, 8-bit rows padded, 16-bit Y in place of X."""
+    m, n = shape
+    dtype = DTYPES["f16" if residual == out8 else "bf16"]
+    buf = torch.full((m * n + 16,), float("nan"), device="cuda", dtype=dtype)
+    X = torch.as_strided(buf, (m, n), (n, 1), 1)
+    X.copy_(normal(shape, dtype, n))
+    R, H = None, None
+    if residual:  # aligned as X is
+        R = torch.as_strided(torch.empty_like(buf), (m, n), (n, 1), 1)
+        R.copy_(normal(shape, dtype, n + 1, 2.0))
+        H = Out(m, n, dtype, pad=3)
+    W = vector(n, dtype, n)
+    x64, r64 = L.to64(X), L.to64(R) if residual else None
+    want = X.float() + R.float() if residual else None
+    Y = Out(m, n, torch.float8_e4m3fn, pad=-n % 16) if out8 else None
+    rstd = torch.empty(m, device="cuda")
+    scale = torch.empty(m, device="cuda") if out8 else None
+    gemm_mod.rms_norm(X, Y.t if out8 else X, weight=W, residual=R, h=H.t if H else None,
+                      scale=scale, rstd=rstd, eps=EPS)
+    torch.cuda.synchronize()
+    y, _, s = L.rms_norm(x64, L.to64(W), r64, EPS)
+    assert_close(L.to64(rstd), s, 2.0 ** -18 * s, "rstd")
+    if residual:
+        assert torch.equal(H.t, want.to(dtype))
+        H.check_guards()
+    if out8:
+        q, qs = L.quantise_e4m3(y)
+        assert_close(L.to64(scale), qs, 2.0 ** -17 * qs, "scale")
+        step = qs[:, None] * 2.0 ** -10
+        assert_close(L.to64(Y.t) * L.to64(scale)[:, None], y,
+                     (2.0 ** -4 + 2.0 ** -16) * np.abs(y) + step * (1 + 2.0 ** -16), "Y")
+        assert (L.to64(Y.t) == q).mean() >= 0.99
+        Y.check_guards()
+    else:
+        assert_close(L.to64(X), y, rounded_bound(y, 2.0 ** -17 * np.abs(y), dtype), "Y")
+    assert torch.isnan(buf[0]) and torch.isnan(buf[m * n + 1:]).all()
+
+
 @pytest.mark.parametrize("n", [1, 3, 7, 9, 13, 101, 1001, 2049, 2056, 4095, 6001, 7777, 16383])
 def test_8_bit_rows_padded_for_the_product(gemm_mod, n):
     """Y in rows of whole 16-byte units, X in packed rows: the two are aligned
