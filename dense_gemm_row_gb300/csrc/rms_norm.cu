@@ -117,13 +117,17 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 }
 
 // The sum of a and the largest of m over the T threads of a row (a whole block
-// in warps, or one warp), in one fixed order. red: one slot pair per warp.
+// in warps, one warp or half of one), in one fixed order. red: one slot pair per
+// warp.
 template <int T>
 __device__ __forceinline__ void row_reduce(float &a, float &m, float2 *red) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  for (int o = T < 32 ? T / 2 : 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (T < 32) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
   // m >= 0 or NaN, whose bits order like its values (NaN last).
-  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  if (T >= 32) m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
   if constexpr (T > 32) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, m);
     __syncthreads();
@@ -190,19 +194,22 @@ __device__ __forceinline__ uint4 per_row(uint4 w) {
 // units. Blocks of max(T, 128) threads.
 template <bool kBf16, int T, int NV>
 __global__ void __launch_bounds__(T < 128 ? 128 : T) rms_norm_kernel(const RmsCall c) {
-  __shared__ float2 red[T / 32];
+  __shared__ float2 red[T < 32 ? 1 : T / 32];
   __shared__ uint64_t packed[T < 256 ? 1 : T * NV];  // a row's 8-bit values
   constexpr int kRows = T < 128 ? 128 / T : 1;
   const int row = static_cast<int>(blockIdx.x) * kRows + static_cast<int>(threadIdx.x) / T;
   const int t = static_cast<int>(threadIdx.x) % T;
   grid_dependency_wait();
   grid_launch_dependents();
-  if (kRows > 1 && row >= c.rows) return;  // whole warps; no block barrier follows
-  const int64_t r = row;
+  if (T == 32 && row >= c.rows) return;  // whole warps; no block barrier follows
+  // Half warps past the last row take part in their warp's reductions.
+  const bool live = T >= 32 || row < c.rows;
+  const int64_t r = live ? row : c.rows - 1;
   const uint16_t *X = c.X + r * c.ldx, *R = c.R ? c.R + r * c.ldr : nullptr;
   uint16_t *H = c.H ? c.H + r * c.ldh : nullptr;
   const int cols = c.cols, off = row_offset(X);
-  const RowWalk k = row_walk(X, cols, t);
+  RowWalk k = row_walk(X, cols, t);
+  if (!live) k.units = 0, k.extra = -1;
   const bool same_r = row_offset(R) == off, same_w = row_offset(c.W) == off;
   uint4 x[NV], q[NV], w[NV];
 #pragma unroll
@@ -236,10 +243,10 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) rms_norm_kernel(const RmsCa
   if (H && k.extra >= 0) H[k.extra] = to16<kBf16>(he);
   row_reduce<T>(sum, top, red);
   const float s = rsqrtf(sum / static_cast<float>(cols) + c.eps);
-  if (t == 0 && c.rstd) c.rstd[r] = s;
+  if (t == 0 && live && c.rstd) c.rstd[r] = s;
   if (c.scale) {
     const float inv = e4m3_inverse(top * s);
-    if (t == 0) c.scale[r] = e4m3_scale(top * s);
+    if (t == 0 && live) c.scale[r] = e4m3_scale(top * s);
     uint8_t *Y = static_cast<uint8_t *>(c.Y) + r * c.ldy;
     const uint32_t lead = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(Y) & 7);
 #pragma unroll
@@ -1049,7 +1056,8 @@ cudaError_t launch_norm(const DeviceInfo &dev, const RmsCall &c, cudaStream_t st
     if (units <= 2048) return launch_norm_ring<kBf16, 512>(dev, c, stream);
   }
   const unsigned rows = static_cast<unsigned>(c.rows);
-  if (units <= 32) return launch_pdl(rms_norm_kernel<kBf16, 32, 1>, (rows + 3) / 4, 128, 0, stream, c);
+  if (units <= 16) return launch_pdl(rms_norm_kernel<kBf16, 16, 1>, (rows + 7) / 8, 128, 0, stream, c);
+  if (units <= 32) return launch_pdl(rms_norm_kernel<kBf16, 16, 2>, (rows + 7) / 8, 128, 0, stream, c);
   if (units <= 64) return launch_pdl(rms_norm_kernel<kBf16, 32, 2>, (rows + 3) / 4, 128, 0, stream, c);
   if (units <= 128) return launch_pdl(rms_norm_kernel<kBf16, 128, 1>, rows, 128, 0, stream, c);
   if (units <= 256) return launch_pdl(rms_norm_kernel<kBf16, 128, 2>, rows, 128, 0, stream, c);
