@@ -168,8 +168,8 @@ def test_grad(gemm_mod, shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES.values(), ids=list(DTYPES))
-@pytest.mark.parametrize("shape", [(6001, 64), (5000, 255), (2433, 500), (4867, 512), (305, 1001),
-                                   (2600, 1000), (4870, 1024), (1521, 1500), (2600, 2047),
+@pytest.mark.parametrize("shape", [(6001, 64), (4864, 255), (2433, 500), (4864, 519), (305, 1001),
+                                   (2600, 1000), (4864, 1024), (1521, 1500), (2432, 2047),
                                    (1530, 2055)], ids=lambda s: "x".join(map(str, s)))
 def test_grad_of_several_rows_per_warp(gemm_mod, shape, dtype):
     """Rows enough that a warp walks over several, with rings shorter and longer
