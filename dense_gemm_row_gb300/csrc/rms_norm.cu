@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) rms_norm_kernel(const RmsCa
 
 // A lane's extra value of a coming row, copied to shared memory asynchronously like
 // the units: a plain load in flight shares a scoreboard with the shared-memory loads
-// and stalls them (16384 x 5279 88 -> 67 us). The copy takes the aligned pair of
+// and stalls them (16384 x 5279 88 -> 69 us). The copy takes the aligned pair of
 // values that the extra one is in; past the row's end nothing is read, before its
 // start the end of the previous row (`first`: there is none).
 __device__ __forceinline__ void copy_extra(uint32_t dst, const uint16_t *row, const RowWalk &k,
@@ -317,7 +317,7 @@ __device__ __forceinline__ uint32_t extra_at(const void *row, const RowWalk &k) 
 //
 // 512 threads per SM with 4 units of 8 values each: what a row costs a thread beside
 // its values (the reduction, the scale, addresses) is as much as some 20 values, and
-// 1024 threads with 2 units took 94 us, not 63, at 16384 x 6144 and 128, not 76, with
+// 1024 threads with 2 units took 94 us, not 63, at 16384 x 6144 and 135, not 76, with
 // 8-bit output.
 constexpr int kNormThreads = 512, kNormUnits = 4;
 
