@@ -715,8 +715,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 constexpr int kMaxGradStages = 4;
 
+// Wide rows take 512 threads per SM with 4 units each, as in the forward pass, for
+// what a row costs a thread beside its values (8192 rows: 5280 columns 62 -> 56 us,
+// 8192 86.4 -> 84.9, 10240 124 -> 105, 16384 205 -> 182, against 1024 with 2 units).
 template <bool kBf16, int T, int NV>
-__global__ void __launch_bounds__(T, 1024 / T)
+__global__ void __launch_bounds__(T, (NV > 2 ? 512 : 1024) / T)
     rms_norm_grad_kernel(const RmsGradCall c, float *part, int stages, uint32_t *err_word) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kMaxGradStages];
@@ -1114,10 +1117,11 @@ cudaError_t launch_grad_warp(const DeviceInfo &dev, const RmsGradCall &c, cudaSt
 template <bool kBf16, int T, int NV = 2>
 cudaError_t launch_grad_ring(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_t stream) {
   auto kern = rms_norm_grad_kernel<kBf16, T, NV>;
-  // 1024 threads per SM share about 200 KB of rows in flight; the blocks beside
-  // each other hide each other's reductions. At the end the ring holds the sums.
+  // An SM's blocks share about 200 KB of rows in flight (220 makes three
+  // stages of 12288 columns, 156 -> 121 us for 8192 rows) and hide each other's reductions. At the end the ring
+  // holds the sums.
   const int units = c.cols / 8, stage = units * 16 * 3;
-  const int room = 200 * T;
+  const int room = (NV > 2 ? 440 : 200) * T;
   const int stages = std::max(2, std::min(kMaxGradStages, room / std::max(stage, 1)));
   const int smem = std::max(stages * stage, ((units + 27) / 32 * 32 + 4) * 8 * 4);
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem, dev.device);
@@ -1187,9 +1191,9 @@ cudaError_t launch_grad(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_
   if (units <= 128) return launch_grad_ring<kBf16, 128, 1>(dev, c, stream);
   if (units <= 256 && c.rows > 10 * dev.sm_count) return launch_grad_rows<kBf16, 8>(dev, c, stream);
   if (units <= 256) return launch_grad_ring<kBf16, 128>(dev, c, stream);
-  if (units <= 512) return launch_grad_ring<kBf16, 256>(dev, c, stream);
-  if (units <= 1024) return launch_grad_ring<kBf16, 512>(dev, c, stream);
-  if (units <= 2048) return launch_grad_ring<kBf16, 1024>(dev, c, stream);
+  if (units <= 512) return launch_grad_ring<kBf16, 128, 4>(dev, c, stream);
+  if (units <= 1024) return launch_grad_ring<kBf16, 256, 4>(dev, c, stream);
+  if (units <= 2048) return launch_grad_ring<kBf16, 512, 4>(dev, c, stream);
   return launch_grad_long<kBf16>(dev, c, stream);
 }
 
