@@ -1117,9 +1117,9 @@ cudaError_t launch_grad_warp(const DeviceInfo &dev, const RmsGradCall &c, cudaSt
 template <bool kBf16, int T, int NV = 2>
 cudaError_t launch_grad_ring(const DeviceInfo &dev, const RmsGradCall &c, cudaStream_t stream) {
   auto kern = rms_norm_grad_kernel<kBf16, T, NV>;
-  // An SM's blocks share about 200 KB of rows in flight (220 makes three
-  // stages of 12288 columns, 156 -> 121 us for 8192 rows) and hide each other's reductions. At the end the ring
-  // holds the sums.
+  // An SM's blocks share about 200 KB of rows in flight (220 makes three stages of
+  // 12288 columns, 156 -> 121 us for 8192 rows) and hide each other's reductions.
+  // At the end the ring holds the sums.
   const int units = c.cols / 8, stage = units * 16 * 3;
   const int room = (NV > 2 ? 440 : 200) * T;
   const int stages = std::max(2, std::min(kMaxGradStages, room / std::max(stage, 1)));
