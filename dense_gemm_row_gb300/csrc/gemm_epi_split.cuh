@@ -371,6 +371,9 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
       }
     });
   }
+  // Lanes leave the finishing loop after different numbers of rows; the barrier
+  // below is one the whole warp has to execute together.
+  __syncwarp();
   if (cl > 1) {
     // No CTA leaves, or reuses its stages, while another reads its sums. Reads
     // only, so the barrier orders no memory: a releasing arrive would wait for

@@ -1,0 +1,39 @@
+"""Edges of the linear-layer operators on the GPU: few rows spread unevenly over a
+warp's lanes, sizes and alignments that pick the rarer kernels, special values in
+gradients, captured gradients. Bounds come from tests/layer_util.py; results that
+are exact by construction are compared exactly."""
+import pytest
+import torch
+
+from tests.layer_util import normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def clean_error_word(gemm_mod):
+    gemm_mod.check_device_error()
+    yield
+    torch.cuda.synchronize()
+    assert gemm_mod.check_device_error() == 0
+
+
+@pytest.mark.parametrize("m", [1, 3, 17, 33, 100])
+def test_lanes_with_different_numbers_of_rows_over_many_calls(gemm_mod, m):
+    """The finishing lanes of the few-rows kernel have different numbers of rows, and
+    of the last column tile's lanes some have none (N = 1000 in tiles of 128): calls
+    back to back, on operands that change, against a call alone."""
+    A = [normal((m, 2048), torch.bfloat16, i) for i in range(4)]
+    B = normal((1000, 2048), torch.bfloat16, 9, 0.02)
+    R = normal((m, 1000), torch.bfloat16, 10)
+    ref = []
+    for a in A:
+        D = torch.empty_like(R)
+        gemm_mod.gemm_epilogue(a, B, D, act="silu", residual=R, trans_b=True)
+        torch.cuda.synchronize()
+        ref.append(D)
+    out = [torch.empty_like(R) for _ in range(400)]
+    for i, D in enumerate(out):
+        gemm_mod.gemm_epilogue(A[i % 4], B, D, act="silu", residual=R, trans_b=True)
+    torch.cuda.synchronize()
+    assert all(torch.equal(D, ref[i % 4]) for i, D in enumerate(out))
