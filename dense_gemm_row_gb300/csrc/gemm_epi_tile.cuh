@@ -170,6 +170,7 @@ __device__ __forceinline__ void store_block(const void *tm, bool tma, uint16_t *
       tma_store_3d(tm, col, row0, 0, stage);
       bulk_commit();
     }
+    __syncwarp();  // the next accumulator load needs the warp converged
   } else {
     __syncwarp();
 #pragma unroll 8
