@@ -409,7 +409,7 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
   const bool got = mbar_wait_lazy(smem_u32(&sm.tmem_full[buf]), use, abort, p.err_word,
                                   kWaitTmemFull);
   if (have_r) take_r();
-  if (!__all_sync(0xffffffffu, got)) {
+  if (!got) {
     ok = false;
     return;
   }
@@ -581,7 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = unit; t < p.tiles; t += units, ++n) {
       int tm, tn;
       tile_coords<kEpiGroupM>(t, p.tiles_m, p.tiles_n, tm, tn);
-      if (!ok || *static_cast<volatile int *>(&sm.abort)) {
+      // (The warp reads the flag as one: its lanes must take the same branch.)
+      if (__any_sync(0xffffffffu, !ok || *static_cast<volatile int *>(&sm.abort))) {
         ok = false;
         if constexpr (!kGrad) {
           epilogue_sync();

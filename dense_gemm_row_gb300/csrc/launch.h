@@ -9,9 +9,9 @@
 namespace dgr {
 
 // Layout of the per-device error word (read and cleared by
-// gemm_check_device_error): bit 0 = a bounded wait gave up; bits 8..15 = the
-// code of the first wait that gave up.
-constexpr uint32_t kErrTimeoutBit = 1u;
+// gemm_check_device_error): bit 0 = a bounded wait gave up; bit 1 (self-test) =
+// not all lanes of a warp did; bits 8..15 = the code of the first wait that gave up.
+constexpr uint32_t kErrTimeoutBit = 1u, kErrLanesBit = 2u;
 constexpr uint32_t kWaitFull = 1, kWaitEmpty = 2, kWaitTmemFull = 3, kWaitTmemEmpty = 4,
                    kWaitDrain = 5, kWaitFlag = 6, kWaitTest = 7;
 

@@ -30,22 +30,31 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// mbar_wait_bounded for the issue loops: the same bound and the same failure, but
-// the clock is first read after 64 polls, so a wait that is met in time costs its
-// polls only. kCluster: acquires at cluster scope.
+// mbar_wait_bounded for the issue loops, by a whole warp: the same bound and the
+// same failure, but the clock is first read after 64 polls, so a wait that is met in
+// time costs its polls only. Lanes poll and read the clock for themselves, so at the
+// limit some could give up a wait that others see met: the warp votes on every poll
+// and on giving up, and all its lanes get the same answer. kCluster: acquires at
+// cluster scope.
 template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_lazy(uint32_t bar, uint32_t parity, volatile int *abort,
-                                               uint32_t *err_word, uint32_t code) {
+                                               uint32_t *err_word, uint32_t code,
+                                               uint64_t limit_ns = kWaitLimitNs) {
+  constexpr uint32_t kWarp = 0xffffffffu;
   uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
-    if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (__all_sync(kWarp, kCluster ? mbar_try_wait_cluster(bar, parity)
+                                   : mbar_try_wait(bar, parity)))
+      return true;
     if ((it & 63u) == 0u) {
-      if (*abort) return false;
       const uint64_t now = global_timer_ns();
       if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs || it >= kWaitMaxPolls) {
-        *abort = 1;
-        record_timeout(err_word, code);
+      const bool late = now - t0 > limit_ns || it >= kWaitMaxPolls;
+      if (__any_sync(kWarp, late || *abort)) {
+        if (late) {
+          *abort = 1;
+          record_timeout(err_word, code);
+        }
         return false;
       }
     }

@@ -470,9 +470,11 @@ GEMM_API gemm_status_t gemm_check_device_error(uint32_t *word);
  * Diagnostic of the failure path: enqueues one warp that waits, with the same
  * bounded mbarrier wait as the GEMM kernels, on a barrier nothing arrives on.
  * After limit_us microseconds (1 .. 1000000) the wait gives up, records a
- * timeout (wait code 7) in the device error word and the kernel returns; the
- * context stays usable and gemm_check_device_error() then reports
- * GEMM_ERR_TIMEOUT. Nothing faults, traps or hangs. Returns
+ * timeout (wait code 7) in the device error word; the same again for the wait
+ * of a whole warp, half of whose lanes see it met (bit 1 of the word is set if
+ * the lanes' answers differ). Then the kernel returns; the context stays usable
+ * and gemm_check_device_error() reports GEMM_ERR_TIMEOUT. Nothing faults, traps
+ * or hangs. Returns
  * GEMM_ERR_INVALID_VALUE for a limit outside the range, else the launch status.
  * Source: none on the pages (their error handling aborts the process); this is
  * the library's own failure detection.
