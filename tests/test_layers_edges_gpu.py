@@ -2,10 +2,12 @@
 warp's lanes, sizes and alignments that pick the rarer kernels, special values in
 gradients, captured gradients. Bounds come from tests/layer_util.py; results that
 are exact by construction are compared exactly."""
+import numpy as np
 import pytest
 import torch
 
-from tests.layer_util import normal
+from oracle import layers as L
+from tests.layer_util import assert_close, normal, product_bound, rounded_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +54,25 @@ def test_stores_of_several_units_per_warp_over_many_calls(gemm_mod, preact):
         gemm_mod.gemm_epilogue(A, B, D, act="gelu_tanh", preact=Z, trans_b=True)
         ref = ref or (D, Z)
         assert torch.equal(D, ref[0]) and (Z is None or torch.equal(Z, ref[1]))
+
+
+@pytest.mark.parametrize("m", [16, 100, 128, 200])
+def test_bias_gradient_of_few_rows_with_a_long_inner_dimension(gemm_mod, m):
+    """Few-rows gradients whose k range is split over a cluster, at every tile height:
+    the sums are those of the stored dZ's unrounded values, the same on every call."""
+    n, k = 1000, 4096
+    A = normal((m, k), torch.bfloat16, 1)
+    B = normal((n, k), torch.bfloat16, 2, k ** -0.5)
+    Z = normal((m, n), torch.bfloat16, 3)
+    ref = None
+    for _ in range(50):
+        dZ, db = torch.empty_like(Z), torch.empty(n, dtype=torch.bfloat16, device="cuda")
+        gemm_mod.gemm_dact(A, B, Z, dZ, act="silu", dbias=db, trans_b=True)
+        ref = ref or (dZ, db)
+        assert torch.equal(dZ, ref[0]) and torch.equal(db, ref[1])
+    A64, B64 = L.to64(A), L.to64(B).T
+    dz, want = L.linear_grad(A64 @ B64, L.to64(Z), "silu")
+    e = 1.13 * product_bound(A64, B64) + np.abs(A64 @ B64) * 2.0 ** -18 * (1 + np.abs(L.to64(Z)))
+    assert_close(L.to64(dZ), dz, rounded_bound(dz, e, torch.bfloat16), "dZ")
+    eb = e.sum(0) + m * 2.0 ** -24 * np.abs(dz).sum(0)
+    assert_close(L.to64(db), want, rounded_bound(want, eb, torch.bfloat16), "dbias")
