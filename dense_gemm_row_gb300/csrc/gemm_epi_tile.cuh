@@ -389,6 +389,11 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
   auto request_r = [&](int col) {
     stage_free(lane);
     if (p.r_tma) {
+      // The buffer's last accesses were ordinary ones where no TMA store followed them.
+      if (!p.d_tma) {
+        fence_proxy_async_shared();
+        __syncwarp();
+      }
       if (lane == 0) {
         mbar_arrive_expect_tx(rbar, kStageCBytes);
         tma_load_3d(stage, &tmR, rbar, col, row0, 0);

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import layers as L
-from tests.layer_util import assert_close, normal, product_bound, rounded_bound
+from tests.layer_util import act_error, assert_close, normal, product_bound, rounded_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +76,33 @@ def test_bias_gradient_of_few_rows_with_a_long_inner_dimension(gemm_mod, m):
     assert_close(L.to64(dZ), dz, rounded_bound(dz, e, torch.bfloat16), "dZ")
     eb = e.sum(0) + m * 2.0 ** -24 * np.abs(dz).sum(0)
     assert_close(L.to64(db), want, rounded_bound(want, eb, torch.bfloat16), "dbias")
+
+
+@pytest.mark.parametrize("op", ["linear", "gradient"])
+@pytest.mark.parametrize("n", [600, 777])
+def test_rows_read_by_copies_and_written_by_plain_stores(gemm_mod, op, n):
+    """R (Zin) in whole 16-byte units, D off them: the tile kernel's staging buffer is
+    in turn filled by an asynchronous copy and by ordinary stores, over several units
+    per warp and several tiles per CTA pair. Against the same call with D aligned."""
+    m, k = 2600, 128
+    A, B = normal((m, k), torch.bfloat16, 1), normal((n, k), torch.bfloat16, 2, 0.1)
+    R = normal((m, n), torch.bfloat16, 3, unit=8)
+    ref = torch.empty(m, 784, dtype=torch.bfloat16, device="cuda")[:, :n]
+    for i in range(10):
+        flat = torch.empty(m * n + 1, dtype=torch.bfloat16, device="cuda")
+        D = flat[1:].view(m, n)
+        for out in (ref, D) if i == 0 else (D,):
+            if op == "linear":
+                gemm_mod.gemm_epilogue(A, B, out, act="gelu", residual=R, trans_b=True)
+            else:
+                gemm_mod.gemm_dact(A, B, R, out, act="silu", trans_b=True)
+        assert torch.equal(D, ref)
+    A64, B64 = L.to64(A), L.to64(B).T
+    if op == "linear":
+        want, z = L.linear(A64, B64, 1.0, None, "gelu", L.to64(R))
+        e = 1.13 * product_bound(A64, B64) + act_error(z, "gelu") + 2.0 ** -23 * np.abs(want)
+    else:
+        d = A64 @ B64
+        want, _ = L.linear_grad(d, L.to64(R), "silu")
+        e = 1.13 * product_bound(A64, B64) + np.abs(d) * 2.0 ** -18 * (1 + np.abs(L.to64(R)))
+    assert_close(L.to64(ref), want, rounded_bound(want, e, torch.bfloat16), "D")
