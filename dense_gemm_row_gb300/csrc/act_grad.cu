@@ -28,6 +28,7 @@ namespace {
 constexpr int kCols = 256;  // columns per block
 constexpr int kSlots = 8;   // rows at a time
 constexpr int kBlocksPerSm = 3;
+constexpr int64_t kMaxChunk = 1 << 30;  // rows; its round-up stays in 32 bits
 // Row groups loaded together, with a second such set in flight (2-byte loads: one,
 // for the registers). Measured at 8192 x 4096, gelu: 1 / 2 / 3 groups 40.1 / 38.1 /
 // 48.4 us; 3 blocks per SM against 4: 38.1, 39.7 us.
@@ -175,12 +176,13 @@ cudaError_t launch_act_grad(const DeviceInfo &dev, bool bf16, int M, int N, int 
                             uint16_t *dZ, int64_t lddz, uint16_t *dbias, cudaStream_t stream) {
   if (M == 0) return launch_col_sums(bf16, nullptr, 0, N, N, dbias, stream);
   // As many row chunks as fill the GPU once (kBlocksPerSm blocks per SM).
-  const int strips = (N + kCols - 1) / kCols;
+  const int strips = (N - 1) / kCols + 1;  // sizes up to 2^31 - 1
   const int64_t want =
       std::max<int64_t>(1, static_cast<int64_t>(dev.sm_count) * kBlocksPerSm / strips);
-  int chunk = static_cast<int>((M + want - 1) / want);
-  chunk = (chunk + kSlots - 1) / kSlots * kSlots;
-  const int chunks = (M + chunk - 1) / chunk;
+  const int64_t even = (M - 1) / want + 1;
+  const int chunk =
+      static_cast<int>(std::min<int64_t>((even - 1) / kSlots * kSlots + kSlots, kMaxChunk));
+  const int chunks = (M - 1) / chunk + 1;
   float *part = nullptr;
   if (dbias != nullptr) {
     cudaMemPool_t pool;

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(32 * kSlots)
 cudaError_t launch_col_sums(bool bf16, const float *part, int parts, int n, int64_t ld,
                             uint16_t *out, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((n + 31) / 32), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((n - 1) / 32 + 1), 1, 1);
   cfg.blockDim = dim3(32, kSlots, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -102,8 +102,7 @@ cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t
                             const EpiCall &epi, cudaStream_t stream) {
   if (K == 0) return launch_empty(M, N, epi, stream);
   const bool ragged = N % 8 != 0 || epi.ldd % 8 != 0 || reinterpret_cast<uintptr_t>(epi.D) % 16 != 0;
-  const EpiPlan plan =
-      plan_epi(dev, a_t, M, N, (K + (e4m3 ? 127 : 63)) / (e4m3 ? 128 : 64), ragged);
+  const EpiPlan plan = plan_epi(dev, a_t, M, N, (K - 1) / (e4m3 ? 128 : 64) + 1, ragged);
   const int mp = plan.split_rows, tile_n = plan.tile_n;
   if (!epi.grad) {
     if (e4m3)

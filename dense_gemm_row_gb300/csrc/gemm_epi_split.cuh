@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   // from memory once and found in L2 by the others.
   const int tile = static_cast<int>(blockIdx.x) / cl;
   const int n0 = tile / p.tiles_m * kSplitN, m0 = tile % p.tiles_m * kMP;
-  const int KB = (p.K + kBK - 1) / kBK;
+  const int KB = (p.K - 1) / kBK + 1;
   const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * KB / cl);
   const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * KB / cl);
 
@@ -461,8 +461,8 @@ cudaError_t launch_split_form(const DeviceInfo &dev, bool b_t, int M, int N, int
 
   SplitArgs p;
   p.M = M, p.N = N, p.K = K;
-  p.mp = std::min((M + 15) / 16 * 16, kMP);
-  p.tiles_m = (M + kMP - 1) / kMP;
+  p.mp = (std::min(M, kMP) + 15) / 16 * 16;
+  p.tiles_m = (M - 1) / kMP + 1;
   p.b_t = b_t;
   auto vec = [](const uint16_t *q, int64_t ld) {
     return reinterpret_cast<uintptr_t>(q) % 8 == 0 && ld % 4 == 0;
@@ -480,9 +480,9 @@ cudaError_t launch_split_form(const DeviceInfo &dev, bool b_t, int M, int N, int
       !(b_t ? make_tmap(&tmB, dt, kEs, B, N, K, ldb, 1, 0, kSplitN, kBK)
             : make_tmap(&tmB, dt, kEs, B, K, N, ldb, 1, 0, 64, 64)))
     return cudaErrorInvalidValue;
-  const int64_t tiles = static_cast<int64_t>((N + kSplitN - 1) / kSplitN) * p.tiles_m;
+  const int64_t tiles = static_cast<int64_t>((N - 1) / kSplitN + 1) * p.tiles_m;
   if (tiles > 0x7fffffffLL / kSplitMaxCl) return cudaErrorInvalidValue;
-  const int KB = (K + kBK - 1) / kBK;
+  const int KB = (K - 1) / kBK + 1;
   // As many parts of k as fill the SMs twice, at least one k-block each.
   int cl = 1;
   while (cl < kSplitMaxCl && tiles * cl * 2 <= static_cast<int64_t>(kSplitCtasPerSm) * dev.sm_count &&

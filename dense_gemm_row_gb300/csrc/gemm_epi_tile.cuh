@@ -239,7 +239,7 @@ __device__ __forceinline__ void epi_produce(const CUtensorMap &tmA, const CUtens
   constexpr uint32_t kMNBoxBytes = kRowBytes * 64;  // 64 rows of k x 64 16-bit values
   volatile int *abort = &sm.abort;
   const uint64_t keep = l2_policy_evict_last();
-  const int KB = (p.K + kBK - 1) / kBK;
+  const int KB = (p.K - 1) / kBK + 1;
   uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
   bool ok = true;
   for (int t = unit; ok && t < p.tiles; t += units) {
@@ -302,7 +302,7 @@ __device__ __forceinline__ void epi_multiply(const EpiArgs &p, EpiSmem<kN> &sm,
   constexpr uint32_t kMNBoxBytes = kRowBytes * 64;
   constexpr uint32_t kMNStep = kRowBytes * 16;  // 16 rows of k
   volatile int *abort = &sm.abort;
-  const int KB = (p.K + kBK - 1) / kBK;
+  const int KB = (p.K - 1) / kBK + 1;
   // K-major: SBO = one 8-row swizzle atom, the next MMA 32 bytes along the row.
   // MN-major (16-bit only): LBO = one 64-value box, the next MMA 16 k-rows on.
   const uint64_t adesc0 =
@@ -655,8 +655,8 @@ cudaError_t launch_epi_tile(const DeviceInfo &dev, bool a_t, bool b_t, int M, in
     return cudaErrorInvalidValue;
   EpiArgs p;
   p.M = M, p.N = N, p.K = K;
-  p.tiles_m = (M + Cf::kTileM - 1) / Cf::kTileM;
-  p.tiles_n = (N + kN - 1) / kN;
+  p.tiles_m = (M - 1) / Cf::kTileM + 1;  // sizes up to 2^31 - 1
+  p.tiles_n = (N - 1) / kN + 1;
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x7fffffffLL - pairs) return cudaErrorInvalidValue;
   p.tiles = static_cast<int>(tiles);
