@@ -478,11 +478,15 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
       if (h == 0) stage_free(lane);
       stage_half(stage, lane, h, w);
       if constexpr (kGrad) {
-        // Rows beyond M hold zeros (zero-filled operands), so they add nothing.
+        // Rows beyond M are left out: they hold 0 * B, NaN where B is not finite.
         if (p.part != nullptr && row0 < p.M) {
           float u[32];
 #pragma unroll
           for (int j = 0; j < 16; ++j) split(v[j], u[2 * j], u[2 * j + 1]);
+          if (row >= p.M) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) u[j] = 0.f;
+          }
           const float s = warp_column_sums(u, lane);
           const int col = col0 + c + 32 * h + lane;
           if (col < p.N) p.part[static_cast<int64_t>(row0 / 32) * p.N + col] = s;

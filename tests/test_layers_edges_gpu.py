@@ -106,3 +106,25 @@ def test_rows_read_by_copies_and_written_by_plain_stores(gemm_mod, op, n):
         want, _ = L.linear_grad(d, L.to64(R), "silu")
         e = 1.13 * product_bound(A64, B64) + np.abs(d) * 2.0 ** -18 * (1 + np.abs(L.to64(R)))
     assert_close(L.to64(ref), want, rounded_bound(want, e, torch.bfloat16), "D")
+
+
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("m", [5, 65, 300, 352, 513])
+def test_bias_gradient_of_an_infinite_column(gemm_mod, m, value, act):
+    """An infinity in column 2 of B makes that column of dZ infinite, of one sign: so
+    is its sum, whatever M is modulo 32, and no other column changes."""
+    A = normal((m, 72), torch.bfloat16, 1)
+    A[:, 5] = A[:, 5].abs() + 0.5
+    B = normal((72, 96), torch.bfloat16, 2)
+    Z = torch.ones(m, 96, dtype=torch.bfloat16, device="cuda")
+    out = []
+    for v in (0.0, value):
+        B[5, 2] = v
+        dZ, db = torch.empty_like(Z), torch.empty(96, dtype=torch.bfloat16, device="cuda")
+        gemm_mod.gemm_dact(A, B, Z, dZ, act=act, dbias=db)
+        out.append((dZ, db))
+    (dZ0, db0), (dZ, db) = out
+    assert bool((dZ[:, 2] == value).all()) and db[2].item() == value
+    dZ[:, 2], db[2] = dZ0[:, 2], db0[2]
+    assert torch.equal(dZ, dZ0) and torch.equal(db, db0)
