@@ -596,8 +596,8 @@ struct GradSums {
 // whether there is a dH; inv_n: 1 / cols.
 //
 // With t = dy s: dw += t h and sum(g n) = sum(t w h), so that
-// dx = s (dy w) - h (s^2 mean(g n)) + dh takes three operations per value, on
-// packed pairs.
+// dx = s (dy w - h (s mean(g n))) + dh takes three operations per value, on packed
+// pairs. (No s^2, which overflows for s above 1.8e19 where dx need not.)
 template <bool kBf16, int T, int NV, typename Get, typename Between>
 __device__ __forceinline__ void grad_row(uint16_t *X, const RowWalk &k, bool same, bool past,
                                          int t, GradSums<kBf16, NV> &sums, float s, float inv_n,
@@ -630,7 +630,7 @@ __device__ __forceinline__ void grad_row(uint16_t *X, const RowWalk &k, bool sam
   }
   dot = row_sum<T>(dot, red);
   between();
-  const float back = -s * s * (dot * inv_n);
+  const float back = -s * (dot * inv_n);
   const F2 back2 = f2(back);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -643,13 +643,14 @@ __device__ __forceinline__ void grad_row(uint16_t *X, const RowWalk &k, bool sam
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         out[q] = pack2<kBf16>(
-            fma2(mul2(unpack2<kBf16>(yw[q]), unpack2<kBf16>(ww[q])), s2,
-                 fma2(unpack2<kBf16>(hw[q]), back2, unpack2<kBf16>(bw[q]))));
+            fma2(fma2(unpack2<kBf16>(hw[q]), back2,
+                      mul2(unpack2<kBf16>(yw[q]), unpack2<kBf16>(ww[q]))),
+                 s2, unpack2<kBf16>(bw[q])));
       store_unit(X, k, i * T + t, same, make_uint4(out[0], out[1], out[2], out[3]));
     }
   }
   if (k.extra >= 0)
-    X[k.extra] = to16<kBf16>(fmaf(ye * we, s, fmaf(he, back, from16<kBf16>(extra[2]))));
+    X[k.extra] = to16<kBf16>(fmaf(fmaf(he, back, ye * we), s, from16<kBf16>(extra[2])));
 }
 
 // Short rows of matrices that are aligned differently: one warp per row, straight

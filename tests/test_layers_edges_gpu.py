@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import layers as L
-from tests.layer_util import act_error, assert_close, normal, product_bound, rounded_bound
+from tests.layer_util import Out, act_error, assert_close, normal, product_bound, rounded_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,24 @@ def test_bias_gradient_of_an_infinite_column(gemm_mod, m, value, act):
     assert bool((dZ[:, 2] == value).all()) and db[2].item() == value
     dZ[:, 2], db[2] = dZ0[:, 2], db0[2]
     assert torch.equal(dZ, dZ0) and torch.equal(db, db0)
+
+
+@pytest.mark.parametrize("m,n", [(9, 64), (700, 500), (40, 1001), (5, 4096), (2, 20001)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_gradient_of_tiny_rows(gemm_mod, m, n, shift):
+    """Rows whose rstd squared is past fp32's largest value, dX itself is not."""
+    H = normal((m, n), torch.bfloat16, n, 2e-20)
+    dY, W = normal((m, n), torch.bfloat16, n + 1), normal((1, n), torch.bfloat16, n + 2)[0]
+    h64, y64, w64 = L.to64(H), L.to64(dY), L.to64(W)
+    rstd = torch.from_numpy((h64 * h64).mean(1) ** -0.5).float().cuda()
+    s64 = L.to64(rstd)
+    assert s64.min() > 2.0 ** 64
+    dX, dW = Out(m, n, torch.bfloat16, shift=shift), Out(1, n, torch.bfloat16)
+    gemm_mod.rms_norm_grad(dY, H, rstd, dX.t, weight=W, dweight=dW.t[0])
+    torch.cuda.synchronize()
+    dx, dw = L.rms_norm_grad(y64, h64, s64, w64)
+    nrm, g = h64 * s64[:, None], np.abs(y64 * w64)
+    terms = s64[:, None] * (g + np.abs(nrm) * (g * np.abs(nrm)).mean(1, keepdims=True))
+    assert_close(L.to64(dX.t), dx, rounded_bound(dx, 2.0 ** -17 * terms, torch.bfloat16), "dX")
+    ew = (m + 20) * 2.0 ** -24 * np.abs(y64 * nrm).sum(0)
+    assert_close(L.to64(dW.t[0]), dw, rounded_bound(dw, ew, torch.bfloat16), "dW")
