@@ -66,6 +66,7 @@ constexpr float kGeluA = 0.044715f;
 constexpr float kInvSqrt2 = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFltMax = 3.402823466e38f;
 
 // Two fp32 values in one register pair, and the packed operations on them: one
 // instruction for two values. It keeps the element-wise gradient near the cost of
@@ -158,8 +159,9 @@ __device__ __forceinline__ F2 logistic2(F2 z) {
   return rcp_fast2(add2(exp2_fast2(mul2(z, f2(-kLog2e))), f2(1.f)));
 }
 
-// The activations of two values. gelu: z Phi(z) = max(z, 0) - |z| Phi(-|z|).
-template <int kAct>
+// The activations of two values. gelu: z Phi(z) = max(z, 0) - |z| Phi(-|z|), where the
+// tail is 0 at +inf: |z| has to be finite there (kFinite: z is known to be).
+template <int kAct, bool kFinite = false>
 __device__ __forceinline__ F2 act_value2(F2 z) {
   if constexpr (kAct == kActNone) return z;
   if constexpr (kAct == kActSilu) return mul2(z, logistic2(z));
@@ -169,10 +171,31 @@ __device__ __forceinline__ F2 act_value2(F2 z) {
   if constexpr (kAct == kActRelu) {  // NaN stays NaN
     return f2(z0 < 0.f ? 0.f : z0, z1 < 0.f ? 0.f : z1);
   } else {
-    const F2 mag = f2(fabsf(z0), fabsf(z1));
+    const F2 mag = kFinite ? f2(fabsf(z0), fabsf(z1))
+                           : f2(fmaxf(fminf(z0, kFltMax), -z0), fmaxf(fminf(z1, kFltMax), -z1));
     F2 e;
     return fma2(mag, minus_tail2(z, mag, e), f2(fmaxf(z0, 0.f), fmaxf(z1, 0.f)));
   }
+}
+// The same for the lanes' 2 kN values, by a whole warp. gelu: a sum shows whether all
+// are finite, for one addition per pair instead of two clamps (8192 x 8192 x 256: 108.0
+// us without care for infinities, 109.8 checked, 114.6 clamped; four sums in turn: 110.1).
+template <int kAct, int kN>
+__device__ __forceinline__ void act_values(F2 (&z)[kN]) {
+  if constexpr (kAct == kActGelu) {
+    F2 sum = z[0];
+#pragma unroll
+    for (int j = 1; j < kN; ++j) sum = add2(sum, z[j]);
+    float a, b;
+    split(sum, a, b);
+    if (__any_sync(0xffffffffu, !(fabsf(a + b) <= kFltMax))) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) z[j] = act_value2<kAct>(z[j]);
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kN; ++j) z[j] = act_value2<kAct, true>(z[j]);
 }
 template <int kAct>
 __device__ __forceinline__ float act_value(float z) {

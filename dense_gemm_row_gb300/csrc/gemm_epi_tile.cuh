@@ -453,10 +453,7 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
       if constexpr (!kGrad) {
         epi_preact<kE4m3, kBf16>(&sm.bias[local0 + c + 32 * h], &sm.scale[local0 + c + 32 * h],
                                  row_scale, acc, v);
-        with_act(p.c.act, [&](auto a) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = act_value2<decltype(a)::value>(v[j]);
-        });
+        with_act(p.c.act, [&](auto a) { act_values<decltype(a)::value>(v); });
         if (have_r) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = add2(v[j], unpack2<kBf16>(r[16 * h + j]));

@@ -286,8 +286,9 @@ GEMM_API gemm_status_t gemm_s8_noalloc(int64_t M, int64_t N, int64_t K, int32_t 
 
 /* Activations. gelu is z Phi(z) (Phi: the normal distribution function),
  * gelu_tanh its tanh form 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))),
- * silu z / (1 + exp(-z)). They are evaluated to a few 2^-20 relative; at an
- * infinite z the formulas' 0 * inf gives NaN. */
+ * silu z / (1 + exp(-z)). They are evaluated to a few 2^-20 relative. At
+ * z = +inf they are +inf, at -inf the formulas' 0 * inf gives NaN, and so do the
+ * slopes of the last three at both; relu is 0 and its slope 0 or 1. */
 typedef enum {
     GEMM_ACT_NONE = 0,
     GEMM_ACT_RELU = 1,

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from oracle import layers as L
-from tests.layer_util import Out, act_error, assert_close, normal, product_bound, rounded_bound
+from tests.layer_util import (DTYPES, Out, act_error, assert_close, normal, product_bound,
+                              rounded_bound)
 
 pytestmark = pytest.mark.gpu
 
@@ -149,3 +150,32 @@ def test_gradient_of_tiny_rows(gemm_mod, m, n, shift):
     assert_close(L.to64(dX.t), dx, rounded_bound(dx, 2.0 ** -17 * terms, torch.bfloat16), "dX")
     ew = (m + 20) * 2.0 ** -24 * np.abs(y64 * nrm).sum(0)
     assert_close(L.to64(dW.t[0]), dw, rounded_bound(dw, ew, torch.bfloat16), "dW")
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("m", [5, 300])
+@pytest.mark.parametrize("k", [0, 8])
+def test_infinite_preactivations(gemm_mod, m, act, k):
+    """+inf stays +inf; -inf is 0 for relu and NaN where the formula has -inf * 0."""
+    inf = float("inf")
+    for dtype in DTYPES.values():
+        A, B = torch.zeros(m, k, dtype=dtype, device="cuda"), torch.zeros(
+            k, 40, dtype=dtype, device="cuda")
+        bias = torch.zeros(40, dtype=dtype, device="cuda")
+        bias[3], bias[4] = inf, -inf
+        if k:
+            B[0] = 1
+            A[1, 0] = inf
+            A[2, 0] = -inf
+        D = torch.empty(m, 40, dtype=dtype, device="cuda")
+        gemm_mod.gemm_epilogue(A, B, D, act=act, bias=bias)
+        z = np.zeros((m, 40))
+        z[:, 3] += inf
+        z[:, 4] -= inf
+        if k:
+            with np.errstate(invalid="ignore"):
+                z[1] += inf
+                z[2] -= inf
+        with np.errstate(invalid="ignore"):
+            ref = L.act(z, act)
+        assert np.array_equal(L.to64(D), ref, equal_nan=True), act
