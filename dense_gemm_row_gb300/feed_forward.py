@@ -76,11 +76,14 @@ class FeedForward:
         return grads
 
     def quantise(self):
-        """Keeps W1 as e4m3 with a scale per output (row) for forward8."""
-        scale = self.w1.float().abs().amax(1) / 448
+        """Keeps W1 as e4m3 with a scale per output (row) for forward8. As in the norm, a
+        row whose largest value is below 1e-30 counts as zeros, with scale 0."""
+        top = self.w1.float().abs().amax(1)
+        scale = torch.where(top < 1e-30, torch.zeros_like(top), top / 448)
+        inverse = torch.where(top < 1e-30, torch.zeros_like(top), 448 / top)
         ld = -(-self.model // 16) * 16  # rows in whole 16-byte units
         q = torch.zeros(self.hidden, ld, dtype=torch.float8_e4m3fn, device="cuda")[:, :self.model]
-        q.copy_((self.w1.float() / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn))
+        q.copy_((self.w1.float() * inverse[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn))
         self.quantised = (q, scale)
 
     def forward8(self, x, r):
