@@ -29,3 +29,18 @@ def test_rows_of_zeros(gemm_mod, tokens, tiny):
     ff.w1[7] = tiny
     ff.w1[200:] = tiny
     assert near(ff, x, r, ff.forward8(x, r))
+
+
+def test_weights_that_change_between_calls(gemm_mod):
+    """forward8 works on the weights of the call: after a change in place, as a
+    training step makes, and after new ones; weights quantised by the caller stay."""
+    ff, other = FeedForward(128, 264, "silu", seed=3), FeedForward(128, 264, "silu", seed=3)
+    x, r = (torch.randn(40, 128, device="cuda").bfloat16() for _ in range(2))
+    kept, first = ff.quantise(), ff.forward8(x, r)
+    ff.w1.neg_()
+    other.w1.neg_()
+    second = ff.forward8(x, r)
+    assert near(ff, x, r, second) and torch.equal(second, other.forward8(x, r))
+    ff.w1 = torch.randn_like(ff.w1) * 0.1
+    assert near(ff, x, r, ff.forward8(x, r))
+    assert torch.equal(ff.forward8(x, r, kept), first)
