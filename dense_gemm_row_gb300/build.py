@@ -5,7 +5,8 @@ Each translation unit is compiled in parallel to an object file under
 statically, so the library needs no libcudart at load time and resolves the
 driver only when a GPU call is made. Beside it, csrc/py_layers.cpp becomes the
 Python module ``_layers`` (argument marshalling of the linear-layer operators;
-needs the headers of Python and torch).
+needs the headers of Python and torch). Without torch the C library alone is
+built; the module is built again when the Python or torch it was made for changes.
 
     python -m dense_gemm_row_gb300.build [--force] [--ptxas-verbose]
 """
@@ -50,11 +51,16 @@ def _deps():
     return hdrs
 
 
-def _layers_command(out: str):
-    """g++ command that builds the _layers module against the running Python and torch."""
+def _torch_dir():
+    """Directory of the torch package, or None without torch."""
     import importlib.util
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _layers_command(torch_dir: str, out: str):
+    """g++ command that builds the _layers module against the running Python and torch."""
     import sysconfig
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     inc = os.path.join(torch_dir, "include")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     return ["g++", "-O2", "-std=c++20", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
@@ -65,6 +71,13 @@ def _layers_command(out: str):
             os.path.join(CSRC, "py_layers.cpp"), "-o", out,
             "-L", os.path.join(torch_dir, "lib"), "-Wl,-rpath," + os.path.join(torch_dir, "lib"),
             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def _layers_made_for(torch_dir: str) -> str:
+    """What a built _layers module depends on beside its sources."""
+    version = os.path.join(torch_dir, "version.py")
+    return "\n".join([sys.version, sys.executable, torch_dir,
+                      open(version).read() if os.path.exists(version) else ""])
 
 
 def _stale(target: str, inputs) -> bool:
@@ -90,23 +103,34 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = False)
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
-    layers_tmp = LAYERS_PATH + f".tmp{os.getpid()}"
-    layers = force or _stale(LAYERS_PATH, [os.path.join(CSRC, "py_layers.cpp"),
-                                           os.path.join(INCLUDE, "dense_gemm_row.h")])
-    if layers:
-        jobs.insert(0, _layers_command(layers_tmp))
+    # The _layers module needs torch; the C library does not, and is built without it.
+    torch_dir = _torch_dir()
+    layers_cmd = None
+    layers_tmp, layers_stamp = LAYERS_PATH + f".tmp{os.getpid()}", os.path.join(BUILD, "layers.txt")
+    if torch_dir is None:
+        if not quiet:
+            sys.stderr.write("torch not found: _layers (the linear-layer operators' Python "
+                             "functions) is not built\n")
+    else:
+        made_for = _layers_made_for(torch_dir)
+        if force or _stale(LAYERS_PATH, [os.path.join(CSRC, "py_layers.cpp"),
+                                         os.path.join(INCLUDE, "dense_gemm_row.h")]) \
+                or not os.path.exists(layers_stamp) or open(layers_stamp).read() != made_for:
+            layers_cmd = _layers_command(torch_dir, layers_tmp)
 
     def run(cmd):
         return cmd, subprocess.run(cmd, capture_output=True, text=True)
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
+    def check(cmd, res):
+        if res.returncode != 0:
+            raise RuntimeError("compiling failed:\n" + " ".join(cmd) + "\n" + res.stderr)
+        if (ptxas_verbose or res.stderr.strip()) and not quiet:
+            sys.stderr.write(res.stderr)
+
+    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
+        layers = ex.submit(run, layers_cmd) if layers_cmd else None
         for cmd, res in ex.map(run, jobs):
-            if res.returncode != 0:
-                raise RuntimeError("compiling failed:\n" + " ".join(cmd) + "\n" + res.stderr)
-            if (ptxas_verbose or res.stderr.strip()) and not quiet:
-                sys.stderr.write(res.stderr)
-    if layers:
-        os.replace(layers_tmp, LAYERS_PATH)
+            check(cmd, res)
     if force or jobs or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
@@ -114,6 +138,11 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = False)
         if res.returncode != 0:
             raise RuntimeError("link failed:\n" + " ".join(cmd) + "\n" + res.stderr)
         os.replace(tmp, LIB_PATH)
+    if layers:  # behind the C library, which a failure here leaves in place
+        check(*layers.result())
+        os.replace(layers_tmp, LAYERS_PATH)
+        with open(layers_stamp, "w") as f:
+            f.write(made_for)
     return LIB_PATH
 
 
