@@ -179,3 +179,42 @@ def test_infinite_preactivations(gemm_mod, m, act, k):
         with np.errstate(invalid="ignore"):
             ref = L.act(z, act)
         assert np.array_equal(L.to64(D), ref, equal_nan=True), act
+
+
+@pytest.mark.parametrize("m,n", [(40, 264), (300, 1000), (2000, 512), (700, 2048)])
+def test_gradients_captured_in_a_graph(gemm_mod, m, n):
+    """A layer's gradients, whose column sums allocate from the library's pool inside
+    the calls, captured once and replayed on new inputs: the bits of plain calls."""
+    dt = torch.bfloat16
+    inputs = [torch.empty(m, n, dtype=dt, device="cuda") for _ in range(4)]
+    dD, Z, H, dH = inputs
+    Wt, gain = normal((n, n), dt, 1, n ** -0.5), normal((1, n), dt, 2)[0]
+    rstd = torch.empty(m, device="cuda")
+
+    def draw(seed):
+        for i, t in enumerate(inputs):
+            t.copy_(normal((m, n), dt, 10 * seed + i))
+        rstd.copy_(torch.rsqrt(H.float().square().mean(1)))
+
+    def layer():
+        out = [torch.empty_like(dD) for _ in range(3)]
+        sums = [torch.empty(n, dtype=dt, device="cuda") for _ in range(3)]
+        gemm_mod.act_grad(dD, Z, out[0], act="gelu", dbias=sums[0])
+        gemm_mod.gemm_dact(out[0], Wt, Z, out[1], act="silu", dbias=sums[1])
+        gemm_mod.rms_norm_grad(out[1], H, rstd, out[2], weight=gain, dh=dH, dweight=sums[2])
+        return out + sums
+
+    draw(1)
+    layer()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = layer()
+    for seed in (2, 3, 3):
+        draw(seed)
+        for t in captured:
+            t.fill_(7)
+        graph.replay()
+        want = layer()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, want))
