@@ -113,8 +113,9 @@ __device__ __forceinline__ uint32_t pack2(F2 v) {
   return pack16<kBf16>(a, b);
 }
 // 2^x and 1 / x of both values: the hardware's approximations, subnormals taken
-// as zero. They are a few 2^-22 (relative) off, far below one 16-bit rounding
-// (2^-9 for bf16, 2^-12 for fp16). 1 / (1 + 2^x) needs no care at the ends: 2^x
+// as zero. They are a few 2^-22 (relative) off, and x's own roundings add |x| 2^-23, at
+// most 2^-16 before the result underflows: far below one 16-bit rounding (2^-9 for
+// bf16, 2^-12 for fp16). 1 / (1 + 2^x) needs no care at the ends: 2^x
 // overflows to infinity, whose reciprocal is 0, the limit.
 __device__ __forceinline__ F2 exp2_fast2(F2 x) {
   float a, b;

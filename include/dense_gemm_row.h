@@ -286,9 +286,12 @@ GEMM_API gemm_status_t gemm_s8_noalloc(int64_t M, int64_t N, int64_t K, int32_t 
 
 /* Activations. gelu is z Phi(z) (Phi: the normal distribution function),
  * gelu_tanh its tanh form 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))),
- * silu z / (1 + exp(-z)). They are evaluated to a few 2^-20 relative. At
- * z = +inf they are +inf, at -inf the formulas' 0 * inf gives NaN, and so do the
- * slopes of the last three at both; relu is 0 and its slope 0 or 1. */
+ * silu z / (1 + exp(-z)). Values are within 2^-15 relative: the error grows with
+ * the exponential's argument, 2^-19 near z = 0 and 2^-16 where a result is
+ * 10^-37; an exponential or logistic factor below 2^-126 counts as zero, so
+ * silu(z) is 0 below z = -87.3. Slopes are within 2^-18 (1 + |z|) absolute. At
+ * z = +inf all four values are +inf; at -inf relu is 0 and the others NaN, the
+ * formulas' -inf * 0. At both, relu's slope is 1 or 0 and the others' NaN. */
 typedef enum {
     GEMM_ACT_NONE = 0,
     GEMM_ACT_RELU = 1,

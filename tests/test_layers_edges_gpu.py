@@ -218,3 +218,28 @@ def test_gradients_captured_in_a_graph(gemm_mod, m, n):
         want = layer()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(captured, want))
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("m", [7, 300])
+def test_tails_keep_their_relative_accuracy(gemm_mod, act, m):
+    """z from -12 to -3 (a product of one value and one, exact): within 2^-15 relative,
+    then rounded. The exponential's argument in base 2 is at most 126, where the factor
+    underflows, and carries at most three roundings of 2^-24; the rest (the polynomial's
+    2^-19, the one-instruction exponential and reciprocal, products) adds less than
+    2^-18: 126 * 3 * 2^-24 * ln 2 + 2^-18 < 2^-15.6. A factor below 2^-126 counts as
+    zero: 2^-126 |z| absolute."""
+    n = 288
+    bf = torch.bfloat16
+    z = torch.linspace(-12, -3, m).to(bf)
+    A = torch.zeros(m, 8, dtype=bf)
+    A[:, 0] = z
+    B = torch.zeros(8, n, dtype=bf)
+    B[0] = 1
+    D = torch.empty(m, n, dtype=bf, device="cuda")
+    gemm_mod.gemm_epilogue(A.cuda(), B.cuda(), D, act=act)
+    z64 = L.to64(z)
+    want = L.act(z64, act) if act != "gelu_tanh" else z64 / (
+        1 + np.exp(-2 * np.sqrt(2 / np.pi) * (z64 + 0.044715 * z64 ** 3)))
+    bound = rounded_bound(want, 2.0 ** -15 * np.abs(want) + 2.0 ** -126 * np.abs(z64), bf)
+    assert_close(L.to64(D), np.repeat(want[:, None], n, 1), np.repeat(bound[:, None], n, 1), "D")
