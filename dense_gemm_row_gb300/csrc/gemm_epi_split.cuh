@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     got = __shfl_sync(0xffffffffu, got, 0);
     // Every MMA has completed and every copy was consumed by one, so the stages
     // are free: partial sums [row][column], lanes on columns. A CTA whose wait
-    // gave up (recorded in the error word) has NaN for sums.
+    // gave up (recorded in the error word, which is what counts) has NaN for sums,
+    // except where a late copy still lands on them.
     tc_fence_after_sync();
     float *red = reinterpret_cast<float *>(sm.b[0]) + quarter * 32 + lane;
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
