@@ -25,7 +25,8 @@ or one expanded along the batch with stride 0, is shared by every entry).
 The linear-layer operators have one function each for CUDA tensors:
 ``gemm_epilogue`` (a product with bias, activation and residual in its
 epilogue), ``gemm_dact`` and ``act_grad`` (the gradient at the pre-activation),
-``rms_norm`` and ``rms_norm_grad``. The dtypes pick the C entry point. They
+``rms_norm``, ``layer_norm`` and their gradients ``rms_norm_grad`` and
+``layer_norm_grad``. The dtypes pick the C entry point. They
 check shapes, dtypes, strides and devices before the call and write into the
 tensors they are given.
 """
@@ -56,7 +57,9 @@ EXPORTED = ("gemm_f32", "gemm_bf16", "gemm_f16", "gemm_s8", "gemm_u8", "gemm_f16
             "gemm_bf16_epi", "gemm_f16_epi", "gemm_e4m3_bf16_epi", "gemm_e4m3_f16_epi",
             "gemm_bf16_dact", "gemm_f16_dact", "gemm_act_grad_bf16", "gemm_act_grad_f16",
             "gemm_rms_norm_bf16", "gemm_rms_norm_f16", "gemm_rms_norm_bf16_e4m3",
-            "gemm_rms_norm_f16_e4m3", "gemm_rms_norm_grad_bf16", "gemm_rms_norm_grad_f16")
+            "gemm_rms_norm_f16_e4m3", "gemm_rms_norm_grad_bf16", "gemm_rms_norm_grad_f16",
+            "gemm_layer_norm_bf16", "gemm_layer_norm_f16", "gemm_layer_norm_grad_bf16",
+            "gemm_layer_norm_grad_f16")
 
 OP_N, OP_T = 0, 1  # gemm_op_t
 
@@ -126,6 +129,10 @@ def _load():
                                           vp, vp, vp],
             f"gemm_rms_norm_grad_{fmt}": [i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64,
                                           vp, vp],
+            f"gemm_layer_norm_{fmt}": [i64, i64, f32, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64,
+                                       vp, vp, vp],
+            f"gemm_layer_norm_grad_{fmt}": [i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp,
+                                            i64, vp, vp, vp],
         }
         for name, argtypes in layer.items():
             fn = getattr(lib, name)
@@ -371,7 +378,7 @@ def _load_layers():
     import torch  # noqa: F401  (the module links against torch's libraries)
     mod = importlib.import_module("dense_gemm_row_gb300._layers")
     for name in EXPORTED:
-        if "_epi" in name or "dact" in name or "act_grad" in name or "rms_norm" in name:
+        if any(part in name for part in ("_epi", "dact", "act_grad", "_norm")):
             mod.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
     _layers = mod
     return mod
@@ -446,4 +453,33 @@ def rms_norm_grad(dY, H, rstd, dX, *, weight=None, dh=None, dweight=None, stream
     st = (_layers or _load_layers()).rms_norm_grad(dY, H, rstd, dX, weight, dh, dweight, stream)
     if st:
         _check(st, "rms_norm_grad")
+    return dX
+
+
+def layer_norm(X, Y, *, weight=None, bias=None, residual=None, h=None, mean=None, rstd=None,
+               eps=1e-5, stream=None):
+    """Y = (H - mean) / sqrt(variance + eps) * weight + bias per row with
+    H = X + residual; returns Y.
+
+    X is rows x cols, bfloat16 or float16; everything else but the statistics has
+    its dtype: weight and bias (cols values), residual, h (which receives H) and Y.
+    mean and rstd (float32, rows values), when given, receive the row's mean and
+    1 / sqrt(variance + eps) for layer_norm_grad."""
+    st = (_layers or _load_layers()).layer_norm(X, Y, weight, bias, residual, h, mean, rstd, eps,
+                                                stream)
+    if st:
+        _check(st, "layer_norm")
+    return Y
+
+
+def layer_norm_grad(dY, H, mean, rstd, dX, *, weight=None, dh=None, dweight=None, dbias=None,
+                    stream=None):
+    """The gradient of layer_norm: dX (of X and of the residual alike), plus dh,
+    the gradient that reaches H past the norm; dweight and dbias (cols values)
+    receive the parameters' gradients. H, mean and rstd are those of the forward
+    call. dX may be dY or dh itself. Returns dX."""
+    st = (_layers or _load_layers()).layer_norm_grad(dY, H, mean, rstd, dX, weight, dh, dweight,
+                                                     dbias, stream)
+    if st:
+        _check(st, "layer_norm_grad")
     return dX

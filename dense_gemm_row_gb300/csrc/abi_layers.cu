@@ -126,62 +126,70 @@ gemm_status_t pointwise(bool bf16, int64_t M, int64_t N, gemm_act_t act, const u
                                 stream));
 }
 
-gemm_status_t norm(bool bf16, bool e4m3, int64_t rows, int64_t cols, float eps, const uint16_t *X,
-                   int64_t ldx, const uint16_t *R, int64_t ldr, const uint16_t *W, uint16_t *H,
-                   int64_t ldh, void *Y, int64_t ldy, float *scale, float *rstd,
-                   cudaStream_t stream) {
+enum class Norm { kRms, kRms8, kLayer };  // 16-bit, 8-bit and 16-bit output
+
+gemm_status_t norm(bool bf16, Norm kind, int64_t rows, int64_t cols, float eps, const uint16_t *X,
+                   int64_t ldx, const uint16_t *R, int64_t ldr, const uint16_t *W,
+                   const uint16_t *B, uint16_t *H, int64_t ldh, void *Y, int64_t ldy, float *scale,
+                   float *mean, float *rstd, cudaStream_t stream) {
+  const bool e4m3 = kind == Norm::kRms8;
   if (!size_ok(rows) || !size_ok(cols) || !(eps >= 0.f)) return GEMM_ERR_INVALID_VALUE;
   if (rows == 0 || cols == 0) return GEMM_OK;
   if (X == nullptr || ldx < cols || Y == nullptr || ldy < cols) return GEMM_ERR_INVALID_VALUE;
   if (e4m3 && scale == nullptr) return GEMM_ERR_INVALID_VALUE;
   if ((R != nullptr && ldr < cols) || (H != nullptr && ldh < cols)) return GEMM_ERR_INVALID_VALUE;
   if (!aligned(X, 2) || !aligned(R, 2) || !aligned(W, 2) || !aligned(H, 2) ||
-      !aligned(Y, e4m3 ? 1 : 2) || !aligned(scale, 4) || !aligned(rstd, 4))
+      !aligned(B, 2) || !aligned(Y, e4m3 ? 1 : 2) || !aligned(scale, 4) || !aligned(mean, 4) ||
+      !aligned(rstd, 4))
     return GEMM_ERR_UNSUPPORTED_LAYOUT;
   const DeviceInfo *dev = nullptr;
   gemm_status_t st = device(&dev);
   if (st != GEMM_OK) return st;
-  RmsCall c;
+  NormCall c;
   c.bf16 = bf16;
   c.rows = static_cast<int>(rows), c.cols = static_cast<int>(cols);
   c.eps = eps;
   c.X = X, c.ldx = ldx;
   c.R = R, c.ldr = ldr;
-  c.W = W;
+  c.W = W, c.B = B;
   c.H = H, c.ldh = ldh;
   c.Y = Y, c.ldy = ldy;
-  c.scale = scale, c.rstd = rstd;
-  return status(launch_rms_norm(*dev, c, stream));
+  c.scale = scale, c.rstd = rstd, c.mean = mean;
+  return status(kind == Norm::kLayer ? launch_layer_norm(*dev, c, stream)
+                                     : launch_rms_norm(*dev, c, stream));
 }
 
-gemm_status_t norm_grad(bool bf16, int64_t rows, int64_t cols, const uint16_t *dY, int64_t lddy,
-                        const uint16_t *H, int64_t ldh, const float *rstd, const uint16_t *W,
-                        const uint16_t *dH, int64_t lddh, uint16_t *dX, int64_t lddx,
-                        uint16_t *dW, cudaStream_t stream) {
+gemm_status_t norm_grad(bool bf16, bool layer, int64_t rows, int64_t cols, const uint16_t *dY,
+                        int64_t lddy, const uint16_t *H, int64_t ldh, const float *mean,
+                        const float *rstd, const uint16_t *W, const uint16_t *dH, int64_t lddh,
+                        uint16_t *dX, int64_t lddx, uint16_t *dW, uint16_t *db,
+                        cudaStream_t stream) {
   if (!size_ok(rows) || !size_ok(cols)) return GEMM_ERR_INVALID_VALUE;
-  if (cols == 0 || (rows == 0 && dW == nullptr)) return GEMM_OK;
+  if (cols == 0 || (rows == 0 && dW == nullptr && db == nullptr)) return GEMM_OK;
   if (rows > 0) {
+    if (layer && mean == nullptr) return GEMM_ERR_INVALID_VALUE;
     if (dY == nullptr || lddy < cols || H == nullptr || ldh < cols || rstd == nullptr ||
         dX == nullptr || lddx < cols || (dH != nullptr && lddh < cols))
       return GEMM_ERR_INVALID_VALUE;
   }
   if (!aligned(dY, 2) || !aligned(H, 2) || !aligned(W, 2) || !aligned(dH, 2) || !aligned(dX, 2) ||
-      !aligned(dW, 2) || !aligned(rstd, 4))
+      !aligned(dW, 2) || !aligned(db, 2) || !aligned(rstd, 4) || !aligned(mean, 4))
     return GEMM_ERR_UNSUPPORTED_LAYOUT;
   const DeviceInfo *dev = nullptr;
   gemm_status_t st = device(&dev);
   if (st != GEMM_OK) return st;
-  RmsGradCall c;
+  NormGradCall c;
   c.bf16 = bf16;
   c.rows = static_cast<int>(rows), c.cols = static_cast<int>(cols);
   c.dY = dY, c.lddy = lddy;
   c.H = H, c.ldh = ldh;
-  c.rstd = rstd;
+  c.rstd = rstd, c.mean = mean;
   c.W = W;
   c.dH = dH, c.lddh = lddh;
   c.dX = dX, c.lddx = lddx;
-  c.dW = dW;
-  return status(launch_rms_norm_grad(*dev, c, stream));
+  c.dW = dW, c.db = db;
+  return status(layer ? launch_layer_norm_grad(*dev, c, stream)
+                      : launch_rms_norm_grad(*dev, c, stream));
 }
 
 }  // namespace
@@ -235,8 +243,8 @@ DGR_ACT_GRAD(gemm_act_grad_f16, false)
   gemm_status_t NAME(int64_t rows, int64_t cols, float eps, const uint16_t *X, int64_t ldx,    \
                      const uint16_t *R, int64_t ldr, const uint16_t *W, uint16_t *H,           \
                      int64_t ldh, uint16_t *Y, int64_t ldy, float *rstd, cudaStream_t stream) { \
-    return dgr::norm(BF16, false, rows, cols, eps, X, ldx, R, ldr, W, H, ldh, Y, ldy, nullptr, \
-                     rstd, stream);                                                            \
+    return dgr::norm(BF16, dgr::Norm::kRms, rows, cols, eps, X, ldx, R, ldr, W, nullptr, H,    \
+                     ldh, Y, ldy, nullptr, nullptr, rstd, stream);                             \
   }
 DGR_NORM(gemm_rms_norm_bf16, true)
 DGR_NORM(gemm_rms_norm_f16, false)
@@ -246,8 +254,8 @@ DGR_NORM(gemm_rms_norm_f16, false)
                      const uint16_t *R, int64_t ldr, const uint16_t *W, uint16_t *H,           \
                      int64_t ldh, uint8_t *Y8, int64_t ldy, float *scale, float *rstd,         \
                      cudaStream_t stream) {                                                    \
-    return dgr::norm(BF16, true, rows, cols, eps, X, ldx, R, ldr, W, H, ldh, Y8, ldy, scale,   \
-                     rstd, stream);                                                            \
+    return dgr::norm(BF16, dgr::Norm::kRms8, rows, cols, eps, X, ldx, R, ldr, W, nullptr, H,   \
+                     ldh, Y8, ldy, scale, nullptr, rstd, stream);                              \
   }
 DGR_NORM8(gemm_rms_norm_bf16_e4m3, true)
 DGR_NORM8(gemm_rms_norm_f16_e4m3, false)
@@ -257,10 +265,32 @@ DGR_NORM8(gemm_rms_norm_f16_e4m3, false)
                      const uint16_t *H, int64_t ldh, const float *rstd, const uint16_t *W,     \
                      const uint16_t *dH, int64_t lddh, uint16_t *dX, int64_t lddx,             \
                      uint16_t *dW, cudaStream_t stream) {                                      \
-    return dgr::norm_grad(BF16, rows, cols, dY, lddy, H, ldh, rstd, W, dH, lddh, dX, lddx, dW, \
-                          stream);                                                             \
+    return dgr::norm_grad(BF16, false, rows, cols, dY, lddy, H, ldh, nullptr, rstd, W, dH,     \
+                          lddh, dX, lddx, dW, nullptr, stream);                                \
   }
 DGR_NORM_GRAD(gemm_rms_norm_grad_bf16, true)
 DGR_NORM_GRAD(gemm_rms_norm_grad_f16, false)
+
+#define DGR_LAYER_NORM(NAME, BF16)                                                             \
+  gemm_status_t NAME(int64_t rows, int64_t cols, float eps, const uint16_t *X, int64_t ldx,    \
+                     const uint16_t *R, int64_t ldr, const uint16_t *W, const uint16_t *b,     \
+                     uint16_t *H, int64_t ldh, uint16_t *Y, int64_t ldy, float *mean,          \
+                     float *rstd, cudaStream_t stream) {                                       \
+    return dgr::norm(BF16, dgr::Norm::kLayer, rows, cols, eps, X, ldx, R, ldr, W, b, H, ldh,   \
+                     Y, ldy, nullptr, mean, rstd, stream);                                     \
+  }
+DGR_LAYER_NORM(gemm_layer_norm_bf16, true)
+DGR_LAYER_NORM(gemm_layer_norm_f16, false)
+
+#define DGR_LAYER_NORM_GRAD(NAME, BF16)                                                        \
+  gemm_status_t NAME(int64_t rows, int64_t cols, const uint16_t *dY, int64_t lddy,             \
+                     const uint16_t *H, int64_t ldh, const float *mean, const float *rstd,     \
+                     const uint16_t *W, const uint16_t *dH, int64_t lddh, uint16_t *dX,        \
+                     int64_t lddx, uint16_t *dW, uint16_t *db, cudaStream_t stream) {          \
+    return dgr::norm_grad(BF16, true, rows, cols, dY, lddy, H, ldh, mean, rstd, W, dH, lddh,   \
+                          dX, lddx, dW, db, stream);                                           \
+  }
+DGR_LAYER_NORM_GRAD(gemm_layer_norm_grad_bf16, true)
+DGR_LAYER_NORM_GRAD(gemm_layer_norm_grad_f16, false)
 
 }  // extern "C"

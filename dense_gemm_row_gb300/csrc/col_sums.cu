@@ -21,9 +21,11 @@ constexpr int kSlots = 32;
 
 template <bool kBf16>
 __global__ void __launch_bounds__(32 * kSlots)
-    col_sums_kernel(const float *part, int parts, int n, int64_t ld, uint16_t *out) {
+    col_sums_kernel(const float *part, int parts, int n, int64_t ld, uint16_t *out, int64_t apart,
+                    uint16_t *out2) {
   __shared__ float red[kSlots][32];
   grid_dependency_wait();
+  if (blockIdx.y != 0) part += apart, out = out2;
   const int j = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
   if (j < n) {
@@ -43,9 +45,10 @@ __global__ void __launch_bounds__(32 * kSlots)
 }  // namespace
 
 cudaError_t launch_col_sums(bool bf16, const float *part, int parts, int n, int64_t ld,
-                            uint16_t *out, cudaStream_t stream) {
+                            uint16_t *out, cudaStream_t stream, int64_t apart, uint16_t *out2) {
+  if (out == nullptr) part += apart, out = out2, out2 = nullptr;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((n - 1) / 32 + 1), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((n - 1) / 32 + 1), out2 ? 2 : 1, 1);
   cfg.blockDim = dim3(32, kSlots, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -53,8 +56,9 @@ cudaError_t launch_col_sums(bool bf16, const float *part, int parts, int n, int6
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return bf16 ? cudaLaunchKernelEx(&cfg, col_sums_kernel<true>, part, parts, n, ld, out)
-              : cudaLaunchKernelEx(&cfg, col_sums_kernel<false>, part, parts, n, ld, out);
+  return bf16 ? cudaLaunchKernelEx(&cfg, col_sums_kernel<true>, part, parts, n, ld, out, apart, out2)
+              : cudaLaunchKernelEx(&cfg, col_sums_kernel<false>, part, parts, n, ld, out, apart,
+                                   out2);
 }
 
 }  // namespace dgr

@@ -228,35 +228,42 @@ cudaError_t launch_act_grad(const DeviceInfo &dev, bool bf16, int M, int N, int 
 
 // out[j] = sum over p of part[p][j] (p in increasing order within a fixed tree;
 // parts rows of n values, row stride ld), rounded to 16 bits (col_sums.cu).
+// With out2, the same of the partial rows `apart` values behind them, in the same
+// launch; either output may be null.
 cudaError_t launch_col_sums(bool bf16, const float *part, int parts, int n, int64_t ld,
-                            uint16_t *out, cudaStream_t stream);
+                            uint16_t *out, cudaStream_t stream, int64_t apart = 0,
+                            uint16_t *out2 = nullptr);
 
-struct RmsCall {
+// The root-mean-square norm (no B, no mean) and the layer norm (no scale).
+struct NormCall {
   bool bf16 = true;
   int rows = 0, cols = 0;
   float eps = 0.f;
-  const uint16_t *X = nullptr, *R = nullptr, *W = nullptr;
+  const uint16_t *X = nullptr, *R = nullptr, *W = nullptr, *B = nullptr;
   int64_t ldx = 0, ldr = 0;
   uint16_t *H = nullptr;
   int64_t ldh = 0;
   void *Y = nullptr;  // 16-bit, or e4m3 when scale is set
   int64_t ldy = 0;
-  float *scale = nullptr, *rstd = nullptr;
+  float *scale = nullptr, *rstd = nullptr, *mean = nullptr;
 };
-cudaError_t launch_rms_norm(const DeviceInfo &dev, const RmsCall &c, cudaStream_t stream);
+cudaError_t launch_rms_norm(const DeviceInfo &dev, const NormCall &c, cudaStream_t stream);
+cudaError_t launch_layer_norm(const DeviceInfo &dev, const NormCall &c, cudaStream_t stream);
 
-struct RmsGradCall {
+struct NormGradCall {
   bool bf16 = true;
   int rows = 0, cols = 0;
   const uint16_t *dY = nullptr, *H = nullptr, *W = nullptr, *dH = nullptr;
   int64_t lddy = 0, ldh = 0, lddh = 0;
-  const float *rstd = nullptr;
+  const float *rstd = nullptr, *mean = nullptr;
   uint16_t *dX = nullptr;
   int64_t lddx = 0;
-  uint16_t *dW = nullptr;
+  uint16_t *dW = nullptr, *db = nullptr;
 };
-cudaError_t launch_rms_norm_grad(const DeviceInfo &dev, const RmsGradCall &c,
+cudaError_t launch_rms_norm_grad(const DeviceInfo &dev, const NormGradCall &c,
                                  cudaStream_t stream);
+cudaError_t launch_layer_norm_grad(const DeviceInfo &dev, const NormGradCall &c,
+                                   cudaStream_t stream);
 
 // K == 0: C = beta * C (C = 0 when beta == 0), M x N window only.
 cudaError_t launch_scale_f32(int M, int N, float beta, float *C, int64_t ldc,

@@ -28,6 +28,8 @@ decltype(&gemm_act_grad_bf16) g_act_grad[2];
 decltype(&gemm_rms_norm_bf16) g_norm[2];
 decltype(&gemm_rms_norm_bf16_e4m3) g_norm8[2];
 decltype(&gemm_rms_norm_grad_bf16) g_norm_grad[2];
+decltype(&gemm_layer_norm_bf16) g_layer_norm[2];
+decltype(&gemm_layer_norm_grad_bf16) g_layer_norm_grad[2];
 
 struct Refused {};  // a Python exception has been set
 
@@ -319,6 +321,58 @@ int rms_norm_grad(PyObject *const *v) {
   });
 }
 
+// (X, Y, weight, bias, residual, h, mean, rstd, eps, stream)
+int layer_norm(PyObject *const *v) {
+  const at::Tensor &X = tensor(v[0], "X"), &Y = tensor(v[1], "Y");
+  const int dev = device_of(X, "X");
+  const int f = format_of(X, "X");
+  const at::ScalarType type = X.scalar_type();
+  if (X.dim() != 2) refuse(PyExc_ValueError, "%s must be 2-D", "X");
+  const int64_t m = X.size(0), n = X.size(1);
+  const Matrix x = matrix(X, "X", m, n, type, dev);
+  const Matrix y = matrix(Y, "Y", m, n, type, dev);
+  void *w = vector_or_none(v[2], "weight", n, type, dev);
+  void *b = vector_or_none(v[3], "bias", n, type, dev);
+  const Matrix r = matrix_or_none(v[4], "residual", m, n, type, dev);
+  const Matrix h = matrix_or_none(v[5], "h", m, n, type, dev);
+  void *mean = vector_or_none(v[6], "mean", m, at::kFloat, dev);
+  void *rstd = vector_or_none(v[7], "rstd", m, at::kFloat, dev);
+  const float eps = number(v[8]);
+  const cudaStream_t s = stream_of(v[9], dev);
+  return unlocked([&] {
+    return g_layer_norm[f](m, n, eps, as<uint16_t>(x.p), x.ld, as<uint16_t>(r.p), r.ld,
+                           as<uint16_t>(w), as<uint16_t>(b), as<uint16_t>(h.p), h.ld,
+                           as<uint16_t>(y.p), y.ld, as<float>(mean), as<float>(rstd), s);
+  });
+}
+
+// (dY, H, mean, rstd, dX, weight, dh, dweight, dbias, stream)
+int layer_norm_grad(PyObject *const *v) {
+  const at::Tensor &dY = tensor(v[0], "dY");
+  const int dev = device_of(dY, "dY");
+  const int f = format_of(dY, "dY");
+  const at::ScalarType type = dY.scalar_type();
+  if (dY.dim() != 2) refuse(PyExc_ValueError, "%s must be 2-D", "dY");
+  const int64_t m = dY.size(0), n = dY.size(1);
+  const Matrix y = matrix(dY, "dY", m, n, type, dev);
+  const Matrix h = matrix(tensor(v[1], "H"), "H", m, n, type, dev);
+  tensor(v[2], "mean"), tensor(v[3], "rstd");
+  void *mean = vector_or_none(v[2], "mean", m, at::kFloat, dev);
+  void *rstd = vector_or_none(v[3], "rstd", m, at::kFloat, dev);
+  const Matrix x = matrix(tensor(v[4], "dX"), "dX", m, n, type, dev);
+  void *w = vector_or_none(v[5], "weight", n, type, dev);
+  const Matrix b = matrix_or_none(v[6], "dh", m, n, type, dev);
+  void *dw = vector_or_none(v[7], "dweight", n, type, dev);
+  void *db = vector_or_none(v[8], "dbias", n, type, dev);
+  const cudaStream_t s = stream_of(v[9], dev);
+  return unlocked([&] {
+    return g_layer_norm_grad[f](m, n, as<uint16_t>(y.p), y.ld, as<uint16_t>(h.p), h.ld,
+                                as<float>(mean), as<float>(rstd), as<uint16_t>(w),
+                                as<uint16_t>(b.p), b.ld, as<uint16_t>(x.p), x.ld,
+                                as<uint16_t>(dw), as<uint16_t>(db), s);
+  });
+}
+
 // A function of exactly kArgs arguments as a Python function returning a status.
 template <int (*kFunction)(PyObject *const *), Py_ssize_t kArgs>
 PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -359,6 +413,10 @@ PyObject *bind(PyObject *, PyObject *args) {
       {"gemm_rms_norm_f16_e4m3", &g_norm8[1]},
       {"gemm_rms_norm_grad_bf16", &g_norm_grad[0]},
       {"gemm_rms_norm_grad_f16", &g_norm_grad[1]},
+      {"gemm_layer_norm_bf16", &g_layer_norm[0]},
+      {"gemm_layer_norm_f16", &g_layer_norm[1]},
+      {"gemm_layer_norm_grad_bf16", &g_layer_norm_grad[0]},
+      {"gemm_layer_norm_grad_f16", &g_layer_norm_grad[1]},
   };
   for (const auto &s : slots) {
     if (std::strcmp(s.name, name) == 0) {
@@ -383,6 +441,8 @@ PyMethodDef g_methods[] = {
     method<act_grad, 6>("act_grad"),
     method<rms_norm, 9>("rms_norm"),
     method<rms_norm_grad, 8>("rms_norm_grad"),
+    method<layer_norm, 10>("layer_norm"),
+    method<layer_norm_grad, 10>("layer_norm_grad"),
     {"bind", bind, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

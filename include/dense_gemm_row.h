@@ -458,6 +458,56 @@ GEMM_API gemm_status_t gemm_rms_norm_grad_f16(int64_t rows, int64_t cols, const 
                                               const gemm_f16_t *dH, int64_t lddh, gemm_f16_t *dX,
                                               int64_t lddx, gemm_f16_t *dW, cudaStream_t stream);
 
+/*
+ * gemm_layer_norm_bf16, gemm_layer_norm_f16 -- layer norm of each row, with the
+ * residual's addition:
+ *
+ *     H = X + R,   mean_i = mean_j H_ij,   rstd_i = (mean_j (H_ij - mean_i)^2 + eps)^(-1/2)
+ *     Y_ij = (H_ij - mean_i) rstd_i W_j + b_j
+ *
+ * R, H, W (1), b (0), mean and rstd (rows fp32 values each) may be NULL. The
+ * statistics and Y are those of the unrounded sum; the squares are summed about
+ * the mean, so a large mean costs no accuracy. Aliasing as gemm_rms_norm_bf16;
+ * eps >= 0. A row of equal values with eps == 0 gives NaN, as the formula does.
+ *
+ * gemm_layer_norm_grad_bf16, gemm_layer_norm_grad_f16 -- the gradient. From dY,
+ * the H, mean and rstd of the forward call, and W (NULL: 1):
+ *
+ *     n_ij = (H_ij - mean_i) rstd_i,   g_ij = dY_ij W_j
+ *     dX_ij = rstd_i (g_ij - mean_k(g_ik) - n_ij mean_k(g_ik n_ik)) + dH_ij
+ *     dW_j = sum_i dY_ij n_ij,   db_j = sum_i dY_ij
+ *
+ * dH, dW and db may each be NULL. dX may be the same matrix as dY or dH. dW and
+ * db are summed in fp32 in a fixed order; rows == 0 gives zeros. Any layout.
+ */
+GEMM_API gemm_status_t gemm_layer_norm_bf16(int64_t rows, int64_t cols, float eps,
+                                            const gemm_bf16_t *X, int64_t ldx,
+                                            const gemm_bf16_t *R, int64_t ldr,
+                                            const gemm_bf16_t *W, const gemm_bf16_t *b,
+                                            gemm_bf16_t *H, int64_t ldh, gemm_bf16_t *Y,
+                                            int64_t ldy, float *mean, float *rstd,
+                                            cudaStream_t stream);
+GEMM_API gemm_status_t gemm_layer_norm_f16(int64_t rows, int64_t cols, float eps,
+                                           const gemm_f16_t *X, int64_t ldx, const gemm_f16_t *R,
+                                           int64_t ldr, const gemm_f16_t *W, const gemm_f16_t *b,
+                                           gemm_f16_t *H, int64_t ldh, gemm_f16_t *Y, int64_t ldy,
+                                           float *mean, float *rstd, cudaStream_t stream);
+GEMM_API gemm_status_t gemm_layer_norm_grad_bf16(int64_t rows, int64_t cols,
+                                                 const gemm_bf16_t *dY, int64_t lddy,
+                                                 const gemm_bf16_t *H, int64_t ldh,
+                                                 const float *mean, const float *rstd,
+                                                 const gemm_bf16_t *W, const gemm_bf16_t *dH,
+                                                 int64_t lddh, gemm_bf16_t *dX, int64_t lddx,
+                                                 gemm_bf16_t *dW, gemm_bf16_t *db,
+                                                 cudaStream_t stream);
+GEMM_API gemm_status_t gemm_layer_norm_grad_f16(int64_t rows, int64_t cols, const gemm_f16_t *dY,
+                                                int64_t lddy, const gemm_f16_t *H, int64_t ldh,
+                                                const float *mean, const float *rstd,
+                                                const gemm_f16_t *W, const gemm_f16_t *dH,
+                                                int64_t lddh, gemm_f16_t *dX, int64_t lddx,
+                                                gemm_f16_t *dW, gemm_f16_t *db,
+                                                cudaStream_t stream);
+
 /* A constant, human-readable name for a status. Never NULL. */
 GEMM_API const char *gemm_status_string(gemm_status_t status);
 

@@ -95,6 +95,26 @@ def rms_norm_grad(dY, H, rstd, W=None, dH=None):
     return (dx if dH is None else dx + dH), (dY * n).sum(axis=0)
 
 
+def layer_norm(X, W=None, b=None, residual=None, eps=0.0):
+    """(Y, H, mean, rstd)."""
+    h = X if residual is None else X + residual
+    mean = h.mean(axis=1)
+    c = h - mean[:, None]
+    rstd = 1.0 / np.sqrt((c * c).mean(axis=1) + eps)
+    y = c * rstd[:, None]
+    y = y if W is None else y * W[None, :]
+    return (y if b is None else y + b[None, :]), h, mean, rstd
+
+
+def layer_norm_grad(dY, H, mean, rstd, W=None, dH=None):
+    """(dX, dW, db)."""
+    n = (H - mean[:, None]) * rstd[:, None]
+    g = dY if W is None else dY * W[None, :]
+    dx = rstd[:, None] * (g - g.mean(axis=1, keepdims=True)
+                          - n * (g * n).mean(axis=1, keepdims=True))
+    return (dx if dH is None else dx + dH), (dY * n).sum(axis=0), dY.sum(axis=0)
+
+
 def round_e4m3(x):
     """x rounded to the e4m3 grid, ties to even, saturating at 448."""
     x = np.asarray(x, dtype=np.float64)

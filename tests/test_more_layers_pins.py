@@ -1,0 +1,45 @@
+"""The float64 definitions of the gated layer, the block-scaled products and the
+layer norm (oracle/layers.py), pinned by closed forms and central differences."""
+import numpy as np
+import pytest
+
+from oracle import layers as L
+
+
+def differences(loss, args, grads, h=1e-4, atol=2e-6):
+    """grads[i] is the gradient of loss(*args) at args[i]."""
+    for put, grad in enumerate(grads):
+        for i in np.ndindex(args[put].shape):
+            up, down = ([a.copy() for a in args] for _ in range(2))
+            up[put][i] += h
+            down[put][i] -= h
+            assert grad[i] == pytest.approx((loss(*up) - loss(*down)) / (2 * h), abs=atol)
+
+
+def test_layer_norm_closed_forms():
+    y, h, m, s = L.layer_norm(np.array([[1.0, 3.0, 1.0, 3.0]]))
+    np.testing.assert_allclose(y, [[-1, 1, -1, 1]], atol=1e-15)
+    assert m[0] == 2 and s[0] == pytest.approx(1)
+    x = np.random.default_rng(0).standard_normal((5, 33))
+    y, h, _, _ = L.layer_norm(x, residual=x)
+    np.testing.assert_array_equal(h, 2 * x)
+    np.testing.assert_allclose(y.mean(1), 0, atol=1e-14)
+    np.testing.assert_allclose((y * y).mean(1), 1, atol=1e-12)
+    np.testing.assert_allclose(L.layer_norm(7 * x + 3)[0], y, atol=1e-12)  # scale and shift
+    w, b = np.arange(33.0), np.linspace(-1, 1, 33)
+    np.testing.assert_allclose(L.layer_norm(x, w, b)[0], y * w + b, atol=1e-12)
+
+
+@pytest.mark.parametrize("gain", [False, True])
+def test_layer_norm_grad_matches_differences(gain):
+    r = np.random.default_rng(5)
+    X, R, G, E = (r.standard_normal((3, 7)) for _ in range(4))
+    W, b = (r.standard_normal(7) for _ in range(2))
+
+    def loss(X, b, W=W):
+        y, h, _, _ = L.layer_norm(X, W if gain else None, b, R, 0.1)
+        return (G * y).sum() + (E * h).sum()  # E: the gradient past the norm
+
+    _, H, m, s = L.layer_norm(X, W if gain else None, b, R, 0.1)
+    dx, dw, db = L.layer_norm_grad(G, H, m, s, W if gain else None, E)
+    differences(loss, [X, b, W], [dx, db, dw] if gain else [dx, db])
