@@ -25,6 +25,7 @@ or one expanded along the batch with stride 0, is shared by every entry).
 The linear-layer operators have one function each for CUDA tensors:
 ``gemm_epilogue`` (a product with bias, activation and residual in its
 epilogue), ``gemm_dact`` and ``act_grad`` (the gradient at the pre-activation),
+``gemm_gated`` (two projections and their gated product), ``gemm_gated_dact``,
 ``rms_norm``, ``layer_norm`` and their gradients ``rms_norm_grad`` and
 ``layer_norm_grad``. The dtypes pick the C entry point. They
 check shapes, dtypes, strides and devices before the call and write into the
@@ -58,6 +59,7 @@ EXPORTED = ("gemm_f32", "gemm_bf16", "gemm_f16", "gemm_s8", "gemm_u8", "gemm_f16
             "gemm_bf16_dact", "gemm_f16_dact", "gemm_act_grad_bf16", "gemm_act_grad_f16",
             "gemm_rms_norm_bf16", "gemm_rms_norm_f16", "gemm_rms_norm_bf16_e4m3",
             "gemm_rms_norm_f16_e4m3", "gemm_rms_norm_grad_bf16", "gemm_rms_norm_grad_f16",
+            "gemm_bf16_gated", "gemm_f16_gated", "gemm_bf16_gated_dact", "gemm_f16_gated_dact",
             "gemm_layer_norm_bf16", "gemm_layer_norm_f16", "gemm_layer_norm_grad_bf16",
             "gemm_layer_norm_grad_f16")
 
@@ -129,6 +131,10 @@ def _load():
                                           vp, vp, vp],
             f"gemm_rms_norm_grad_{fmt}": [i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64,
                                           vp, vp],
+            f"gemm_{fmt}_gated": [op, op, i64, i64, i64, f32, vp, i64, vp, i64, vp, i64, op, vp,
+                                  vp, vp, i64, vp, i64, vp, i64, vp],
+            f"gemm_{fmt}_gated_dact": [op, op, i64, i64, i64, f32, vp, i64, vp, i64, op, vp, i64,
+                                       vp, i64, vp, i64, vp, i64, vp, vp, vp],
             f"gemm_layer_norm_{fmt}": [i64, i64, f32, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64,
                                        vp, vp, vp],
             f"gemm_layer_norm_grad_{fmt}": [i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp,
@@ -378,7 +384,7 @@ def _load_layers():
     import torch  # noqa: F401  (the module links against torch's libraries)
     mod = importlib.import_module("dense_gemm_row_gb300._layers")
     for name in EXPORTED:
-        if any(part in name for part in ("_epi", "dact", "act_grad", "_norm")):
+        if any(part in name for part in ("_epi", "gated", "dact", "act_grad", "_norm")):
             mod.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
     _layers = mod
     return mod
@@ -454,6 +460,36 @@ def rms_norm_grad(dY, H, rstd, dX, *, weight=None, dh=None, dweight=None, stream
     if st:
         _check(st, "rms_norm_grad")
     return dX
+
+
+def gemm_gated(A, Bg, Bu, D, *, act="silu", alpha=1.0, bias_gate=None, bias_up=None, gate=None,
+               up=None, trans_a=False, trans_b=False, stream=None):
+    """D = act(G) * U with G = alpha * op(A) * op(Bg) + bias_gate and
+    U = alpha * op(A) * op(Bu) + bias_up, in one kernel; returns D.
+
+    A is M x K (K x M with trans_a), Bg and Bu are K x N (N x K with trans_b), D
+    M x N; all are bfloat16 or float16. bias_gate and bias_up (N values each) may be
+    None; gate and up (M x N), when given, receive G and U for gemm_gated_dact. Bg
+    and Bu may be parts of one matrix. Layouts as gemm_epilogue."""
+    st = (_layers or _load_layers()).gemm_gated(A, Bg, Bu, D, act, alpha, bias_gate, bias_up,
+                                                gate, up, trans_a, trans_b, stream)
+    if st:
+        _check(st, "gemm_gated")
+    return D
+
+
+def gemm_gated_dact(A, B, G, U, dG, dU, *, act="silu", alpha=1.0, dbias_gate=None, dbias_up=None,
+                    trans_a=False, trans_b=False, stream=None):
+    """The gradient of gemm_gated at its projections, from the product
+    dD = alpha * op(A) * op(B) that carries it back (A the next layer's output
+    gradient, B its weights): dG = dD * U * act'(G), dU = dD * act(G), and their
+    column sums dbias_gate and dbias_up (N values each, either may be None). G and U
+    are what gemm_gated stored; dG may be G itself, dU U. Returns (dG, dU)."""
+    st = (_layers or _load_layers()).gemm_gated_dact(A, B, G, U, dG, dU, act, alpha, dbias_gate,
+                                                     dbias_up, trans_a, trans_b, stream)
+    if st:
+        _check(st, "gemm_gated_dact")
+    return dG, dU
 
 
 def layer_norm(X, Y, *, weight=None, bias=None, residual=None, h=None, mean=None, rstd=None,

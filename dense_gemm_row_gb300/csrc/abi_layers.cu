@@ -30,30 +30,40 @@ gemm_status_t product(bool e4m3, gemm_op_t opA, gemm_op_t opB, int64_t M, int64_
                       gemm_act_t act, cudaStream_t stream) {
   if (!op_ok(opA) || !op_ok(opB) || !act_ok(act)) return GEMM_ERR_INVALID_VALUE;
   if (!size_ok(M) || !size_ok(N) || !size_ok(K)) return GEMM_ERR_INVALID_VALUE;
-  if (N == 0 || (M == 0 && c.dbias == nullptr)) return GEMM_OK;
+  if (N == 0 || (M == 0 && c.dbias == nullptr && c.dbias2 == nullptr)) return GEMM_OK;
   const bool a_t = opA == GEMM_OP_T, b_t = opB == GEMM_OP_T;
   if (M > 0) {
     if (c.D == nullptr || c.ldd < N) return GEMM_ERR_INVALID_VALUE;
     if (c.R != nullptr && c.ldr < N) return GEMM_ERR_INVALID_VALUE;
     if (c.Z != nullptr && c.ldz < N) return GEMM_ERR_INVALID_VALUE;
     if (c.grad && act != GEMM_ACT_NONE && c.R == nullptr) return GEMM_ERR_INVALID_VALUE;
+    if (c.gated && c.grad && (c.R == nullptr || c.R2 == nullptr || c.ldr2 < N ||
+                              c.D2 == nullptr || c.ldd2 < N))
+      return GEMM_ERR_INVALID_VALUE;
+    if (c.Z2 != nullptr && c.ldz2 < N) return GEMM_ERR_INVALID_VALUE;
     if (K > 0) {
       if (A == nullptr || lda < (a_t ? M : K)) return GEMM_ERR_INVALID_VALUE;
       if (B == nullptr || ldb < (b_t ? K : N)) return GEMM_ERR_INVALID_VALUE;
       const int unit = e4m3 ? 16 : 8;
       if (!aligned(A, 16) || !aligned(B, 16) || lda % unit || ldb % unit)
         return GEMM_ERR_UNSUPPORTED_LAYOUT;
+      if (c.gated && !c.grad) {
+        if (c.B2 == nullptr || c.ldb2 < (b_t ? K : N)) return GEMM_ERR_INVALID_VALUE;
+        if (!aligned(c.B2, 16) || c.ldb2 % unit) return GEMM_ERR_UNSUPPORTED_LAYOUT;
+      }
     }
   }
   if (!aligned(c.bias, 2) || !aligned(c.R, 2) || !aligned(c.Z, 2) || !aligned(c.D, 2) ||
-      !aligned(c.dbias, 2) || !aligned(c.scale_a, 4) || !aligned(c.scale_b, 4))
+      !aligned(c.dbias, 2) || !aligned(c.scale_a, 4) || !aligned(c.scale_b, 4) ||
+      !aligned(c.bias2, 2) || !aligned(c.R2, 2) || !aligned(c.Z2, 2) || !aligned(c.D2, 2) ||
+      !aligned(c.dbias2, 2))
     return GEMM_ERR_UNSUPPORTED_LAYOUT;
   const DeviceInfo *dev = nullptr;
   gemm_status_t st = device(&dev);
   if (st != GEMM_OK) return st;
   if (M == 0)
     return status(
-        launch_col_sums(c.bf16, nullptr, 0, static_cast<int>(N), N, c.dbias, stream));
+        launch_col_sums(c.bf16, nullptr, 0, static_cast<int>(N), N, c.dbias, stream, 0, c.dbias2));
   c.act = static_cast<int>(act);
   return status(launch_gemm_epi(*dev, e4m3, a_t, b_t, static_cast<int>(M), static_cast<int>(N),
                                 static_cast<int>(K), A, lda, B, ldb, c, stream));
@@ -100,6 +110,41 @@ gemm_status_t gradient(bool bf16, gemm_op_t opA, gemm_op_t opB, int64_t M, int64
   if (act != GEMM_ACT_NONE) c.R = Z, c.ldr = ldz;
   c.D = dZ, c.ldd = lddz;
   c.dbias = dbias;
+  return product(false, opA, opB, M, N, K, A, lda, B, ldb, c, act, stream);
+}
+
+gemm_status_t gated(bool bf16, gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N, int64_t K,
+                    float alpha, const uint16_t *A, int64_t lda, const uint16_t *Bg, int64_t ldbg,
+                    const uint16_t *Bu, int64_t ldbu, gemm_act_t act, const uint16_t *bias_g,
+                    const uint16_t *bias_u, uint16_t *G, int64_t ldg, uint16_t *U, int64_t ldu,
+                    uint16_t *D, int64_t ldd, cudaStream_t stream) {
+  EpiCall c;
+  c.bf16 = bf16;
+  c.gated = true;
+  c.alpha = alpha;
+  c.B2 = Bu, c.ldb2 = ldbu;
+  c.bias = bias_g, c.bias2 = bias_u;
+  c.Z = G, c.ldz = ldg;
+  c.Z2 = U, c.ldz2 = ldu;
+  c.D = D, c.ldd = ldd;
+  return product(false, opA, opB, M, N, K, A, lda, Bg, ldbg, c, act, stream);
+}
+
+gemm_status_t gated_gradient(bool bf16, gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N,
+                             int64_t K, float alpha, const uint16_t *A, int64_t lda,
+                             const uint16_t *B, int64_t ldb, gemm_act_t act, const uint16_t *G,
+                             int64_t ldg, const uint16_t *U, int64_t ldu, uint16_t *dG,
+                             int64_t lddg, uint16_t *dU, int64_t lddu, uint16_t *dbias_g,
+                             uint16_t *dbias_u, cudaStream_t stream) {
+  EpiCall c;
+  c.bf16 = bf16;
+  c.grad = c.gated = true;
+  c.alpha = alpha;
+  c.R = G, c.ldr = ldg;
+  c.R2 = U, c.ldr2 = ldu;
+  c.D = dG, c.ldd = lddg;
+  c.D2 = dU, c.ldd2 = lddu;
+  c.dbias = dbias_g, c.dbias2 = dbias_u;
   return product(false, opA, opB, M, N, K, A, lda, B, ldb, c, act, stream);
 }
 
@@ -229,6 +274,30 @@ DGR_EPI8(gemm_e4m3_f16_epi, false)
   }
 DGR_DACT(gemm_bf16_dact, true)
 DGR_DACT(gemm_f16_dact, false)
+
+#define DGR_GATED(NAME, BF16)                                                                   \
+  gemm_status_t NAME(gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N, int64_t K, float alpha, \
+                     const uint16_t *A, int64_t lda, const uint16_t *Bg, int64_t ldbg,          \
+                     const uint16_t *Bu, int64_t ldbu, gemm_act_t act, const uint16_t *bias_g,  \
+                     const uint16_t *bias_u, uint16_t *G, int64_t ldg, uint16_t *U, int64_t ldu, \
+                     uint16_t *D, int64_t ldd, cudaStream_t stream) {                           \
+    return dgr::gated(BF16, opA, opB, M, N, K, alpha, A, lda, Bg, ldbg, Bu, ldbu, act, bias_g,  \
+                      bias_u, G, ldg, U, ldu, D, ldd, stream);                                  \
+  }
+DGR_GATED(gemm_bf16_gated, true)
+DGR_GATED(gemm_f16_gated, false)
+
+#define DGR_GATED_DACT(NAME, BF16)                                                              \
+  gemm_status_t NAME(gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N, int64_t K, float alpha, \
+                     const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb,            \
+                     gemm_act_t act, const uint16_t *G, int64_t ldg, const uint16_t *U,         \
+                     int64_t ldu, uint16_t *dG, int64_t lddg, uint16_t *dU, int64_t lddu,       \
+                     uint16_t *dbias_g, uint16_t *dbias_u, cudaStream_t stream) {               \
+    return dgr::gated_gradient(BF16, opA, opB, M, N, K, alpha, A, lda, B, ldb, act, G, ldg, U,  \
+                               ldu, dG, lddg, dU, lddu, dbias_g, dbias_u, stream);              \
+  }
+DGR_GATED_DACT(gemm_bf16_gated_dact, true)
+DGR_GATED_DACT(gemm_f16_gated_dact, false)
 
 #define DGR_ACT_GRAD(NAME, BF16)                                                               \
   gemm_status_t NAME(int64_t M, int64_t N, gemm_act_t act, const uint16_t *dD, int64_t lddd,   \

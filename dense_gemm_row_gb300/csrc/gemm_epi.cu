@@ -30,6 +30,19 @@ cudaError_t launch_split_fwd8(const DeviceInfo &dev, int mp, bool b_t, int M, in
 cudaError_t launch_split_grad(const DeviceInfo &dev, int mp, bool b_t, int M, int N, int K,
                               const void *A, int64_t lda, const void *B, int64_t ldb,
                               const EpiCall &epi, float *part, cudaStream_t stream);
+// The gated layer's and its gradient's (gemm_gated_*.cu).
+cudaError_t launch_gated_fwd(const DeviceInfo &dev, bool a_t, bool b_t, int M, int N, int K,
+                             const void *A, int64_t lda, const void *B, int64_t ldb,
+                             const EpiCall &epi, cudaStream_t stream);
+cudaError_t launch_gated_grad(const DeviceInfo &dev, int tile_n, bool a_t, bool b_t, int M, int N,
+                              int K, const void *A, int64_t lda, const void *B, int64_t ldb,
+                              const EpiCall &epi, float *part, cudaStream_t stream);
+cudaError_t launch_gated_split_fwd(const DeviceInfo &dev, int mp, bool b_t, int M, int N, int K,
+                                   const void *A, int64_t lda, const void *B, int64_t ldb,
+                                   const EpiCall &epi, float *part, cudaStream_t stream);
+cudaError_t launch_gated_split_grad(const DeviceInfo &dev, int mp, bool b_t, int M, int N, int K,
+                                    const void *A, int64_t lda, const void *B, int64_t ldb,
+                                    const EpiCall &epi, float *part, cudaStream_t stream);
 
 namespace {
 
@@ -45,9 +58,15 @@ __global__ void epi_empty_kernel(int M, int N, const EpiCall c) {
       const float z = c.bias ? from16<kBf16>(c.bias[j]) : 0.f;
       if (c.Z) c.Z[r * c.ldz + j] = to16<kBf16>(z);
       with_act(c.act, [&](auto a) { d = act_value<decltype(a)::value>(z); });
+      if (c.gated) {
+        const float z2 = c.bias2 ? from16<kBf16>(c.bias2[j]) : 0.f;
+        if (c.Z2) c.Z2[r * c.ldz2 + j] = to16<kBf16>(z2);
+        d *= z2;
+      }
       if (c.R) d += from16<kBf16>(c.R[r * c.ldr + j]);
     }
     c.D[r * c.ldd + j] = to16<kBf16>(d);
+    if (c.D2) c.D2[r * c.ldd2 + j] = to16<kBf16>(d);
   }
 }
 
@@ -56,8 +75,8 @@ cudaError_t launch_empty(int M, int N, const EpiCall &epi, cudaStream_t stream) 
   auto kern = epi.bf16 ? epi_empty_kernel<true> : epi_empty_kernel<false>;
   kern<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(M, N, epi);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && epi.dbias != nullptr)
-    e = launch_col_sums(epi.bf16, nullptr, 0, N, N, epi.dbias, stream);
+  if (e == cudaSuccess && (epi.dbias != nullptr || epi.dbias2 != nullptr))
+    e = launch_col_sums(epi.bf16, nullptr, 0, N, N, epi.dbias, stream, 0, epi.dbias2);
   return e;
 }
 
@@ -79,11 +98,13 @@ struct EpiPlan {
   int split_rows;  // rows per token tile of the few-rows kernel, or 0
   int tile_n;      // columns per tile otherwise
 };
-EpiPlan plan_epi(const DeviceInfo &dev, bool a_t, int M, int N, int KB, bool ragged) {
+EpiPlan plan_epi(const DeviceInfo &dev, bool a_t, int M, int64_t N, int KB, bool ragged,
+                 bool pair) {
   const int64_t pairs = std::max(dev.sm_count / 2, 1);
   const int64_t rows = (static_cast<int64_t>(M) + 255) / 256;
-  const int64_t t256 = rows * ((static_cast<int64_t>(N) + 255) / 256);
-  const int64_t t128 = rows * ((static_cast<int64_t>(N) + 127) / 128);
+  if (pair) N *= 2;
+  const int64_t t256 = rows * ((N + 255) / 256);
+  const int64_t t128 = rows * ((N + 127) / 128);
   const int64_t idle = pairs / t128;
   EpiPlan plan{0, 256};
   // The few-rows kernel's token tiles are K-major.
@@ -102,8 +123,13 @@ cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t
                             const EpiCall &epi, cudaStream_t stream) {
   if (K == 0) return launch_empty(M, N, epi, stream);
   const bool ragged = N % 8 != 0 || epi.ldd % 8 != 0 || reinterpret_cast<uintptr_t>(epi.D) % 16 != 0;
-  const EpiPlan plan = plan_epi(dev, a_t, M, N, (K - 1) / (e4m3 ? 128 : 64) + 1, ragged);
+  // A gated layer is a product of twice the columns, in 256-wide tiles only.
+  const EpiPlan plan = plan_epi(dev, a_t, M, N, (K - 1) / (e4m3 ? 128 : 64) + 1, ragged,
+                                epi.gated && !epi.grad);
   const int mp = plan.split_rows, tile_n = plan.tile_n;
+  if (epi.gated && !epi.grad)
+    return mp ? launch_gated_split_fwd(dev, mp, b_t, M, N, K, A, lda, B, ldb, epi, nullptr, stream)
+              : launch_gated_fwd(dev, a_t, b_t, M, N, K, A, lda, B, ldb, epi, stream);
   if (!epi.grad) {
     if (e4m3)
       return mp ? launch_split_fwd8(dev, mp, true, M, N, K, A, lda, B, ldb, epi, nullptr, stream)
@@ -113,24 +139,27 @@ cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t
   }
   // Gradient: partial column sums, one row per token tile or per 32 rows of D. A
   // single token tile's kernel writes dbias itself.
+  auto split = epi.gated ? launch_gated_split_grad : launch_split_grad;
+  auto tiles = epi.gated ? launch_gated_grad : launch_epi_grad;
   if (mp && M <= mp)
-    return launch_split_grad(dev, mp, b_t, M, N, K, A, lda, B, ldb, epi, nullptr, stream);
+    return split(dev, mp, b_t, M, N, K, A, lda, B, ldb, epi, nullptr, stream);
   const int parts = static_cast<int>((static_cast<int64_t>(M) + (mp ? mp : 32) - 1) / (mp ? mp : 32));
   void *part = nullptr;
-  if (epi.dbias != nullptr) {
+  if (epi.dbias != nullptr || epi.dbias2 != nullptr) {
     cudaMemPool_t pool;
     cudaError_t e = device_pool(dev, &pool);
     if (e != cudaSuccess) return e;
-    e = cudaMallocFromPoolAsync(&part, static_cast<size_t>(parts) * N * 4, pool, stream);
+    e = cudaMallocFromPoolAsync(&part, static_cast<size_t>(epi.gated ? 2 : 1) * parts * N * 4, pool,
+                                stream);
     if (e != cudaSuccess) return e;
   }
   float *sums = static_cast<float *>(part);
-  cudaError_t e = mp ? launch_split_grad(dev, mp, b_t, M, N, K, A, lda, B, ldb, epi, sums, stream)
-                     : launch_epi_grad(dev, tile_n, a_t, b_t, M, N, K, A, lda, B, ldb, epi, sums,
-                                       stream);
+  cudaError_t e = mp ? split(dev, mp, b_t, M, N, K, A, lda, B, ldb, epi, sums, stream)
+                     : tiles(dev, tile_n, a_t, b_t, M, N, K, A, lda, B, ldb, epi, sums, stream);
   if (part != nullptr) {
     if (e == cudaSuccess)
-      e = launch_col_sums(epi.bf16, sums, parts, N, N, epi.dbias, stream);
+      e = launch_col_sums(epi.bf16, sums, parts, N, N, epi.dbias, stream,
+                          static_cast<int64_t>(parts) * N, epi.dbias2);
     cudaError_t f = cudaFreeAsync(part, stream);
     if (e == cudaSuccess) e = f;
   }

@@ -15,6 +15,9 @@
 //
 // Operands: A (tokens) as stored M x K; B stored N x K (K-major) or K x N
 // (N-major, 16-bit only); 16-bit or e4m3.
+//
+// A gated layer's tile has 64 columns of D: the MMA's rows are those of the first
+// B, then the same ones of the second, and a finishing thread adds both.
 #pragma once
 
 #include "epi.cuh"
@@ -68,6 +71,10 @@ struct __align__(1024) SplitSmem {
   int abort;
 };
 
+struct NoSecond {};
+template <bool kPair>
+using SplitMap = std::conditional_t<kPair, CUtensorMap, NoSecond>;
+
 struct SplitArgs {
   int M, N, K;
   int mp;       // rows of a token tile: min(M, kMP) rounded up to 16 (the MMA's N)
@@ -75,9 +82,11 @@ struct SplitArgs {
   int cl;
   bool b_t;     // B stored N x K
   bool r_vec, d_vec, z_vec;  // rows of R / D / Z in whole 8-byte units
+  bool r2_vec, d2_vec, z2_vec;
   uint32_t idesc;
   uint32_t *err_word;
   float *part;  // gradient, several token tiles: column sums of each [tiles_m][N]
+                // (gated: dU's behind dG's)
   EpiCall c;
 };
 
@@ -180,13 +189,95 @@ __device__ __forceinline__ void split_finish(const SplitArgs &p, uint32_t red, i
   }
 }
 
-template <bool kE4m3, int kMP, bool kGrad>
+// The same for a gated layer (forward: the projections are kSplitN / 2 columns apart)
+// and its gradient. One row's loads are a row ahead there, of G and U.
+struct GatedCols {
+  uint32_t bias[2][4];
+};
+struct GatedRow {
+  uint2 g, u;
+};
+template <bool kGrad>
+__device__ __forceinline__ void gated_load_row(const SplitArgs &p, int64_t row, int col,
+                                               GatedRow &k) {
+  k.g = k.u = make_uint2(0, 0);
+  if (!kGrad || row >= p.M || col >= p.N) return;
+  k.g = load4(p.c.R + row * p.c.ldr + col, p.r_vec, p.N - col);
+  k.u = load4(p.c.R2 + row * p.c.ldr2 + col, p.r2_vec, p.N - col);
+}
+__device__ __forceinline__ void split_add(const SplitArgs &p, uint32_t off, float (&v)[4]) {
+  float4 s[kSplitMaxCl];
+#pragma unroll
+  for (int q = 0; q < kSplitMaxCl; ++q)
+    if (q < p.cl) s[q] = ld_dsmem_f4(mapa_shared(off, static_cast<uint32_t>(q)));
+  v[0] = v[1] = v[2] = v[3] = 0.f;
+#pragma unroll
+  for (int q = 0; q < kSplitMaxCl; ++q)  // CTA order: one fixed order per element
+    if (q < p.cl) v[0] += s[q].x, v[1] += s[q].y, v[2] += s[q].z, v[3] += s[q].w;
+}
+template <bool kGrad, bool kBf16, int kAct>
+__device__ __forceinline__ void gated_finish(const SplitArgs &p, uint32_t red, int t, int wq,
+                                             int lc, int m0, int col, const GatedCols &cols,
+                                             GatedRow next, float (&sum)[2][4]) {
+  const int step = kSplitFinish / wq;
+  const int rows = min(p.M - m0, p.mp), left = p.N - col;
+  if (left <= 0) return;
+  auto pack = [](const float (&v)[4]) {
+    return make_uint2(pack16<kBf16>(v[0], v[1]), pack16<kBf16>(v[2], v[3]));
+  };
+  for (int m = t / wq; m < rows; m += step) {
+    const int64_t row = m0 + m;
+    const GatedRow now = next;
+    const uint32_t off = red + static_cast<uint32_t>((m * kSplitN + lc) * 4);
+    float g[4], u[4];
+    if constexpr (!kGrad) {
+      split_add(p, off, g);
+      split_add(p, off + kSplitN / 2 * 4, u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        g[e] = fmaf(g[e], p.c.alpha, from16<kBf16>(cols.bias[0][e]));
+        u[e] = fmaf(u[e], p.c.alpha, from16<kBf16>(cols.bias[1][e]));
+      }
+      if (p.c.Z) store4(p.c.Z + row * p.c.ldz + col, p.z_vec, left, pack(g));
+      if (p.c.Z2) store4(p.c.Z2 + row * p.c.ldz2 + col, p.z2_vec, left, pack(u));
+#pragma unroll
+      for (int e = 0; e < 4; e += 2)
+        split(mul2(act_value2<kAct>(f2(g[e], g[e + 1])), f2(u[e], u[e + 1])), g[e], g[e + 1]);
+      store4(p.c.D + row * p.c.ldd + col, p.d_vec, left, pack(g));
+    } else {
+      float d[4], dg[4], du[4];
+      split_add(p, off, d);
+      if (m + step < rows) gated_load_row<kGrad>(p, row + step, col, next);
+      unpack16<kBf16>(now.g.x, g[0], g[1]);
+      unpack16<kBf16>(now.g.y, g[2], g[3]);
+      unpack16<kBf16>(now.u.x, u[0], u[1]);
+      unpack16<kBf16>(now.u.y, u[2], u[3]);
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const F2 d2 = mul2(f2(d[e], d[e + 1]), f2(p.c.alpha));
+        split(mul2(mul2(d2, f2(u[e], u[e + 1])), act_slope2<kAct>(g[e], g[e + 1])), dg[e],
+              dg[e + 1]);
+        split(mul2(d2, act_value2<kAct>(f2(g[e], g[e + 1]))), du[e], du[e + 1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[0][e] += dg[e], sum[1][e] += du[e];
+      store4(p.c.D + row * p.c.ldd + col, p.d_vec, left, pack(dg));
+      store4(p.c.D2 + row * p.c.ldd2 + col, p.d2_vec, left, pack(du));
+    }
+  }
+}
+
+// tmS: a gated layer's second B.
+template <bool kE4m3, int kMP, bool kGrad, bool kGated>
 __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     gemm_epi_split_kernel(const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ CUtensorMap tmB,
+                          const __grid_constant__ SplitMap<kGated && !kGrad> tmS,
                           const __grid_constant__ SplitArgs p) {
   using Cf = SplitCfg<kMP>;
   constexpr int kBK = kE4m3 ? 128 : 64;
+  constexpr bool kPair = kGated && !kGrad;
+  constexpr int kCols = kPair ? kSplitN / 2 : kSplitN;  // of D in a tile
   extern __shared__ uint8_t smem_raw[];
   SplitSmem<kMP> &sm = *reinterpret_cast<SplitSmem<kMP> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -206,6 +297,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     fence_mbar_init();
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
+    if constexpr (kPair) prefetch_tmap(&tmS);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&sm.tmem_base), Cf::kTmem);
@@ -223,18 +315,20 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   // Token tiles of one column block are neighbours, so its weights are read
   // from memory once and found in L2 by the others.
   const int tile = static_cast<int>(blockIdx.x) / cl;
-  const int n0 = tile / p.tiles_m * kSplitN, m0 = tile % p.tiles_m * kMP;
+  const int n0 = tile / p.tiles_m * kCols, m0 = tile % p.tiles_m * kMP;
   const int KB = (p.K - 1) / kBK + 1;
   const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * KB / cl);
   const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * KB / cl);
 
   // Finishing threads: t owns columns lc .. lc + 3 of the tile (wq divides the
   // thread count, so they stay the same from row to row).
-  const int W = kSplitN / cl, wq = W / 4;
+  const int W = kCols / cl, wq = W / 4;
   const int t = static_cast<int>(threadIdx.x) - 64;
   const int lc = rank * W + (t & (wq - 1)) * 4, col = n0 + lc;
   SplitCols cols;
   SplitRow first;
+  GatedCols gated_cols;
+  GatedRow gated_first;
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const uint32_t bytes = Cf::kBBytes + static_cast<uint32_t>(p.mp) * kRowBytes;
@@ -247,7 +341,12 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
         const uint32_t bar = smem_u32(&sm.full[stage]);
         mbar_arrive_expect_tx(bar, bytes);
         const int k0 = kb * kBK;
-        if (kE4m3 || p.b_t) {
+        if constexpr (kPair) {
+          const bool kmajor = kE4m3 || p.b_t;
+          const int c0 = kmajor ? k0 : n0, c1 = kmajor ? n0 : k0;
+          tma_load_3d(smem_u32(sm.b[stage]), &tmB, bar, c0, c1, 0);
+          tma_load_3d(smem_u32(sm.b[stage]) + kRowBytes * 64, &tmS, bar, c0, c1, 0);
+        } else if (kE4m3 || p.b_t) {
           tma_load_3d(smem_u32(sm.b[stage]), &tmB, bar, k0, n0, 0);
         } else {
           tma_load_3d(smem_u32(sm.b[stage]), &tmB, bar, n0, k0, 0);
@@ -320,8 +419,17 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     // ------------------------------------------- accumulator -> partial sums
     const int quarter = warp & 3;
     grid_dependency_wait();
-    split_load_cols<kGrad>(p, col, cols);
-    split_load_row<kGrad>(p, m0 + t / wq, col, first);
+    if constexpr (kGated) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        gated_cols.bias[0][e] = !kGrad && p.c.bias && col + e < p.N ? p.c.bias[col + e] : 0;
+        gated_cols.bias[1][e] = !kGrad && p.c.bias2 && col + e < p.N ? p.c.bias2[col + e] : 0;
+      }
+      gated_load_row<kGrad>(p, m0 + t / wq, col, gated_first);
+    } else {
+      split_load_cols<kGrad>(p, col, cols);
+      split_load_row<kGrad>(p, m0 + t / wq, col, first);
+    }
     int got = 0;
     if (lane == 0)
       got = mbar_wait_bounded(smem_u32(&sm.done), 0, abort, p.err_word, kWaitTmemFull);
@@ -360,15 +468,22 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     __syncthreads();
   }
 
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  float sum[kGated ? 2 : 1][4] = {};
   if (warp >= 2) {
     const uint32_t red = smem_u32(sm.b[0]);
     with_act(p.c.act, [&](auto a) {
       constexpr int kAct = decltype(a)::value;
-      if (p.c.bf16) {
-        split_finish<kGrad, true, kAct>(p, red, t, lc, m0, col, cols, first, sum);
+      if constexpr (kGated) {
+        if (p.c.bf16) {
+          gated_finish<kGrad, true, kAct>(p, red, t, wq, lc, m0, col, gated_cols, gated_first, sum);
+        } else {
+          gated_finish<kGrad, false, kAct>(p, red, t, wq, lc, m0, col, gated_cols, gated_first,
+                                           sum);
+        }
+      } else if (p.c.bf16) {
+        split_finish<kGrad, true, kAct>(p, red, t, lc, m0, col, cols, first, sum[0]);
       } else {
-        split_finish<kGrad, false, kAct>(p, red, t, lc, m0, col, cols, first, sum);
+        split_finish<kGrad, false, kAct>(p, red, t, lc, m0, col, cols, first, sum[0]);
       }
     });
   }
@@ -388,25 +503,35 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   }
 
   if constexpr (kGrad) {
-    if (p.c.dbias != nullptr) {
+    if (p.c.dbias != nullptr || (kGated && p.c.dbias2 != nullptr)) {
       // Column sums of this CTA's columns: the threads of a column in row order, in a
       // part of the stages that holds no partial sums (other CTAs read those).
       constexpr uint32_t kSums = kMP * kSplitN * 4, kB = Cf::kStages * Cf::kBBytes;
       constexpr uint32_t kSlots = kSums > kB ? kSums - kB : 0;  // offset into the stages of A
-      static_assert(kSlots + kSplitFinish * 16 <= Cf::kStages * Cf::kABytes, "room for the sums");
+      constexpr int kSets = kGated ? 2 : 1;
+      static_assert(kSlots + kSets * kSplitFinish * 16 <= Cf::kStages * Cf::kABytes,
+                    "room for the sums");
       float4 *slots = reinterpret_cast<float4 *>(&sm.a[0][0] + kSlots);
-      if (warp >= 2) slots[t] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+      if (warp >= 2) {
+#pragma unroll
+        for (int w = 0; w < kSets; ++w)
+          slots[w * kSplitFinish + t] = make_float4(sum[w][0], sum[w][1], sum[w][2], sum[w][3]);
+      }
       __syncthreads();
       const int at = n0 + rank * W + t;
       if (warp >= 2 && t < W && at < p.N) {
-        float s = 0.f;
-        for (int i = t / 4; i < kSplitFinish; i += wq)
-          s += reinterpret_cast<const float *>(slots + i)[t & 3];
-        // All rows in one token tile: the sum is complete.
-        if (p.part != nullptr) {
-          p.part[static_cast<int64_t>(tile % p.tiles_m) * p.N + at] = s;
-        } else {
-          p.c.dbias[at] = p.c.bf16 ? to16<true>(s) : to16<false>(s);
+#pragma unroll
+        for (int w = 0; w < kSets; ++w) {
+          uint16_t *dbias = w ? p.c.dbias2 : p.c.dbias;
+          float s = 0.f;
+          for (int i = t / 4; i < kSplitFinish; i += wq)
+            s += reinterpret_cast<const float *>(slots + w * kSplitFinish + i)[t & 3];
+          // All rows in one token tile: the sum is complete.
+          if (p.part != nullptr) {
+            p.part[static_cast<int64_t>(w * p.tiles_m + tile % p.tiles_m) * p.N + at] = s;
+          } else if (!kGated || dbias != nullptr) {
+            dbias[at] = p.c.bf16 ? to16<true>(s) : to16<false>(s);
+          }
         }
       }
     }
@@ -443,7 +568,7 @@ inline bool split_clusters_fit(const DeviceInfo &dev, const void *kern, size_t s
   return n > 0;
 }
 
-template <bool kE4m3, int kMP, bool kGrad>
+template <bool kE4m3, int kMP, bool kGrad, bool kGated>
 cudaError_t launch_split_form(const DeviceInfo &dev, bool b_t, int M, int N, int K, const void *A,
                               int64_t lda, const void *B, int64_t ldb, const EpiCall &epi,
                               float *part, cudaStream_t stream) {
@@ -455,7 +580,8 @@ cudaError_t launch_split_form(const DeviceInfo &dev, bool b_t, int M, int N, int
                     Cf::kStages * (Cf::kBBytes + Cf::kABytes) >= kMP * kSplitN * 4,
                 "partial sums fit in the stages");
   const size_t smem = sizeof(SplitSmem<kMP>) + 1024;
-  auto kern = gemm_epi_split_kernel<kE4m3, kMP, kGrad>;
+  constexpr bool kPair = kGated && !kGrad;
+  auto kern = gemm_epi_split_kernel<kE4m3, kMP, kGrad, kGated>;
   const void *kp = reinterpret_cast<const void *>(kern);
   cudaError_t e = set_max_dynamic_smem(kp, static_cast<int>(smem), dev.device);
   if (e != cudaSuccess) return e;
@@ -469,6 +595,8 @@ cudaError_t launch_split_form(const DeviceInfo &dev, bool b_t, int M, int N, int
     return reinterpret_cast<uintptr_t>(q) % 8 == 0 && ld % 4 == 0;
   };
   p.r_vec = vec(epi.R, epi.ldr), p.d_vec = vec(epi.D, epi.ldd), p.z_vec = vec(epi.Z, epi.ldz);
+  p.r2_vec = vec(epi.R2, epi.ldr2), p.d2_vec = vec(epi.D2, epi.ldd2);
+  p.z2_vec = vec(epi.Z2, epi.ldz2);
   p.idesc = idesc_mma(kE4m3 || !epi.bf16 ? 0u : kFmtBF16, !b_t, false, kSplitN, p.mp);
   p.err_word = dev.err_word;
   p.part = part;
@@ -478,10 +606,18 @@ cudaError_t launch_split_form(const DeviceInfo &dev, bool b_t, int M, int N, int
                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap tmA, tmB;
   if (!make_tmap(&tmA, dt, kEs, A, M, K, lda, 1, 0, static_cast<uint32_t>(p.mp), kBK) ||
-      !(b_t ? make_tmap(&tmB, dt, kEs, B, N, K, ldb, 1, 0, kSplitN, kBK)
+      !(b_t ? make_tmap(&tmB, dt, kEs, B, N, K, ldb, 1, 0, kPair ? 64 : kSplitN, kBK)
             : make_tmap(&tmB, dt, kEs, B, K, N, ldb, 1, 0, 64, 64)))
     return cudaErrorInvalidValue;
-  const int64_t tiles = static_cast<int64_t>((N - 1) / kSplitN + 1) * p.tiles_m;
+  SplitMap<kPair> tmS;
+  std::memset(&tmS, 0, sizeof tmS);
+  if constexpr (kPair) {
+    if (!(b_t ? make_tmap(&tmS, dt, kEs, epi.B2, N, K, epi.ldb2, 1, 0, 64, kBK)
+              : make_tmap(&tmS, dt, kEs, epi.B2, K, N, epi.ldb2, 1, 0, 64, 64)))
+      return cudaErrorInvalidValue;
+  }
+  const int64_t tiles =
+      static_cast<int64_t>((N - 1) / (kPair ? kSplitN / 2 : kSplitN) + 1) * p.tiles_m;
   if (tiles > 0x7fffffffLL / kSplitMaxCl) return cudaErrorInvalidValue;
   const int KB = (K - 1) / kBK + 1;
   // As many parts of k as fill the SMs twice, at least one k-block each.
@@ -505,19 +641,19 @@ cudaError_t launch_split_form(const DeviceInfo &dev, bool b_t, int M, int N, int
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cl > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, p);
+  e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmS, p);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <bool kE4m3, bool kGrad>
+template <bool kE4m3, bool kGrad, bool kGated = false>
 cudaError_t launch_split(const DeviceInfo &dev, int mp, bool b_t, int M, int N, int K,
                          const void *A, int64_t lda, const void *B, int64_t ldb,
                          const EpiCall &epi, float *part, cudaStream_t stream) {
   switch (mp) {
-    case 16: return launch_split_form<kE4m3, 16, kGrad>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
-    case 32: return launch_split_form<kE4m3, 32, kGrad>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
-    case 64: return launch_split_form<kE4m3, 64, kGrad>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
-    default: return launch_split_form<kE4m3, 128, kGrad>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
+    case 16: return launch_split_form<kE4m3, 16, kGrad, kGated>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
+    case 32: return launch_split_form<kE4m3, 32, kGrad, kGated>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
+    case 64: return launch_split_form<kE4m3, 64, kGrad, kGated>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
+    default: return launch_split_form<kE4m3, 128, kGrad, kGated>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
   }
 }
 

@@ -3,6 +3,8 @@
 //
 //   forward   Z = alpha op(A) op(B) scale_a_i scale_b_j + bias_j,  D = act(Z) + R
 //   gradient  D = alpha op(A) op(B) act'(Zin), column sums of D
+//   gated     D = act(G) U, where G and U are Z for two matrices B
+//   its gradient  d = alpha op(A) op(B), dG = d U act'(G), dU = d act(G), column sums
 //
 // 16-bit operands (kind::f16) or e4m3 (kind::f8f6f4: twice the k per MMA, the
 // same bytes per stage), fp32 accumulation in tensor memory, 16-bit results.
@@ -34,7 +36,15 @@
 // exchanges (16 + 8 + 4 + 2 + 1 shuffles) leave the sum over the warp's 32 rows
 // of column l in lane l, which goes to partial row (row / 32); col_sums adds the
 // partial rows. No atomics: the same bits on every call.
+//
+// The gated forms. Forward, a tile is 256 rows x 128 columns of D: CTA 0 of the pair
+// stages 128 columns of the first B and CTA 1 of the second, so the pair's MMA of 256
+// columns leaves G's in the accumulator's first 128 and U's in the others, and both
+// loops are those of the plain product. Gradient: G and U come into two buffers per
+// warp, where dG and dU take their places, for one ring stage less.
 #pragma once
+
+#include <type_traits>
 
 #include "epi.cuh"
 #include "gemm_tc_kernel.cuh"
@@ -52,26 +62,29 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
-template <int kN>
+// kBufs: staging buffers of 4 KiB per epilogue warp.
+template <int kN, int kBufs = 1>
 struct EpiCfg {
   static constexpr int kTileM = 256;
-  static constexpr int kBNLoad = kN / 2;             // B columns staged per CTA
-  static constexpr int kStages = kN == 256 ? 6 : 8;  // 192 KiB
+  static constexpr int kBNLoad = kN / 2;  // B columns staged per CTA
+  // 192 KiB, or with two buffers 160 and 144.
+  static constexpr int kStages = kBufs == 1 ? (kN == 256 ? 6 : 8) : (kN == 256 ? 5 : 6);
   static constexpr uint32_t kABytes = kBM * kRowBytes;
   static constexpr uint32_t kBBytes = kBNLoad * kRowBytes;
   static constexpr uint32_t kTxBytes = 2 * (kABytes + kBBytes);  // both CTAs, one phase
   static constexpr uint32_t kTmem = 2 * kN;                      // two accumulators
 };
 
-template <int kN>
+template <int kN, int kBufs = 1>
 struct __align__(1024) EpiSmem {
-  uint8_t a[EpiCfg<kN>::kStages][EpiCfg<kN>::kABytes];
-  uint8_t b[EpiCfg<kN>::kStages][EpiCfg<kN>::kBBytes];
-  uint8_t stage[kEpiWarps][kStageCBytes];
+  using Cf = EpiCfg<kN, kBufs>;
+  uint8_t a[Cf::kStages][Cf::kABytes];
+  uint8_t b[Cf::kStages][Cf::kBBytes];
+  uint8_t stage[kEpiWarps * kBufs][kStageCBytes];
   uint16_t bias[kN];  // the tile's bias (as stored) and column scales
   float scale[kN];
-  uint64_t full[EpiCfg<kN>::kStages];
-  uint64_t empty[EpiCfg<kN>::kStages];
+  uint64_t full[Cf::kStages];
+  uint64_t empty[Cf::kStages];
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint64_t arrived[kEpiWarps];  // R is in a warp's buffer
@@ -86,9 +99,13 @@ struct EpiArgs {
   bool a_t, b_t;
   bool d_tma, z_tma;  // D / Z written through their tensor maps
   bool r_tma;         // R (Zin) read through its tensor map
+  // Gated: D / Z as above (gradient: dG / dU), r_tma for U (written, or gradient: G
+  // read), s_tma for U read.
+  bool s_tma;
   uint32_t idesc;
   uint32_t *err_word;
   float *part;        // gradient: partial column sums [ceil(M / 32)][N], or null
+  int64_t part_apart;  // gated: dU's are this far behind dG's
   EpiCall c;
 };
 
@@ -230,11 +247,12 @@ __device__ __forceinline__ void epi_preact(const uint16_t *bias, const float *sc
 constexpr int kEpiGroupM = 16;
 
 // The producer's loop for one operand form.
-template <bool kE4m3, int kN, bool kAT, bool kBT>
+// kPair: both CTAs stage the same columns, of a B of their own.
+template <bool kE4m3, int kN, bool kAT, bool kBT, int kBufs, bool kPair>
 __device__ __forceinline__ void epi_produce(const CUtensorMap &tmA, const CUtensorMap &tmB,
-                                            const EpiArgs &p, EpiSmem<kN> &sm, uint32_t rank,
-                                            int unit, int units) {
-  using Cf = EpiCfg<kN>;
+                                            const EpiArgs &p, EpiSmem<kN, kBufs> &sm,
+                                            uint32_t rank, int unit, int units) {
+  using Cf = EpiCfg<kN, kBufs>;
   constexpr int kBK = kE4m3 ? 128 : 64;
   constexpr uint32_t kMNBoxBytes = kRowBytes * 64;  // 64 rows of k x 64 16-bit values
   volatile int *abort = &sm.abort;
@@ -246,7 +264,7 @@ __device__ __forceinline__ void epi_produce(const CUtensorMap &tmA, const CUtens
     int tm, tn;
     tile_coords<kEpiGroupM>(t, p.tiles_m, p.tiles_n, tm, tn);
     const int m0 = tm * Cf::kTileM + static_cast<int>(rank) * kBM;
-    const int n0 = tn * kN + static_cast<int>(rank) * Cf::kBNLoad;
+    const int n0 = kPair ? tn * Cf::kBNLoad : tn * kN + static_cast<int>(rank) * Cf::kBNLoad;
     for (int kb = 0; kb < KB; ++kb) {
       if (!mbar_wait_lazy(smem_u32(&sm.empty[stage]), phase ^ 1u, abort, p.err_word,
                           kWaitEmpty)) {
@@ -294,10 +312,10 @@ __device__ __forceinline__ void epi_produce(const CUtensorMap &tmA, const CUtens
 }
 
 // The leader's MMA loop for one operand form.
-template <bool kE4m3, int kN, bool kAT, bool kBT>
-__device__ __forceinline__ void epi_multiply(const EpiArgs &p, EpiSmem<kN> &sm,
+template <bool kE4m3, int kN, bool kAT, bool kBT, int kBufs>
+__device__ __forceinline__ void epi_multiply(const EpiArgs &p, EpiSmem<kN, kBufs> &sm,
                                              uint32_t tmem_base, int unit, int units) {
-  using Cf = EpiCfg<kN>;
+  using Cf = EpiCfg<kN, kBufs>;
   constexpr int kBK = kE4m3 ? 128 : 64;
   constexpr uint32_t kMNBoxBytes = kRowBytes * 64;
   constexpr uint32_t kMNStep = kRowBytes * 16;  // 16 rows of k
@@ -498,18 +516,215 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
   }
 }
 
-template <bool kE4m3, int kN, bool kGrad>
+// One tile's epilogue of the gated layer by one warp: 32 rows x 64 columns of D. The
+// projections are read from the accumulator again for each matrix that is written.
+template <bool kBf16, int kN>
+__device__ __forceinline__ void epi_tile_gated(const CUtensorMap &tmD, const CUtensorMap &tmG,
+                                               const CUtensorMap &tmU, const EpiArgs &p,
+                                               EpiSmem<kN> &sm, uint32_t tmem_base, uint32_t n,
+                                               int tm, int tn, uint32_t rank, int warp, int lane,
+                                               bool &ok) {
+  static_assert(kN == 256, "a warp has one block of 64 columns");
+  constexpr int kCols = kN / 2;  // of D in a tile, and of each projection
+  const int e = warp - 2, quarter = warp & 3, half = e >> 2;
+  const uint32_t stage = smem_u32(sm.stage[e]);
+  const uint32_t buf = n & 1u, use = (n >> 1) & 1u;
+  const int row0 = tm * EpiCfg<kN>::kTileM + static_cast<int>(rank) * kBM + quarter * 32;
+  const int local0 = half * 64, col = tn * kCols + local0;
+  epilogue_sync();  // every warp has read the previous tile's
+  for (int i = threadIdx.x - 64; i < kN; i += 32 * kEpiWarps) {
+    const uint16_t *bias = i < kCols ? p.c.bias : p.c.bias2;
+    const int j = tn * kCols + (i & (kCols - 1));
+    sm.bias[i] = bias && j < p.N ? bias[j] : 0;
+  }
+  epilogue_sync();
+  if (!mbar_wait_lazy(smem_u32(&sm.tmem_full[buf]), use, &sm.abort, p.err_word, kWaitTmemFull)) {
+    ok = false;
+    return;
+  }
+  tc_fence_after_sync();
+  const uint32_t taddr =
+      tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kN + local0;
+  // 32 columns of a projection (0: G, 1: U).
+  auto project = [&](int which, int h, F2 (&v)[16]) {
+    uint32_t acc[32];
+    tmem_ld_32x32b_x32(taddr + which * kCols + 32 * h, acc);
+    tmem_ld_wait();
+    epi_preact<false, kBf16>(&sm.bias[which * kCols + local0 + 32 * h], nullptr, p.c.alpha, acc,
+                             v);
+  };
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    uint16_t *out = which ? p.c.Z2 : p.c.Z;
+    if (out == nullptr) continue;
+    stage_free(lane);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[16];
+      F2 v[16];
+      project(which, h, v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) w[j] = pack2<kBf16>(v[j]);
+      stage_half(stage, lane, h, w);
+    }
+    store_block(which ? &tmU : &tmG, which ? p.r_tma : p.z_tma, out, which ? p.c.ldz2 : p.c.ldz,
+                row0, col, p.M, p.N, stage, lane);
+  }
+  stage_free(lane);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[16];
+    F2 g[16], u[16];
+    project(0, h, g);
+    project(1, h, u);
+    if (h == 1) {  // all in registers: the next tile may have it
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.tmem_empty[buf]), 0));
+    }
+    with_act(p.c.act, [&](auto a) { act_values<decltype(a)::value>(g); });
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack2<kBf16>(mul2(g[j], u[j]));
+    stage_half(stage, lane, h, w);
+  }
+  store_block(&tmD, p.d_tma, p.c.D, p.c.ldd, row0, col, p.M, p.N, stage, lane);
+}
+
+// One tile's epilogue of its gradient by one warp: 32 rows x kN / 2 columns. A lane
+// reads its row of G and U from the warp's two buffers and puts dG and dU in their
+// places.
+template <bool kBf16, int kN>
+__device__ __forceinline__ void epi_tile_gated_grad(
+    const CUtensorMap &tmDG, const CUtensorMap &tmDU, const CUtensorMap &tmG,
+    const CUtensorMap &tmU, const EpiArgs &p, EpiSmem<kN, 2> &sm, uint32_t tmem_base, uint32_t n,
+    int tm, int tn, uint32_t rank, int warp, int lane, uint32_t &rphase, bool &ok) {
+  const int e = warp - 2, quarter = warp & 3, half = e >> 2;
+  const uint32_t stage[2] = {smem_u32(sm.stage[2 * e]), smem_u32(sm.stage[2 * e + 1])};
+  const uint32_t buf = n & 1u, use = (n >> 1) & 1u;
+  const int row0 = tm * EpiCfg<kN>::kTileM + static_cast<int>(rank) * kBM + quarter * 32;
+  const int row = row0 + lane;
+  const int local0 = half * (kN / 2), col0 = tn * kN + local0;
+  const uint32_t bar = smem_u32(&sm.arrived[e]);
+  const uint32_t bytes = (p.r_tma ? kStageCBytes : 0) + (p.s_tma ? kStageCBytes : 0);
+  auto request = [&](int col) {
+    stage_free(lane);
+    if (bytes != 0) {
+      // The buffers' last accesses were ordinary ones where no TMA store followed them.
+      if (!p.d_tma || !p.z_tma) {
+        fence_proxy_async_shared();
+        __syncwarp();
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, bytes);
+        if (p.r_tma) tma_load_3d(stage[0], &tmG, bar, col, row0, 0);
+        if (p.s_tma) tma_load_3d(stage[1], &tmU, bar, col, row0, 0);
+      }
+    }
+    if (!p.r_tma) stage_block(p.c.R, p.c.ldr, row0, col, p.M, p.N, stage[0], lane);
+    if (!p.s_tma) stage_block(p.c.R2, p.c.ldr2, row0, col, p.M, p.N, stage[1], lane);
+  };
+  auto arrive = [&] {
+    if (bytes != 0) {
+      wait_copy(bar, rphase, p.err_word);
+      rphase ^= 1u;
+    }
+  };
+  request(col0);
+  const bool got = mbar_wait_lazy(smem_u32(&sm.tmem_full[buf]), use, &sm.abort, p.err_word,
+                                  kWaitTmemFull);
+  arrive();
+  if (!got) {
+    ok = false;
+    return;
+  }
+  tc_fence_after_sync();
+  const uint32_t taddr =
+      tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kN + local0;
+#pragma unroll 1
+  for (int c = 0; c < kN / 2; c += 64) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t acc[32], g[16], u[16];
+      F2 dg[16], du[16];
+      tmem_ld_32x32b_x32(taddr + c + 32 * h, acc);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ld_shared_v4(stage_unit(stage[0], lane, 4 * h + j), g[4 * j], g[4 * j + 1], g[4 * j + 2],
+                     g[4 * j + 3]);
+        ld_shared_v4(stage_unit(stage[1], lane, 4 * h + j), u[4 * j], u[4 * j + 1], u[4 * j + 2],
+                     u[4 * j + 3]);
+      }
+      tmem_ld_wait();
+      if (c + 32 * h + 32 == kN / 2) {  // all in registers: the next tile may have it
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.tmem_empty[buf]), 0));
+      }
+      with_act(p.c.act, [&](auto a) {
+        constexpr int kAct = decltype(a)::value;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float lo, hi;
+          unpack16<kBf16>(g[j], lo, hi);
+          const F2 d = mul2(f2(__uint_as_float(acc[2 * j]), __uint_as_float(acc[2 * j + 1])),
+                            f2(p.c.alpha));
+          dg[j] = mul2(mul2(d, unpack2<kBf16>(u[j])), act_slope2<kAct>(lo, hi));
+          du[j] = mul2(d, act_value2<kAct>(f2(lo, hi)));
+        }
+      });
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) w[j] = pack2<kBf16>(dg[j]);
+      stage_half(stage[0], lane, h, w);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) w[j] = pack2<kBf16>(du[j]);
+      stage_half(stage[1], lane, h, w);
+      if (p.part != nullptr && row0 < p.M) {
+        float *part = p.part + static_cast<int64_t>(row0 / 32) * p.N;
+        const int col = col0 + c + 32 * h + lane;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) split(which ? du[j] : dg[j], v[2 * j], v[2 * j + 1]);
+          // Rows beyond M are left out: they hold 0 * B, NaN where B is not finite.
+          if (row >= p.M) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          }
+          const float s = warp_column_sums(v, lane);
+          if (col < p.N) part[which * p.part_apart + col] = s;
+        }
+      }
+    }
+    store_block(&tmDG, p.d_tma, p.c.D, p.c.ldd, row0, col0 + c, p.M, p.N, stage[0], lane);
+    store_block(&tmDU, p.z_tma, p.c.D2, p.c.ldd2, row0, col0 + c, p.M, p.N, stage[1], lane);
+    if (c + 64 < kN / 2) {
+      request(col0 + c + 64);
+      arrive();
+    }
+  }
+}
+
+struct NoMap {};
+
+// Maps: tmZ, tmR and tmS stand for Z, R and nothing; gated: G and U (written) and the
+// second B; its gradient: dU, G and U.
+template <bool kE4m3, int kN, bool kGrad, bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_epi_tile_kernel(const __grid_constant__ CUtensorMap tmA,
                          const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmD,
                          const __grid_constant__ CUtensorMap tmZ,
                          const __grid_constant__ CUtensorMap tmR,
+                         const __grid_constant__ std::conditional_t<kGated, CUtensorMap, NoMap> tmS,
                          const __grid_constant__ EpiArgs p) {
-  using Cf = EpiCfg<kN>;
+  constexpr int kBufs = kGated && kGrad ? 2 : 1;
+  constexpr bool kPair = kGated && !kGrad;
+  using Cf = EpiCfg<kN, kBufs>;
   extern __shared__ uint8_t smem_raw[];
   // Same offset in both CTAs of the pair, as the pair MMA needs.
-  EpiSmem<kN> &sm = *reinterpret_cast<EpiSmem<kN> *>(
+  EpiSmem<kN, kBufs> &sm = *reinterpret_cast<EpiSmem<kN, kBufs> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -532,6 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmB);
     if (p.d_tma) prefetch_tmap(&tmD);
     if (p.r_tma) prefetch_tmap(&tmR);
+    if constexpr (kGated)
+      if (kPair || p.s_tma) prefetch_tmap(&tmS);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(&sm.tmem_base), Cf::kTmem);
@@ -547,34 +764,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_launch_dependents();
 
   if (warp == 0) {
+    const CUtensorMap *b = &tmB;
+    if constexpr (kPair) b = rank == 0 ? &tmB : &tmS;
     if constexpr (kE4m3) {
-      epi_produce<true, kN, false, true>(tmA, tmB, p, sm, rank, unit, units);
+      epi_produce<true, kN, false, true, kBufs, kPair>(tmA, *b, p, sm, rank, unit, units);
     } else if (p.a_t) {
       if (p.b_t) {
-        epi_produce<false, kN, true, true>(tmA, tmB, p, sm, rank, unit, units);
+        epi_produce<false, kN, true, true, kBufs, kPair>(tmA, *b, p, sm, rank, unit, units);
       } else {
-        epi_produce<false, kN, true, false>(tmA, tmB, p, sm, rank, unit, units);
+        epi_produce<false, kN, true, false, kBufs, kPair>(tmA, *b, p, sm, rank, unit, units);
       }
     } else if (p.b_t) {
-      epi_produce<false, kN, false, true>(tmA, tmB, p, sm, rank, unit, units);
+      epi_produce<false, kN, false, true, kBufs, kPair>(tmA, *b, p, sm, rank, unit, units);
     } else {
-      epi_produce<false, kN, false, false>(tmA, tmB, p, sm, rank, unit, units);
+      epi_produce<false, kN, false, false, kBufs, kPair>(tmA, *b, p, sm, rank, unit, units);
     }
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
       if constexpr (kE4m3) {
-        epi_multiply<true, kN, false, true>(p, sm, tmem_base, unit, units);
+        epi_multiply<true, kN, false, true, kBufs>(p, sm, tmem_base, unit, units);
       } else if (p.a_t) {
         if (p.b_t) {
-          epi_multiply<false, kN, true, true>(p, sm, tmem_base, unit, units);
+          epi_multiply<false, kN, true, true, kBufs>(p, sm, tmem_base, unit, units);
         } else {
-          epi_multiply<false, kN, true, false>(p, sm, tmem_base, unit, units);
+          epi_multiply<false, kN, true, false, kBufs>(p, sm, tmem_base, unit, units);
         }
       } else if (p.b_t) {
-        epi_multiply<false, kN, false, true>(p, sm, tmem_base, unit, units);
+        epi_multiply<false, kN, false, true, kBufs>(p, sm, tmem_base, unit, units);
       } else {
-        epi_multiply<false, kN, false, false>(p, sm, tmem_base, unit, units);
+        epi_multiply<false, kN, false, false, kBufs>(p, sm, tmem_base, unit, units);
       }
     }
     __syncwarp();
@@ -596,7 +815,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      if (p.c.bf16) {
+      if constexpr (kGated && kGrad) {
+        if (p.c.bf16) {
+          epi_tile_gated_grad<true, kN>(tmD, tmZ, tmR, tmS, p, sm, tmem_base, n, tm, tn, rank,
+                                        warp, lane, rphase, ok);
+        } else {
+          epi_tile_gated_grad<false, kN>(tmD, tmZ, tmR, tmS, p, sm, tmem_base, n, tm, tn, rank,
+                                         warp, lane, rphase, ok);
+        }
+      } else if constexpr (kGated) {
+        if (p.c.bf16) {
+          epi_tile_gated<true, kN>(tmD, tmZ, tmR, p, sm, tmem_base, n, tm, tn, rank, warp, lane,
+                                   ok);
+        } else {
+          epi_tile_gated<false, kN>(tmD, tmZ, tmR, p, sm, tmem_base, n, tm, tn, rank, warp, lane,
+                                    ok);
+        }
+      } else if (p.c.bf16) {
         epi_tile<kE4m3, kGrad, true, kN>(tmD, tmZ, tmR, p, sm, tmem_base, n, tm, tn, rank, warp,
                                           lane, rphase, ok);
       } else {
@@ -630,15 +865,17 @@ inline bool out_tmap(CUtensorMap *tm, bool bf16, const uint16_t *p, int64_t ld, 
   return N % 8 == 0 && block_tmap(tm, bf16, p, ld, M, N);
 }
 
-template <bool kE4m3, int kN, bool kGrad>
+template <bool kE4m3, int kN, bool kGrad, bool kGated = false>
 cudaError_t launch_epi_tile(const DeviceInfo &dev, bool a_t, bool b_t, int M, int N, int K,
                             const void *A, int64_t lda, const void *B, int64_t ldb,
                             const EpiCall &epi, float *part, cudaStream_t stream) {
-  using Cf = EpiCfg<kN>;
+  constexpr int kBufs = kGated && kGrad ? 2 : 1;
+  constexpr bool kPair = kGated && !kGrad;
+  using Cf = EpiCfg<kN, kBufs>;
   constexpr int kEs = kE4m3 ? 1 : 2, kBK = kE4m3 ? 128 : 64;
-  static_assert(sizeof(EpiSmem<kN>) + 1024 <= 232448, "shared memory");
-  const size_t smem = sizeof(EpiSmem<kN>) + 1024;
-  auto kern = gemm_epi_tile_kernel<kE4m3, kN, kGrad>;
+  static_assert(sizeof(EpiSmem<kN, kBufs>) + 1024 <= 232448, "shared memory");
+  const size_t smem = sizeof(EpiSmem<kN, kBufs>) + 1024;
+  auto kern = gemm_epi_tile_kernel<kE4m3, kN, kGrad, kGated>;
   const int pairs = pair_capacity(dev, reinterpret_cast<const void *>(kern), smem);
   if (pairs < 1) return cudaErrorInvalidConfiguration;
 
@@ -654,17 +891,34 @@ cudaError_t launch_epi_tile(const DeviceInfo &dev, bool a_t, bool b_t, int M, in
       !(b_t ? make_tmap(&tmB, dt, kEs, B, N, K, ldb, 1, 0, Cf::kBNLoad, kBK)
             : make_tmap(&tmB, dt, kEs, B, K, N, ldb, 1, 0, 64, 64)))
     return cudaErrorInvalidValue;
+  std::conditional_t<kGated, CUtensorMap, NoMap> tmS;
+  std::memset(&tmS, 0, sizeof tmS);
   EpiArgs p;
   p.M = M, p.N = N, p.K = K;
   p.tiles_m = (M - 1) / Cf::kTileM + 1;  // sizes up to 2^31 - 1
-  p.tiles_n = (N - 1) / kN + 1;
+  p.tiles_n = (N - 1) / (kPair ? kN / 2 : kN) + 1;
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x7fffffffLL - pairs) return cudaErrorInvalidValue;
   p.tiles = static_cast<int>(tiles);
   p.a_t = a_t, p.b_t = b_t;
   p.d_tma = out_tmap(&tmD, epi.bf16, epi.D, epi.ldd, M, N);
-  p.z_tma = out_tmap(&tmZ, epi.bf16, epi.Z, epi.ldz, M, N);
-  p.r_tma = block_tmap(&tmR, epi.bf16, epi.R, epi.ldr, M, N);
+  p.s_tma = false;
+  p.part_apart = static_cast<int64_t>((M - 1) / 32 + 1) * N;
+  if constexpr (kPair) {
+    if (!(b_t ? make_tmap(&tmS, dt, kEs, epi.B2, N, K, epi.ldb2, 1, 0, Cf::kBNLoad, kBK)
+              : make_tmap(&tmS, dt, kEs, epi.B2, K, N, epi.ldb2, 1, 0, 64, 64)))
+      return cudaErrorInvalidValue;
+    p.z_tma = out_tmap(&tmZ, epi.bf16, epi.Z, epi.ldz, M, N);
+    p.r_tma = out_tmap(&tmR, epi.bf16, epi.Z2, epi.ldz2, M, N);
+  } else {
+    p.r_tma = block_tmap(&tmR, epi.bf16, epi.R, epi.ldr, M, N);
+    if constexpr (kGated) {
+      p.z_tma = out_tmap(&tmZ, epi.bf16, epi.D2, epi.ldd2, M, N);
+      p.s_tma = block_tmap(&tmS, epi.bf16, epi.R2, epi.ldr2, M, N);
+    } else {
+      p.z_tma = out_tmap(&tmZ, epi.bf16, epi.Z, epi.ldz, M, N);
+    }
+  }
   p.idesc = idesc_mma(kE4m3 || !epi.bf16 ? 0u : kFmtBF16, a_t, !b_t, Cf::kTileM, kN);
   p.err_word = dev.err_word;
   p.part = part;
@@ -684,7 +938,7 @@ cudaError_t launch_epi_tile(const DeviceInfo &dev, bool a_t, bool b_t, int M, in
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, tmZ, tmR, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, tmZ, tmR, tmS, p);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

@@ -213,6 +213,20 @@ struct EpiCall {
   uint16_t *D = nullptr;
   int64_t ldd = 0;
   uint16_t *dbias = nullptr;
+  // A gated layer: two projections of op(A) and their product, or its gradient.
+  //   forward   z2 = alpha sum_k op(A)_ik op(B2)_kj + bias2[j]; Z2 = z2; D = act(z) z2
+  //   gradient  d = alpha acc; D = d R2 act'(R); D2 = d act(R); their column sums
+  bool gated = false;
+  const void *B2 = nullptr;  // op as B
+  int64_t ldb2 = 0;
+  const uint16_t *bias2 = nullptr;
+  const uint16_t *R2 = nullptr;
+  int64_t ldr2 = 0;
+  uint16_t *Z2 = nullptr;
+  int64_t ldz2 = 0;
+  uint16_t *D2 = nullptr;
+  int64_t ldd2 = 0;
+  uint16_t *dbias2 = nullptr;
 };
 // The product with that epilogue. 16-bit A and B of the call's format, or, with
 // e4m3, 8-bit A (M x K) and B stored N x K. Layout already checked: A and B

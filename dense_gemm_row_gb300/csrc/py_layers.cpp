@@ -29,6 +29,8 @@ decltype(&gemm_rms_norm_bf16) g_norm[2];
 decltype(&gemm_rms_norm_bf16_e4m3) g_norm8[2];
 decltype(&gemm_rms_norm_grad_bf16) g_norm_grad[2];
 decltype(&gemm_layer_norm_bf16) g_layer_norm[2];
+decltype(&gemm_bf16_gated) g_gated[2];
+decltype(&gemm_bf16_gated_dact) g_gated_dact[2];
 decltype(&gemm_layer_norm_grad_bf16) g_layer_norm_grad[2];
 
 struct Refused {};  // a Python exception has been set
@@ -321,6 +323,55 @@ int rms_norm_grad(PyObject *const *v) {
   });
 }
 
+// (A, Bg, Bu, D, act, alpha, bias_gate, bias_up, gate, up, trans_a, trans_b, stream)
+int gated(PyObject *const *v) {
+  const at::Tensor &A = tensor(v[0], "A"), &Bg = tensor(v[1], "Bg"), &Bu = tensor(v[2], "Bu");
+  const at::Tensor &D = tensor(v[3], "D");
+  const int dev = device_of(A, "A");
+  const int f = format_of(A, "A");
+  const at::ScalarType type = A.scalar_type();
+  const Product p = product(A, Bg, v[10], v[11], dev, 8);
+  const Matrix b2 = matrix(Bu, "Bu", Bg.size(0), Bg.size(1), type, dev, 8);
+  const Matrix d = matrix(D, "D", p.m, p.n, type, dev);
+  const Matrix g = matrix_or_none(v[8], "gate", p.m, p.n, type, dev);
+  const Matrix u = matrix_or_none(v[9], "up", p.m, p.n, type, dev);
+  void *bias_g = vector_or_none(v[6], "bias_gate", p.n, type, dev);
+  void *bias_u = vector_or_none(v[7], "bias_up", p.n, type, dev);
+  const gemm_act_t act = act_of(v[4]);
+  const float alpha = number(v[5]);
+  const cudaStream_t s = stream_of(v[12], dev);
+  return unlocked([&] {
+    return g_gated[f](p.op_a, p.op_b, p.m, p.n, p.k, alpha, as<uint16_t>(p.a.p), p.a.ld,
+                      as<uint16_t>(p.b.p), p.b.ld, as<uint16_t>(b2.p), b2.ld, act,
+                      as<uint16_t>(bias_g), as<uint16_t>(bias_u), as<uint16_t>(g.p), g.ld,
+                      as<uint16_t>(u.p), u.ld, as<uint16_t>(d.p), d.ld, s);
+  });
+}
+
+// (A, B, G, U, dG, dU, act, alpha, dbias_gate, dbias_up, trans_a, trans_b, stream)
+int gated_dact(PyObject *const *v) {
+  const at::Tensor &A = tensor(v[0], "A"), &B = tensor(v[1], "B");
+  const int dev = device_of(A, "A");
+  const int f = format_of(A, "A");
+  const at::ScalarType type = A.scalar_type();
+  const Product p = product(A, B, v[10], v[11], dev, 8);
+  const Matrix g = matrix(tensor(v[2], "G"), "G", p.m, p.n, type, dev);
+  const Matrix u = matrix(tensor(v[3], "U"), "U", p.m, p.n, type, dev);
+  const Matrix dg = matrix(tensor(v[4], "dG"), "dG", p.m, p.n, type, dev);
+  const Matrix du = matrix(tensor(v[5], "dU"), "dU", p.m, p.n, type, dev);
+  void *dbg = vector_or_none(v[8], "dbias_gate", p.n, type, dev);
+  void *dbu = vector_or_none(v[9], "dbias_up", p.n, type, dev);
+  const gemm_act_t act = act_of(v[6]);
+  const float alpha = number(v[7]);
+  const cudaStream_t s = stream_of(v[12], dev);
+  return unlocked([&] {
+    return g_gated_dact[f](p.op_a, p.op_b, p.m, p.n, p.k, alpha, as<uint16_t>(p.a.p), p.a.ld,
+                           as<uint16_t>(p.b.p), p.b.ld, act, as<uint16_t>(g.p), g.ld,
+                           as<uint16_t>(u.p), u.ld, as<uint16_t>(dg.p), dg.ld,
+                           as<uint16_t>(du.p), du.ld, as<uint16_t>(dbg), as<uint16_t>(dbu), s);
+  });
+}
+
 // (X, Y, weight, bias, residual, h, mean, rstd, eps, stream)
 int layer_norm(PyObject *const *v) {
   const at::Tensor &X = tensor(v[0], "X"), &Y = tensor(v[1], "Y");
@@ -413,6 +464,10 @@ PyObject *bind(PyObject *, PyObject *args) {
       {"gemm_rms_norm_f16_e4m3", &g_norm8[1]},
       {"gemm_rms_norm_grad_bf16", &g_norm_grad[0]},
       {"gemm_rms_norm_grad_f16", &g_norm_grad[1]},
+      {"gemm_bf16_gated", &g_gated[0]},
+      {"gemm_f16_gated", &g_gated[1]},
+      {"gemm_bf16_gated_dact", &g_gated_dact[0]},
+      {"gemm_f16_gated_dact", &g_gated_dact[1]},
       {"gemm_layer_norm_bf16", &g_layer_norm[0]},
       {"gemm_layer_norm_f16", &g_layer_norm[1]},
       {"gemm_layer_norm_grad_bf16", &g_layer_norm_grad[0]},
@@ -441,6 +496,8 @@ PyMethodDef g_methods[] = {
     method<act_grad, 6>("act_grad"),
     method<rms_norm, 9>("rms_norm"),
     method<rms_norm_grad, 8>("rms_norm_grad"),
+    method<gated, 13>("gemm_gated"),
+    method<gated_dact, 13>("gemm_gated_dact"),
     method<layer_norm, 10>("layer_norm"),
     method<layer_norm_grad, 10>("layer_norm_grad"),
     {"bind", bind, METH_VARARGS, nullptr},

@@ -459,6 +459,68 @@ GEMM_API gemm_status_t gemm_rms_norm_grad_f16(int64_t rows, int64_t cols, const 
                                               int64_t lddx, gemm_f16_t *dW, cudaStream_t stream);
 
 /*
+ * gemm_bf16_gated, gemm_f16_gated -- the two projections of a gated layer and
+ * their product:
+ *
+ *     G = alpha * op(A) * op(Bg) + bias_g,   U = alpha * op(A) * op(Bu) + bias_u
+ *     D = act(G) .* U
+ *
+ * Bg and Bu have one operand form opB. bias_g, bias_u (N values each), G and U
+ * may be NULL (no such term; not written). act(G) and the product are taken of
+ * the fp32 values, not of the rounded ones. Layouts, K == 0 and the rest are
+ * those of gemm_bf16_epi, with ldbg and ldbu under ldb's rules; G, U and D are
+ * distinct.
+ */
+GEMM_API gemm_status_t gemm_bf16_gated(gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N,
+                                       int64_t K, float alpha, const gemm_bf16_t *A, int64_t lda,
+                                       const gemm_bf16_t *Bg, int64_t ldbg, const gemm_bf16_t *Bu,
+                                       int64_t ldbu, gemm_act_t act, const gemm_bf16_t *bias_g,
+                                       const gemm_bf16_t *bias_u, gemm_bf16_t *G, int64_t ldg,
+                                       gemm_bf16_t *U, int64_t ldu, gemm_bf16_t *D, int64_t ldd,
+                                       cudaStream_t stream);
+GEMM_API gemm_status_t gemm_f16_gated(gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N,
+                                      int64_t K, float alpha, const gemm_f16_t *A, int64_t lda,
+                                      const gemm_f16_t *Bg, int64_t ldbg, const gemm_f16_t *Bu,
+                                      int64_t ldbu, gemm_act_t act, const gemm_f16_t *bias_g,
+                                      const gemm_f16_t *bias_u, gemm_f16_t *G, int64_t ldg,
+                                      gemm_f16_t *U, int64_t ldu, gemm_f16_t *D, int64_t ldd,
+                                      cudaStream_t stream);
+
+/*
+ * gemm_bf16_gated_dact, gemm_f16_gated_dact -- the product that carries a
+ * gradient back to the two projections of a gated layer:
+ *
+ *     dD = alpha * op(A) * op(B)
+ *     dG = dD .* U .* act'(G),   dU = dD .* act(G)
+ *     dbias_g, dbias_u = the column sums of dG and dU
+ *
+ * (A the next layer's output gradient, B its weights; dD stays in fp32 and is
+ * not written.) G and U are what the forward call stored. dbias_g and dbias_u (N
+ * values each) may each be NULL; they are summed in fp32 from the unrounded
+ * terms, in a fixed order. dG may be the same matrix as G, dU the same as U.
+ * M == 0 or K == 0 gives zero sums. Layout rules as gemm_bf16_epi. The rest of the
+ * layer's gradient are products: dA = dG * op(Bg)^T + dU * op(Bu)^T (two
+ * gemm_*_epi calls, the first one's D the second one's R), dBg = op(A)^T * dG and
+ * dBu = op(A)^T * dU.
+ */
+GEMM_API gemm_status_t gemm_bf16_gated_dact(gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N,
+                                            int64_t K, float alpha, const gemm_bf16_t *A,
+                                            int64_t lda, const gemm_bf16_t *B, int64_t ldb,
+                                            gemm_act_t act, const gemm_bf16_t *G, int64_t ldg,
+                                            const gemm_bf16_t *U, int64_t ldu, gemm_bf16_t *dG,
+                                            int64_t lddg, gemm_bf16_t *dU, int64_t lddu,
+                                            gemm_bf16_t *dbias_g, gemm_bf16_t *dbias_u,
+                                            cudaStream_t stream);
+GEMM_API gemm_status_t gemm_f16_gated_dact(gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N,
+                                           int64_t K, float alpha, const gemm_f16_t *A,
+                                           int64_t lda, const gemm_f16_t *B, int64_t ldb,
+                                           gemm_act_t act, const gemm_f16_t *G, int64_t ldg,
+                                           const gemm_f16_t *U, int64_t ldu, gemm_f16_t *dG,
+                                           int64_t lddg, gemm_f16_t *dU, int64_t lddu,
+                                           gemm_f16_t *dbias_g, gemm_f16_t *dbias_u,
+                                           cudaStream_t stream);
+
+/*
  * gemm_layer_norm_bf16, gemm_layer_norm_f16 -- layer norm of each row, with the
  * residual's addition:
  *

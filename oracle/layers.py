@@ -79,6 +79,18 @@ def linear_grad(dD, Z, act_name=None):
     return dz, dz.sum(axis=0)
 
 
+def gated(A, Bg, Bu, alpha=1.0, bias_g=None, bias_u=None, act_name="silu"):
+    """(D, G, U) of D = act(G) U with G = alpha A Bg + bias_g and U likewise."""
+    G, U = (linear(A, B, alpha, b)[1] for B, b in ((Bg, bias_g), (Bu, bias_u)))
+    return act(G, act_name) * U, G, U
+
+
+def gated_grad(dD, G, U, act_name="silu"):
+    """(dG, dU, dbias_g, dbias_u) from the gradient dD of act(G) U."""
+    dg, du = dD * U * act_slope(G, act_name), dD * act(G, act_name)
+    return dg, du, dg.sum(axis=0), du.sum(axis=0)
+
+
 def rms_norm(X, W=None, residual=None, eps=0.0):
     """(Y, H, rstd)."""
     h = X if residual is None else X + residual

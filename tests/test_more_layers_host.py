@@ -13,7 +13,16 @@ FAMILIES = {
                                Y=P, ldy=32, mean=P, rstd=P, s=None),
     "gemm_layer_norm_grad_{}": dict(M=16, N=32, dY=P, lddy=32, H=P, ldh=32, mean=P, rstd=P, W=P,
                                     dH=P, lddh=32, dX=P, lddx=32, dW=P, db=P, s=None),
+    "gemm_{}_gated": dict(opA=0, opB=0, M=16, N=32, K=64, alpha=1.0, A=P, lda=64, Bg=P, ldbg=32,
+                          Bu=P, ldbu=32, act=4, bias_g=P, bias_u=P, G=P, ldg=32, U=P, ldu=32, D=P,
+                          ldd=32, s=None),
+    "gemm_{}_gated_dact": dict(opA=0, opB=0, M=16, N=32, K=64, alpha=1.0, A=P, lda=64, B=P, ldb=32,
+                               act=4, G=P, ldg=32, U=P, ldu=32, dG=P, lddg=32, dU=P, lddu=32,
+                               dbias_g=P, dbias_u=P, s=None),
 }
+PRODUCT = [dict(M=-1), dict(N=-1), dict(K=-1), dict(M=BIG), dict(N=BIG), dict(K=BIG),
+           dict(A=None), dict(lda=56), dict(act=5), dict(act=-1)]
+FORMS = [dict(opA=2), dict(opB=-1), dict(opA=1, M=128)]
 # What each refuses: changes of the good call and the status.
 REFUSED = {
     "gemm_layer_norm_{}": [
@@ -27,12 +36,27 @@ REFUSED = {
                    dict(lddh=31), dict(lddx=31)]),
         (LAYOUT, [{k: P + 1} for k in ("dY", "H", "W", "dH", "dX", "dW", "db")]
          + [dict(mean=P + 2), dict(rstd=P + 2)])],
+    "gemm_{}_gated": [
+        (INVALID, PRODUCT + FORMS + [dict(Bg=None), dict(Bu=None), dict(D=None), dict(ldbg=24),
+                                     dict(ldbu=24), dict(opB=1), dict(opB=1, ldbg=64),
+                                     dict(ldd=31), dict(ldg=31), dict(ldu=31)]),
+        (LAYOUT, [{k: P + 1} for k in ("bias_g", "bias_u", "G", "U", "D")]
+         + [{k: P + 8} for k in ("A", "Bg", "Bu")] + [dict(lda=68), dict(ldbg=36), dict(ldbu=36)])],
+    "gemm_{}_gated_dact": [
+        (INVALID, PRODUCT + FORMS + [dict(B=None), dict(ldb=24), dict(opB=1)]
+         + [{k: None} for k in ("G", "U", "dG", "dU")] + [dict(act=0, G=None)]
+         + [{k: 31} for k in ("ldg", "ldu", "lddg", "lddu")]),
+        (LAYOUT, [{k: P + 1} for k in ("G", "U", "dG", "dU", "dbias_g", "dbias_u")]
+         + [dict(A=P + 8), dict(B=P + 8), dict(lda=68), dict(ldb=36)])],
 }
 # Empty problems: nothing is read, written or enqueued.
 EMPTY = {
     "gemm_layer_norm_{}": [dict(M=0), dict(N=0), dict(M=0, X=None, Y=None)],
     "gemm_layer_norm_grad_{}": [dict(N=0), dict(M=0, dW=None, db=None),
                                 dict(M=0, dW=None, db=None, dY=None, H=None, dX=None, mean=None)],
+    "gemm_{}_gated": [dict(M=0), dict(N=0), dict(M=0, A=None, D=None, G=None)],
+    "gemm_{}_gated_dact": [dict(N=0), dict(M=0, dbias_g=None, dbias_u=None),
+                           dict(M=0, dbias_g=None, dbias_u=None, G=None, dU=None)],
 }
 
 
@@ -60,6 +84,8 @@ def test_empty_problems_are_no_ops(gemm_mod, family, dtype):
 def test_cpu_tensors_are_refused(gemm_mod):
     import torch
     x, s = torch.zeros(8, 16, dtype=torch.bfloat16), torch.zeros(8)
-    for f in (lambda: gemm_mod.layer_norm(x, x), lambda: gemm_mod.layer_norm_grad(x, x, s, s, x)):
+    for f in (lambda: gemm_mod.gemm_gated(x, x, x, x[:, :8], trans_b=True),
+              lambda: gemm_mod.gemm_gated_dact(x, x, *[x[:, :8]] * 4, trans_b=True),
+              lambda: gemm_mod.layer_norm(x, x), lambda: gemm_mod.layer_norm_grad(x, x, s, s, x)):
         with pytest.raises(ValueError, match="CUDA"):
             f()

@@ -43,3 +43,28 @@ def test_layer_norm_grad_matches_differences(gain):
     _, H, m, s = L.layer_norm(X, W if gain else None, b, R, 0.1)
     dx, dw, db = L.layer_norm_grad(G, H, m, s, W if gain else None, E)
     differences(loss, [X, b, W], [dx, db, dw] if gain else [dx, db])
+
+
+def test_gated_closed_forms():
+    r = np.random.default_rng(1)
+    A, B = r.standard_normal((3, 4)), r.standard_normal((4, 5))
+    D, G, U = L.gated(A, B, 2 * B, act_name="none")
+    np.testing.assert_allclose(D, 2 * (A @ B) ** 2)
+    np.testing.assert_allclose(G, A @ B)
+    one = L.gated(A, B, 0 * B, 0.5, None, np.ones(5), "silu")[0]  # U = 1: the activation alone
+    np.testing.assert_allclose(one, L.linear(A, B, 0.5, act_name="silu")[0])
+
+
+@pytest.mark.parametrize("name", ["none", "gelu", "gelu_tanh", "silu"])
+def test_gated_grad_matches_differences(name):
+    r = np.random.default_rng(7)
+    A, Bg, Bu = r.standard_normal((3, 4)), r.standard_normal((4, 5)), r.standard_normal((4, 5))
+    bg, bu, E = r.standard_normal(5), r.standard_normal(5), r.standard_normal((3, 5))
+
+    def loss(A, Bg, Bu, bg, bu):
+        return (E * L.gated(A, Bg, Bu, 1.0, bg, bu, name)[0]).sum()
+
+    _, G, U = L.gated(A, Bg, Bu, 1.0, bg, bu, name)
+    dg, du, sg, su = L.gated_grad(E, G, U, name)
+    differences(loss, [A, Bg, Bu, bg, bu], [dg @ Bg.T + du @ Bu.T, A.T @ dg, A.T @ du, sg, su],
+                atol=1e-5)
