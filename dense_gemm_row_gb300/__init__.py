@@ -11,7 +11,8 @@ import importlib
 
 __all__ = ["gemm_f32", "gemm_bf16", "gemm_f16", "gemm_s8", "gemm_s8_noalloc", "gemm", "GemmError",
            "check_device_error", "lib", "gemm_epilogue", "gemm_dact", "act_grad", "rms_norm",
-           "rms_norm_grad", "gemm_gated", "gemm_gated_dact", "layer_norm", "layer_norm_grad"]
+           "rms_norm_grad", "gemm_gated", "gemm_gated_dact", "quantise_blocks",
+           "layer_norm", "layer_norm_grad"]
 
 
 def __getattr__(name):

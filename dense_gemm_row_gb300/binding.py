@@ -26,6 +26,7 @@ The linear-layer operators have one function each for CUDA tensors:
 ``gemm_epilogue`` (a product with bias, activation and residual in its
 epilogue), ``gemm_dact`` and ``act_grad`` (the gradient at the pre-activation),
 ``gemm_gated`` (two projections and their gated product), ``gemm_gated_dact``,
+``quantise_blocks`` (8-bit operands with a scale for each block of 128),
 ``rms_norm``, ``layer_norm`` and their gradients ``rms_norm_grad`` and
 ``layer_norm_grad``. The dtypes pick the C entry point. They
 check shapes, dtypes, strides and devices before the call and write into the
@@ -60,6 +61,8 @@ EXPORTED = ("gemm_f32", "gemm_bf16", "gemm_f16", "gemm_s8", "gemm_u8", "gemm_f16
             "gemm_rms_norm_bf16", "gemm_rms_norm_f16", "gemm_rms_norm_bf16_e4m3",
             "gemm_rms_norm_f16_e4m3", "gemm_rms_norm_grad_bf16", "gemm_rms_norm_grad_f16",
             "gemm_bf16_gated", "gemm_f16_gated", "gemm_bf16_gated_dact", "gemm_f16_gated_dact",
+            "gemm_e4m3_bf16_gated", "gemm_e4m3_f16_gated", "gemm_e4m3_block_bf16_epi",
+            "gemm_e4m3_block_f16_epi", "gemm_quantise_bf16_e4m3", "gemm_quantise_f16_e4m3",
             "gemm_layer_norm_bf16", "gemm_layer_norm_f16", "gemm_layer_norm_grad_bf16",
             "gemm_layer_norm_grad_f16")
 
@@ -133,6 +136,11 @@ def _load():
                                           vp, vp],
             f"gemm_{fmt}_gated": [op, op, i64, i64, i64, f32, vp, i64, vp, i64, vp, i64, op, vp,
                                   vp, vp, i64, vp, i64, vp, i64, vp],
+            f"gemm_e4m3_{fmt}_gated": [i64, i64, i64, f32, vp, i64, vp, i64, vp, i64, vp, i64, vp,
+                                       i64, vp, i64, op, vp, vp, vp, i64, vp, i64, vp, i64, vp],
+            f"gemm_e4m3_block_{fmt}_epi": [i64, i64, i64, f32, vp, i64, vp, i64, vp, i64, vp, i64,
+                                           op, vp, vp, i64, vp, i64, vp, i64, vp],
+            f"gemm_quantise_{fmt}_e4m3": [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp],
             f"gemm_{fmt}_gated_dact": [op, op, i64, i64, i64, f32, vp, i64, vp, i64, op, vp, i64,
                                        vp, i64, vp, i64, vp, i64, vp, vp, vp],
             f"gemm_layer_norm_{fmt}": [i64, i64, f32, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64,
@@ -384,7 +392,7 @@ def _load_layers():
     import torch  # noqa: F401  (the module links against torch's libraries)
     mod = importlib.import_module("dense_gemm_row_gb300._layers")
     for name in EXPORTED:
-        if any(part in name for part in ("_epi", "gated", "dact", "act_grad", "_norm")):
+        if any(part in name for part in ("_epi", "gated", "quantise", "dact", "act_grad", "_norm")):
             mod.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
     _layers = mod
     return mod
@@ -398,7 +406,9 @@ def gemm_epilogue(A, B, D, *, alpha=1.0, bias=None, act=None, residual=None, pre
     bfloat16 or float16 A, B: everything else has their dtype. float8_e4m3fn A
     and B (trans_b only: B stored N x K): D is bfloat16 or float16 and the
     product of row i and column j is scaled by scale_a[i] * scale_b[j] (float32
-    vectors, either may be None). bias (N values), residual (M x N, may be D
+    vectors, either may be None), or, block by block of 128 along K, by
+    scale_a[i, k // 128] * scale_b[j // 128, k // 128] (float32 matrices, as
+    quantise_blocks writes them with rows=1 for A and rows=128 for B). bias (N values), residual (M x N, may be D
     itself) and act ("relu", "gelu", "gelu_tanh", "silu" or None) may be left
     out; preact (M x N), when given, receives Z for gemm_dact or act_grad.
     A and B start on 16-byte boundaries with row strides in whole 16-byte units."""
@@ -463,19 +473,36 @@ def rms_norm_grad(dY, H, rstd, dX, *, weight=None, dh=None, dweight=None, stream
 
 
 def gemm_gated(A, Bg, Bu, D, *, act="silu", alpha=1.0, bias_gate=None, bias_up=None, gate=None,
-               up=None, trans_a=False, trans_b=False, stream=None):
+               up=None, trans_a=False, trans_b=False, scale_a=None, scale_gate=None, scale_up=None,
+               stream=None):
     """D = act(G) * U with G = alpha * op(A) * op(Bg) + bias_gate and
     U = alpha * op(A) * op(Bu) + bias_up, in one kernel; returns D.
 
     A is M x K (K x M with trans_a), Bg and Bu are K x N (N x K with trans_b), D
     M x N; all are bfloat16 or float16. bias_gate and bias_up (N values each) may be
     None; gate and up (M x N), when given, receive G and U for gemm_gated_dact. Bg
-    and Bu may be parts of one matrix. Layouts as gemm_epilogue."""
+    and Bu may be parts of one matrix. float8_e4m3fn A, Bg and Bu (trans_b only) come
+    with scales per block of 128: scale_a, scale_gate and scale_up as gemm_epilogue's
+    float32 matrices. Layouts as gemm_epilogue."""
     st = (_layers or _load_layers()).gemm_gated(A, Bg, Bu, D, act, alpha, bias_gate, bias_up,
-                                                gate, up, trans_a, trans_b, stream)
+                                                gate, up, trans_a, trans_b, scale_a, scale_gate,
+                                                scale_up, stream)
     if st:
         _check(st, "gemm_gated")
     return D
+
+
+def quantise_blocks(X, Y, scale, *, rows=1, stream=None):
+    """Y = X / scale in float8_e4m3fn with scale = max |X| / 448 over each block of
+    `rows` (1 or 128) x 128 values; returns Y.
+
+    X is bfloat16 or float16; scale is float32, ceil(M / rows) x ceil(N / 128) for an
+    M x N X. rows=1 makes an A and scale_a for gemm_epilogue or gemm_gated, rows=128 a
+    B and its scales; a product wants Y's rows in whole 16-byte units."""
+    st = (_layers or _load_layers()).quantise_blocks(X, Y, scale, rows, stream)
+    if st:
+        _check(st, "quantise_blocks")
+    return Y
 
 
 def gemm_gated_dact(A, B, G, U, dG, dU, *, act="silu", alpha=1.0, dbias_gate=None, dbias_up=None,

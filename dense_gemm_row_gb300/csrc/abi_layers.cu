@@ -51,12 +51,18 @@ gemm_status_t product(bool e4m3, gemm_op_t opA, gemm_op_t opB, int64_t M, int64_
         if (c.B2 == nullptr || c.ldb2 < (b_t ? K : N)) return GEMM_ERR_INVALID_VALUE;
         if (!aligned(c.B2, 16) || c.ldb2 % unit) return GEMM_ERR_UNSUPPORTED_LAYOUT;
       }
+      const int64_t kb = (K + 127) / 128;
+      if (c.block && (c.block_a == nullptr || c.ldsa < kb || c.block_b == nullptr || c.ldsb < kb))
+        return GEMM_ERR_INVALID_VALUE;
+      if (c.block && c.gated && (c.block_b2 == nullptr || c.ldsb2 < kb))
+        return GEMM_ERR_INVALID_VALUE;
     }
   }
   if (!aligned(c.bias, 2) || !aligned(c.R, 2) || !aligned(c.Z, 2) || !aligned(c.D, 2) ||
       !aligned(c.dbias, 2) || !aligned(c.scale_a, 4) || !aligned(c.scale_b, 4) ||
       !aligned(c.bias2, 2) || !aligned(c.R2, 2) || !aligned(c.Z2, 2) || !aligned(c.D2, 2) ||
-      !aligned(c.dbias2, 2))
+      !aligned(c.dbias2, 2) || !aligned(c.block_a, 4) || !aligned(c.block_b, 4) ||
+      !aligned(c.block_b2, 4))
     return GEMM_ERR_UNSUPPORTED_LAYOUT;
   const DeviceInfo *dev = nullptr;
   gemm_status_t st = device(&dev);
@@ -99,6 +105,25 @@ gemm_status_t forward8(bool bf16, int64_t M, int64_t N, int64_t K, float alpha, 
   return product(true, GEMM_OP_N, GEMM_OP_T, M, N, K, A, lda, B, ldb, c, act, stream);
 }
 
+gemm_status_t forward_block(bool bf16, int64_t M, int64_t N, int64_t K, float alpha,
+                            const uint8_t *A, int64_t lda, const float *scale_a, int64_t ldsa,
+                            const uint8_t *B, int64_t ldb, const float *scale_b, int64_t ldsb,
+                            gemm_act_t act, const uint16_t *bias, const uint16_t *R, int64_t ldr,
+                            uint16_t *Z, int64_t ldz, uint16_t *D, int64_t ldd,
+                            cudaStream_t stream) {
+  EpiCall c;
+  c.bf16 = bf16;
+  c.block = true;
+  c.alpha = alpha;
+  c.block_a = scale_a, c.ldsa = ldsa;
+  c.block_b = scale_b, c.ldsb = ldsb;
+  c.bias = bias;
+  c.R = R, c.ldr = ldr;
+  c.Z = Z, c.ldz = ldz;
+  c.D = D, c.ldd = ldd;
+  return product(true, GEMM_OP_N, GEMM_OP_T, M, N, K, A, lda, B, ldb, c, act, stream);
+}
+
 gemm_status_t gradient(bool bf16, gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N, int64_t K,
                        float alpha, const uint16_t *A, int64_t lda, const uint16_t *B,
                        int64_t ldb, gemm_act_t act, const uint16_t *Z, int64_t ldz, uint16_t *dZ,
@@ -128,6 +153,46 @@ gemm_status_t gated(bool bf16, gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t 
   c.Z2 = U, c.ldz2 = ldu;
   c.D = D, c.ldd = ldd;
   return product(false, opA, opB, M, N, K, A, lda, Bg, ldbg, c, act, stream);
+}
+
+gemm_status_t gated_block(bool bf16, int64_t M, int64_t N, int64_t K, float alpha,
+                          const uint8_t *A, int64_t lda, const float *scale_a, int64_t ldsa,
+                          const uint8_t *Bg, int64_t ldbg, const float *scale_g, int64_t ldsg,
+                          const uint8_t *Bu, int64_t ldbu, const float *scale_u, int64_t ldsu,
+                          gemm_act_t act, const uint16_t *bias_g, const uint16_t *bias_u,
+                          uint16_t *G, int64_t ldg, uint16_t *U, int64_t ldu, uint16_t *D,
+                          int64_t ldd, cudaStream_t stream) {
+  EpiCall c;
+  c.bf16 = bf16;
+  c.gated = c.block = true;
+  c.alpha = alpha;
+  c.block_a = scale_a, c.ldsa = ldsa;
+  c.block_b = scale_g, c.ldsb = ldsg;
+  c.block_b2 = scale_u, c.ldsb2 = ldsu;
+  c.B2 = Bu, c.ldb2 = ldbu;
+  c.bias = bias_g, c.bias2 = bias_u;
+  c.Z = G, c.ldz = ldg;
+  c.Z2 = U, c.ldz2 = ldu;
+  c.D = D, c.ldd = ldd;
+  return product(true, GEMM_OP_N, GEMM_OP_T, M, N, K, A, lda, Bg, ldbg, c, act, stream);
+}
+
+gemm_status_t quantise(bool bf16, int64_t rows, int64_t cols, int64_t block_rows,
+                       const uint16_t *X, int64_t ldx, uint8_t *Y, int64_t ldy, float *scale,
+                       int64_t lds, cudaStream_t stream) {
+  if (!size_ok(rows) || !size_ok(cols) || (block_rows != 1 && block_rows != 128))
+    return GEMM_ERR_INVALID_VALUE;
+  if (rows == 0 || cols == 0) return GEMM_OK;
+  if (X == nullptr || ldx < cols || Y == nullptr || ldy < cols || scale == nullptr ||
+      lds < (cols + 127) / 128)
+    return GEMM_ERR_INVALID_VALUE;
+  if (!aligned(X, 2) || !aligned(scale, 4)) return GEMM_ERR_UNSUPPORTED_LAYOUT;
+  const DeviceInfo *dev = nullptr;
+  gemm_status_t st = device(&dev);
+  if (st != GEMM_OK) return st;
+  return status(launch_quantise(bf16, static_cast<int>(rows), static_cast<int>(cols),
+                                static_cast<int>(block_rows), X, ldx, Y, ldy, scale, lds,
+                                stream));
 }
 
 gemm_status_t gated_gradient(bool bf16, gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N,
@@ -286,6 +351,42 @@ DGR_DACT(gemm_f16_dact, false)
   }
 DGR_GATED(gemm_bf16_gated, true)
 DGR_GATED(gemm_f16_gated, false)
+
+#define DGR_BLOCK(NAME, BF16)                                                                  \
+  gemm_status_t NAME(int64_t M, int64_t N, int64_t K, float alpha, const uint8_t *A,           \
+                     int64_t lda, const float *scale_a, int64_t ldsa, const uint8_t *B,        \
+                     int64_t ldb, const float *scale_b, int64_t ldsb, gemm_act_t act,          \
+                     const uint16_t *bias, const uint16_t *R, int64_t ldr, uint16_t *Z,        \
+                     int64_t ldz, uint16_t *D, int64_t ldd, cudaStream_t stream) {             \
+    return dgr::forward_block(BF16, M, N, K, alpha, A, lda, scale_a, ldsa, B, ldb, scale_b,    \
+                              ldsb, act, bias, R, ldr, Z, ldz, D, ldd, stream);                \
+  }
+DGR_BLOCK(gemm_e4m3_block_bf16_epi, true)
+DGR_BLOCK(gemm_e4m3_block_f16_epi, false)
+
+#define DGR_GATED8(NAME, BF16)                                                                 \
+  gemm_status_t NAME(int64_t M, int64_t N, int64_t K, float alpha, const uint8_t *A,           \
+                     int64_t lda, const float *scale_a, int64_t ldsa, const uint8_t *Bg,       \
+                     int64_t ldbg, const float *scale_g, int64_t ldsg, const uint8_t *Bu,      \
+                     int64_t ldbu, const float *scale_u, int64_t ldsu, gemm_act_t act,         \
+                     const uint16_t *bias_g, const uint16_t *bias_u, uint16_t *G, int64_t ldg, \
+                     uint16_t *U, int64_t ldu, uint16_t *D, int64_t ldd,                       \
+                     cudaStream_t stream) {                                                    \
+    return dgr::gated_block(BF16, M, N, K, alpha, A, lda, scale_a, ldsa, Bg, ldbg, scale_g,    \
+                            ldsg, Bu, ldbu, scale_u, ldsu, act, bias_g, bias_u, G, ldg, U,     \
+                            ldu, D, ldd, stream);                                              \
+  }
+DGR_GATED8(gemm_e4m3_bf16_gated, true)
+DGR_GATED8(gemm_e4m3_f16_gated, false)
+
+#define DGR_QUANTISE(NAME, BF16)                                                               \
+  gemm_status_t NAME(int64_t rows, int64_t cols, int64_t block_rows, const uint16_t *X,        \
+                     int64_t ldx, uint8_t *Y8, int64_t ldy, float *scale, int64_t lds,         \
+                     cudaStream_t stream) {                                                    \
+    return dgr::quantise(BF16, rows, cols, block_rows, X, ldx, Y8, ldy, scale, lds, stream);   \
+  }
+DGR_QUANTISE(gemm_quantise_bf16_e4m3, true)
+DGR_QUANTISE(gemm_quantise_f16_e4m3, false)
 
 #define DGR_GATED_DACT(NAME, BF16)                                                              \
   gemm_status_t NAME(gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N, int64_t K, float alpha, \

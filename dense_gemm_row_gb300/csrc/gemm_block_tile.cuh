@@ -1,0 +1,522 @@
+// gemm_block_tile.cuh -- e4m3 products with a scale for each block of 128 along k, on
+// 256-row tiles:
+//
+//   Z_ij = alpha sum_b sa[i][b] sb[j / 128][b] sum_{k in b} A_ik B_jk + bias_j,  D = act(Z) + R
+//   gated   D = act(G) U, where G and U are Z for two matrices B
+//
+// A block of 128 is one 128-byte row of a stage, so the accumulator is restarted for
+// every stage (4 MMAs) and its 256 x kN sums are added, scaled, into fp32 registers:
+// 128 per thread at kN = 256. That addition is what a k-block costs beside its MMAs
+// (512 cycles at the e4m3 rate): 32 KB of tensor memory to read per warp scheduler and
+// 128 packed multiply-adds. The scales of a thread are one value per row and one per
+// 128 columns, which a warp's columns never cross. The accumulators alternate, so that
+// the MMAs of the next k-block run meanwhile.
+//
+// Warps as in gemm_epi_tile.cuh, whose producer this kernel shares; the final epilogue
+// works on the registers. Each warp has two staging buffers: R of both of its blocks
+// of 64 columns is requested before the main loop, and D takes its place.
+#pragma once
+
+#include "gemm_epi_tile.cuh"
+
+namespace dgr {
+namespace {
+
+struct BlockScales {
+  const float *a, *b, *b2;  // b2: a gated layer's second B
+  int64_t lda, ldb, ldb2;
+  int KB;
+};
+
+// The scales of k-blocks kb .. kb + 3 of one row (zeros past the last).
+__device__ __forceinline__ float4 load_scales(const float *row, int kb, int KB, bool vec) {
+  if (row == nullptr) return make_float4(0.f, 0.f, 0.f, 0.f);
+  if (vec && kb + 4 <= KB) return __ldg(reinterpret_cast<const float4 *>(row + kb));
+  float4 v;
+  v.x = kb < KB ? __ldg(row + kb) : 0.f;
+  v.y = kb + 1 < KB ? __ldg(row + kb + 1) : 0.f;
+  v.z = kb + 2 < KB ? __ldg(row + kb + 2) : 0.f;
+  v.w = kb + 3 < KB ? __ldg(row + kb + 3) : 0.f;
+  return v;
+}
+__device__ __forceinline__ float pick(const float4 &v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// Three warpgroups: producer, MMAs and two idle warps; the epilogue's eight. They are
+// launched with 168 registers a thread, of which the first group keeps 40 and the
+// others take 232: 40 + 2 * 232 = 3 * 168.
+constexpr int kBlockThreads = 384, kBlockFirst = 4;  // the first epilogue warp
+
+template <int kN>
+constexpr int kBlockBufs = 512 / kN;  // accumulators in tensor memory
+
+template <int kN>
+using BlockSmem = EpiSmem<kN, 2>;
+
+// The leader's MMA loop: one accumulator per k-block.
+template <int kN>
+__device__ __forceinline__ void block_multiply(const EpiArgs &p, BlockSmem<kN> &sm,
+                                               uint32_t tmem_base, int unit, int units) {
+  using Cf = EpiCfg<kN, 2>;
+  constexpr int kBufs = kBlockBufs<kN>;
+  volatile int *abort = &sm.abort;
+  const int KB = (p.K - 1) / 128 + 1;
+  const uint64_t adesc0 = smem_desc(smem_u32(sm.a[0]), 16, kAtomBytes, 2u);
+  const uint64_t bdesc0 = smem_desc(smem_u32(sm.b[0]), 16, kAtomBytes, 2u);
+  uint32_t stage = 0, phase = 0, buf = 0, use = 0;
+  bool ok = true, any = false;
+  for (int t = unit; ok && t < p.tiles; t += units) {
+    for (int kb = 0; kb < KB; ++kb) {
+      if (!mbar_wait_lazy<true>(smem_u32(&sm.tmem_empty[buf]), use ^ 1u, abort, p.err_word,
+                                kWaitTmemEmpty) ||
+          !mbar_wait_lazy(smem_u32(&sm.full[stage]), phase, abort, p.err_word, kWaitFull)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint64_t ad = adesc0 + stage * (Cf::kABytes >> 4);
+      const uint64_t bd = bdesc0 + stage * (Cf::kBBytes >> 4);
+      const uint32_t d_tmem = tmem_base + buf * kN;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_f8_pair(d_tmem, ad + kk * 2, bd + kk * 2, p.idesc, kk > 0 ? 1u : 0u);
+        tc_commit_pair_mc(smem_u32(&sm.empty[stage]), 0x3);
+        tc_commit_pair_mc(smem_u32(&sm.tmem_full[buf]), 0x3);
+      }
+      __syncwarp();
+      any = true;
+      if (++stage == Cf::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if (++buf == kBufs) {
+        buf = 0;
+        use ^= 1u;
+      }
+    }
+  }
+  // Never leave with an MMA still reading shared memory or writing TMEM. (The
+  // same lane is elected each time, so its commit covers them all.)
+  if (any) {
+    if (elect_one()) tc_commit_pair_mc(smem_u32(&sm.drain), 0x1);
+    __syncwarp();
+    drain_wait(smem_u32(&sm.drain), 0, p.err_word);
+  }
+}
+
+// Adds s times 16 accumulator columns to sum[0 .. 7].
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// The final epilogue of a warp's 64 kBlocks columns: z = alpha sum + bias, and what
+// follows, block of 64 columns by block. bias: the tile's, from the warp's columns on.
+template <bool kBf16, int kCount>
+__device__ __forceinline__ void block_finish(const CUtensorMap &tmD, const CUtensorMap &tmZ,
+                                             const EpiArgs &p, const uint16_t *bias,
+                                             F2 (&sum)[32 * kCount],
+                                             const uint32_t (&stage)[2], int row0, int col0,
+                                             bool early_r, uint32_t rbar, uint32_t &rphase,
+                                             const CUtensorMap &tmR, int lane) {
+  const bool have_r = p.c.R != nullptr;
+#pragma unroll
+  for (int j = 0; j < 32 * kCount; j += 4) {
+    const uint4 q = *reinterpret_cast<const uint4 *>(bias + 2 * j);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sum[j + i] = fma2(sum[j + i], f2(p.c.alpha), unpack2<kBf16>(w[i]));
+  }
+  if (have_r && early_r && p.r_tma) {
+    wait_copy(rbar, rphase, p.err_word);
+    rphase ^= 1u;
+  }
+#pragma unroll
+  for (int c = 0; c < kCount; ++c) {
+    const int col = col0 + 64 * c;
+    if (p.c.Z != nullptr) {
+      stage_free(lane);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j] = pack2<kBf16>(sum[32 * c + 16 * h + j]);
+        stage_half(stage[c], lane, h, w);
+      }
+      store_block(&tmZ, p.z_tma, p.c.Z, p.c.ldz, row0, col, p.M, p.N, stage[c], lane);
+    }
+    if (have_r && !early_r) {
+      stage_free(lane);
+      if (p.r_tma) {
+        // The buffer's last accesses were ordinary ones where no TMA store followed them.
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(rbar, kStageCBytes);
+          tma_load_3d(stage[c], &tmR, rbar, col, row0, 0);
+        }
+        wait_copy(rbar, rphase, p.err_word);
+        rphase ^= 1u;
+      } else {
+        stage_block(p.c.R, p.c.ldr, row0, col, p.M, p.N, stage[c], lane);
+      }
+    } else if (!have_r) {
+      stage_free(lane);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t r[16];
+      F2 v[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = sum[32 * c + 16 * h + j];
+      if (p.c.act != kActNone)
+        with_act(p.c.act, [&](auto a) { act_values<decltype(a)::value>(v); });
+      if (have_r) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          ld_shared_v4(stage_unit(stage[c], lane, 4 * h + j), r[4 * j], r[4 * j + 1], r[4 * j + 2],
+                       r[4 * j + 3]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = add2(v[j], unpack2<kBf16>(r[j]));
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) r[j] = pack2<kBf16>(v[j]);
+      stage_half(stage[c], lane, h, r);
+    }
+    store_block(&tmD, p.d_tma, p.c.D, p.c.ldd, row0, col, p.M, p.N, stage[c], lane);
+  }
+}
+
+// The same for the gated layer: sum holds 64 columns of G, then the same ones of U.
+template <bool kBf16>
+__device__ __forceinline__ void block_finish_gated(const CUtensorMap &tmD, const CUtensorMap &tmG,
+                                                   const CUtensorMap &tmU, const EpiArgs &p,
+                                                   const uint16_t *bias, F2 (&sum)[64],
+                                                   const uint32_t (&stage)[2], int row0, int col,
+                                                   int lane) {
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const uint4 q = *reinterpret_cast<const uint4 *>(bias + 128 * which + 2 * j);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        sum[32 * which + j + i] =
+            fma2(sum[32 * which + j + i], f2(p.c.alpha), unpack2<kBf16>(w[i]));
+    }
+  }
+  stage_free(lane);
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    uint16_t *out = which ? p.c.Z2 : p.c.Z;
+    if (out == nullptr) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) w[j] = pack2<kBf16>(sum[32 * which + 16 * h + j]);
+      stage_half(stage[which], lane, h, w);
+    }
+    store_block(which ? &tmU : &tmG, which ? p.r_tma : p.z_tma, out, which ? p.c.ldz2 : p.c.ldz,
+                row0, col, p.M, p.N, stage[which], lane);
+  }
+  if (p.c.Z != nullptr) stage_free(lane);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[16];
+    F2 g[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) g[j] = sum[16 * h + j];
+    with_act(p.c.act, [&](auto a) { act_values<decltype(a)::value>(g); });
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack2<kBf16>(mul2(g[j], sum[32 + 16 * h + j]));
+    stage_half(stage[0], lane, h, w);
+  }
+  store_block(&tmD, p.d_tma, p.c.D, p.c.ldd, row0, col, p.M, p.N, stage[0], lane);
+}
+
+// Maps as gemm_epi_tile_kernel's.
+template <int kN, bool kGated>
+__global__ void __launch_bounds__(kBlockThreads, 1)
+    gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA,
+                           const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmD,
+                           const __grid_constant__ CUtensorMap tmZ,
+                           const __grid_constant__ CUtensorMap tmR,
+                           const __grid_constant__ std::conditional_t<kGated, CUtensorMap, NoMap> tmS,
+                           const __grid_constant__ EpiArgs p,
+                           const __grid_constant__ BlockScales sc) {
+  static_assert(!kGated || kN == 256, "a warp has one block of 64 columns of D");
+  constexpr int kBufs = kBlockBufs<kN>;
+  constexpr int kTileCols = kGated ? kN / 2 : kN;  // of D
+  constexpr int kCols = kN / 2;                    // accumulator columns of a warp
+  constexpr int kChunks = kCols / 16;
+  extern __shared__ uint8_t smem_raw[];
+  // Same offset in both CTAs of the pair, as the pair MMA needs.
+  BlockSmem<kN> &sm = *reinterpret_cast<BlockSmem<kN> *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int unit = static_cast<int>(blockIdx.x >> 1), units = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < EpiCfg<kN, 2>::kStages; ++s) {
+      mbar_init(smem_u32(&sm.full[s]), 1);
+      mbar_init(smem_u32(&sm.empty[s]), 1);
+    }
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(smem_u32(&sm.tmem_full[i]), 1);
+      mbar_init(smem_u32(&sm.tmem_empty[i]), 2 * kEpiWarps);
+    }
+    mbar_init(smem_u32(&sm.drain), 1);
+    for (int i = 0; i < kEpiWarps; ++i) mbar_init(smem_u32(&sm.arrived[i]), 1);
+    sm.abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    if (p.d_tma) prefetch_tmap(&tmD);
+    if (p.r_tma) prefetch_tmap(&tmR);
+    if constexpr (kGated) prefetch_tmap(&tmS);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&sm.tmem_base), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  cluster_sync();  // the leader's barriers exist before the peer signals them
+  tc_fence_after_sync();
+  const uint32_t tmem_base = sm.tmem_base;
+  // Launched as a programmatic dependent, as gemm_epi_tile_kernel.
+  grid_launch_dependents();
+
+  if (warp < kBlockFirst) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+    if (warp == 0) {
+      const CUtensorMap *b = &tmB;
+      if constexpr (kGated) b = rank == 0 ? &tmB : &tmS;
+      epi_produce<true, kN, false, true, 2, kGated>(tmA, *b, p, sm, rank, unit, units);
+    } else if (warp == 1 && rank == 0) {
+      block_multiply<kN>(p, sm, tmem_base, unit, units);
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
+    // Every epilogue warp walks the same tiles and meets the same named barriers;
+    // after a wait that gave up it skips the work, not the barriers.
+    grid_dependency_wait();
+    const int e = warp - kBlockFirst, quarter = warp & 3, half = e >> 2;
+    const uint32_t stage[2] = {smem_u32(sm.stage[2 * e]), smem_u32(sm.stage[2 * e + 1])};
+    const uint32_t rbar = smem_u32(&sm.arrived[e]);
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const bool have_r = !kGated && p.c.R != nullptr, early_r = have_r && p.c.Z == nullptr;
+    auto whole = [](const float *q, int64_t ld) {
+      return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % 4 == 0;
+    };
+    const bool vec_a = whole(sc.a, sc.lda), vec_b = whole(sc.b, sc.ldb);
+    const bool vec_b2 = kGated && whole(sc.b2, sc.ldb2);
+    uint32_t rphase = 0, buf = 0, use = 0;
+    bool ok = true;
+    for (int t = unit; t < p.tiles; t += units) {
+      int tm, tn;
+      tile_coords<kEpiGroupM>(t, p.tiles_m, p.tiles_n, tm, tn);
+      const int row0 = tm * 256 + static_cast<int>(rank) * kBM + quarter * 32;
+      const int local0 = half * (kTileCols / 2), col0 = tn * kTileCols + local0;
+      epilogue_sync();  // every warp has read the previous tile's bias
+      for (int i = threadIdx.x - 32 * kBlockFirst; i < kN; i += 32 * kEpiWarps) {
+        const uint16_t *bias = !kGated || i < kTileCols ? p.c.bias : p.c.bias2;
+        const int j = tn * kTileCols + (kGated ? i & (kTileCols - 1) : i);
+        sm.bias[i] = bias && j < p.N ? bias[j] : 0;
+      }
+      epilogue_sync();
+      // (The warp reads the flag as one: its lanes must take the same branch.)
+      if (__any_sync(0xffffffffu, !ok || *static_cast<volatile int *>(&sm.abort))) {
+        ok = false;
+        continue;
+      }
+      if (early_r) {
+        stage_free(lane);
+        if (p.r_tma) {
+          // The buffers' last accesses were ordinary ones where no TMA store followed.
+          if (!p.d_tma) {
+            fence_proxy_async_shared();
+            __syncwarp();
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(rbar, kCols / 64 * kStageCBytes);
+#pragma unroll
+            for (int c = 0; c < kCols / 64; ++c)
+              tma_load_3d(stage[c], &tmR, rbar, col0 + 64 * c, row0, 0);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCols / 64; ++c)
+            stage_block(p.c.R, p.c.ldr, row0, col0 + 64 * c, p.M, p.N, stage[c], lane);
+        }
+      }
+      const int64_t row = row0 + lane, jb = col0 / 128;
+      const float *sa = row < p.M ? sc.a + row * sc.lda : nullptr;
+      const float *sb = col0 < p.N ? sc.b + jb * sc.ldb : nullptr;
+      const float *sb2 = kGated && col0 < p.N ? sc.b2 + jb * sc.ldb2 : nullptr;
+      float4 a4 = load_scales(sa, 0, sc.KB, vec_a), b4 = load_scales(sb, 0, sc.KB, vec_b);
+      float4 u4 = load_scales(sb2, 0, sc.KB, vec_b2);
+      F2 sum[kCols / 2];
+#pragma unroll
+      for (int j = 0; j < kCols / 2; ++j) sum[j] = f2(0.f);
+      for (int kb0 = 0; ok && kb0 < sc.KB; kb0 += 4) {
+        const float4 an = load_scales(sa, kb0 + 4, sc.KB, vec_a);
+        const float4 bn = load_scales(sb, kb0 + 4, sc.KB, vec_b);
+        const float4 un = load_scales(sb2, kb0 + 4, sc.KB, vec_b2);
+        const int left = min(sc.KB - kb0, 4);
+#pragma unroll 1
+        for (int i = 0; i < left; ++i) {
+          const F2 s = f2(pick(a4, i) * pick(b4, i));
+          const F2 s2 = kGated ? f2(pick(a4, i) * pick(u4, i)) : s;
+          if (!mbar_wait_lazy(smem_u32(&sm.tmem_full[buf]), use, &sm.abort, p.err_word,
+                              kWaitTmemFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t taddr = tmem_base + lane_addr + buf * kN + local0;
+          // The next 16 columns are on their way while these are added.
+          uint32_t r[2][16];
+          auto column = [&](int c) {  // gated: 64 of G's columns, then 64 of U's
+            return kGated && c >= kChunks / 2 ? kTileCols + 16 * (c - kChunks / 2) : 16 * c;
+          };
+          tmem_ld_x16(taddr + column(0), r[0]);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            tmem_ld_wait();
+            if (c + 1 < kChunks) {
+              tmem_ld_x16(taddr + column(c + 1), r[(c + 1) & 1]);
+            } else {  // all in registers: the MMAs may have it
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.tmem_empty[buf]), 0));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              sum[8 * c + j] = fma2(f2(__uint_as_float(r[c & 1][2 * j]),
+                                       __uint_as_float(r[c & 1][2 * j + 1])),
+                                    kGated && c >= kChunks / 2 ? s2 : s, sum[8 * c + j]);
+          }
+          if (++buf == kBufs) {
+            buf = 0;
+            use ^= 1u;
+          }
+        }
+        a4 = an, b4 = bn, u4 = un;
+      }
+      if (!ok) {
+        // Never leave with a copy of R still writing into shared memory.
+        if (early_r && p.r_tma) {
+          wait_copy(rbar, rphase, p.err_word);
+          rphase ^= 1u;
+        }
+        continue;
+      }
+      const uint16_t *bias = sm.bias + local0;
+      if constexpr (kGated) {
+        if (p.c.bf16) {
+          block_finish_gated<true>(tmD, tmZ, tmR, p, bias, sum, stage, row0, col0, lane);
+        } else {
+          block_finish_gated<false>(tmD, tmZ, tmR, p, bias, sum, stage, row0, col0, lane);
+        }
+      } else if (p.c.bf16) {
+        block_finish<true, kCols / 64>(tmD, tmZ, p, bias, sum, stage, row0, col0, early_r, rbar,
+                                       rphase, tmR, lane);
+      } else {
+        block_finish<false, kCols / 64>(tmD, tmZ, p, bias, sum, stage, row0, col0, early_r, rbar,
+                                        rphase, tmR, lane);
+      }
+    }
+    // Never leave with a TMA store still reading the staging buffers (its writes
+    // are complete when the grid is).
+    if (lane == 0) bulk_wait_read_all();
+    __syncwarp();
+  }
+
+  tc_fence_before_sync();
+  cluster_sync();  // both CTAs done: no MMA, copy or arrival targets either
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+template <int kN, bool kGated>
+cudaError_t launch_block_form(const DeviceInfo &dev, int M, int N, int K, const void *A,
+                              int64_t lda, const void *B, int64_t ldb, const EpiCall &epi,
+                              cudaStream_t stream) {
+  using Cf = EpiCfg<kN, 2>;
+  constexpr int kTileCols = kGated ? kN / 2 : kN;
+  static_assert(sizeof(BlockSmem<kN>) + 1024 <= 232448, "shared memory");
+  const size_t smem = sizeof(BlockSmem<kN>) + 1024;
+  auto kern = gemm_block_tile_kernel<kN, kGated>;
+  const int pairs = pair_capacity(dev, reinterpret_cast<const void *>(kern), smem, kBlockThreads);
+  if (pairs < 1) return cudaErrorInvalidConfiguration;
+  constexpr CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  CUtensorMap tmA, tmB, tmD, tmZ, tmR;
+  std::conditional_t<kGated, CUtensorMap, NoMap> tmS;
+  std::memset(&tmD, 0, sizeof tmD);
+  std::memset(&tmZ, 0, sizeof tmZ);
+  std::memset(&tmR, 0, sizeof tmR);
+  std::memset(&tmS, 0, sizeof tmS);
+  if (!make_tmap(&tmA, dt, 1, A, M, K, lda, 1, 0, kBM, 128) ||
+      !make_tmap(&tmB, dt, 1, B, N, K, ldb, 1, 0, Cf::kBNLoad, 128))
+    return cudaErrorInvalidValue;
+  EpiArgs p;
+  p.M = M, p.N = N, p.K = K;
+  p.tiles_m = (M - 1) / Cf::kTileM + 1;  // sizes up to 2^31 - 1
+  p.tiles_n = (N - 1) / kTileCols + 1;
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  if (tiles > 0x7fffffffLL - pairs) return cudaErrorInvalidValue;
+  p.tiles = static_cast<int>(tiles);
+  p.a_t = false, p.b_t = true;
+  p.d_tma = out_tmap(&tmD, epi.bf16, epi.D, epi.ldd, M, N);
+  p.z_tma = out_tmap(&tmZ, epi.bf16, epi.Z, epi.ldz, M, N);
+  if constexpr (kGated) {
+    if (!make_tmap(&tmS, dt, 1, epi.B2, N, K, epi.ldb2, 1, 0, Cf::kBNLoad, 128))
+      return cudaErrorInvalidValue;
+    p.r_tma = out_tmap(&tmR, epi.bf16, epi.Z2, epi.ldz2, M, N);
+  } else {
+    p.r_tma = block_tmap(&tmR, epi.bf16, epi.R, epi.ldr, M, N);
+  }
+  p.s_tma = false;
+  p.idesc = idesc_mma(0u, false, false, Cf::kTileM, kN);
+  p.err_word = dev.err_word;
+  p.part = nullptr, p.part_apart = 0;
+  p.c = epi;
+  const BlockScales sc{epi.block_a, epi.block_b,  epi.block_b2,     epi.ldsa,
+                       epi.ldsb,    epi.ldsb2, (K - 1) / 128 + 1};
+  const int units = static_cast<int>(tiles < pairs ? tiles : pairs);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(units), 1, 1);
+  cfg.blockDim = dim3(kBlockThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, tmZ, tmR, tmS, p, sc);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace
+}  // namespace dgr

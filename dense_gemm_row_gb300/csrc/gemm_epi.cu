@@ -43,6 +43,16 @@ cudaError_t launch_gated_split_fwd(const DeviceInfo &dev, int mp, bool b_t, int 
 cudaError_t launch_gated_split_grad(const DeviceInfo &dev, int mp, bool b_t, int M, int N, int K,
                                     const void *A, int64_t lda, const void *B, int64_t ldb,
                                     const EpiCall &epi, float *part, cudaStream_t stream);
+// The block-scaled e4m3 product's (gemm_block*.cu).
+cudaError_t launch_block_fwd(const DeviceInfo &dev, int tile_n, int M, int N, int K, const void *A,
+                             int64_t lda, const void *B, int64_t ldb, const EpiCall &epi,
+                             cudaStream_t stream);
+cudaError_t launch_block_gated(const DeviceInfo &dev, int M, int N, int K, const void *A,
+                               int64_t lda, const void *B, int64_t ldb, const EpiCall &epi,
+                               cudaStream_t stream);
+cudaError_t launch_block_split(const DeviceInfo &dev, int mp, int M, int N, int K, const void *A,
+                               int64_t lda, const void *B, int64_t ldb, const EpiCall &epi,
+                               cudaStream_t stream);
 
 namespace {
 
@@ -127,6 +137,10 @@ cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t
   const EpiPlan plan = plan_epi(dev, a_t, M, N, (K - 1) / (e4m3 ? 128 : 64) + 1, ragged,
                                 epi.gated && !epi.grad);
   const int mp = plan.split_rows, tile_n = plan.tile_n;
+  if (epi.block)
+    return mp          ? launch_block_split(dev, mp, M, N, K, A, lda, B, ldb, epi, stream)
+           : epi.gated ? launch_block_gated(dev, M, N, K, A, lda, B, ldb, epi, stream)
+                       : launch_block_fwd(dev, tile_n, M, N, K, A, lda, B, ldb, epi, stream);
   if (epi.gated && !epi.grad)
     return mp ? launch_gated_split_fwd(dev, mp, b_t, M, N, K, A, lda, B, ldb, epi, nullptr, stream)
               : launch_gated_fwd(dev, a_t, b_t, M, N, K, A, lda, B, ldb, epi, stream);

@@ -16,6 +16,12 @@
 // Operands: A (tokens) as stored M x K; B stored N x K (K-major) or K x N
 // (N-major, 16-bit only); 16-bit or e4m3.
 //
+// Block-scaled e4m3 (kBlock; what is computed: gemm_block_tile.cuh): every k-block has
+// an accumulator of its own, of up to eight in turn, and the four warps that drain
+// tensor memory add each one, scaled, into registers. A warp's rows are the weights',
+// with one scale per k-block, its columns the tokens, whose scales it puts in shared
+// memory a k-block ahead.
+//
 // A gated layer's tile has 64 columns of D: the MMA's rows are those of the first
 // B, then the same ones of the second, and a finishing thread adds both.
 #pragma once
@@ -33,6 +39,17 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 
@@ -59,7 +76,20 @@ struct SplitCfg {
   static constexpr uint32_t kTmem = kMP < 32 ? 32 : kMP;
 };
 
+// Accumulators of the block-scaled form: half of tensor memory, two CTAs share an SM.
 template <int kMP>
+constexpr int kSplitBufs = kMP <= 32 ? 8 : 256 / kMP;
+
+template <int kMP, bool kBlock>
+struct SplitBlock {};
+template <int kMP>
+struct SplitBlock<kMP, true> {
+  alignas(16) float scale[4][2][kMP];  // a draining warp's, of two k-blocks
+  uint64_t acc_full[kSplitBufs<kMP>];
+  uint64_t acc_empty[kSplitBufs<kMP>];
+};
+
+template <int kMP, bool kBlock>
 struct __align__(1024) SplitSmem {
   uint8_t b[SplitCfg<kMP>::kStages][SplitCfg<kMP>::kBBytes];  // also the partial sums
   uint8_t a[SplitCfg<kMP>::kStages][SplitCfg<kMP>::kABytes];
@@ -69,6 +99,7 @@ struct __align__(1024) SplitSmem {
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
+  SplitBlock<kMP, kBlock> block;
 };
 
 struct NoSecond {};
@@ -267,8 +298,72 @@ __device__ __forceinline__ void gated_finish(const SplitArgs &p, uint32_t red, i
   }
 }
 
+// The block-scaled sums of k-blocks kb0 .. kb1 - 1 by one of the four warps that drain
+// tensor memory: 32 rows of the transposed product, token j in sum[j / 2]. Returns
+// whether every accumulator arrived.
+template <int kMP, bool kPair>
+__device__ __forceinline__ bool split_blocks(const SplitArgs &p, SplitSmem<kMP, true> &sm,
+                                             uint32_t tmem_base, int quarter, int lane, int m0,
+                                             int n0, int kb0, int kb1, F2 (&sum)[kMP / 2]) {
+  constexpr int kBufs = kSplitBufs<kMP>, kOwn = (kMP + 31) / 32;  // tokens per lane
+  const bool second = kPair && quarter >= 2;
+  const float *sb = second ? p.c.block_b2 + n0 / 128 * p.c.ldsb2
+                           : p.c.block_b + n0 / 128 * p.c.ldsb;
+  const float *sa = p.c.block_a + static_cast<int64_t>(m0 + lane) * p.c.ldsa;
+  auto load = [&](int kb, float (&s)[kOwn]) {
+    const float b = kb < kb1 ? __ldg(sb + kb) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      s[i] = kb < kb1 && lane + 32 * i < kMP && m0 + lane + 32 * i < p.M
+                 ? __ldg(sa + 32 * i * p.c.ldsa + kb) * b
+                 : 0.f;
+  };
+#pragma unroll
+  for (int j = 0; j < kMP / 2; ++j) sum[j] = f2(0.f);
+  float next[kOwn];
+  load(kb0, next);
+  uint32_t buf = 0, use = 0;
+  for (int kb = kb0; kb < kb1; ++kb) {
+    float *slot = sm.block.scale[quarter][(kb - kb0) & 1];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (lane + 32 * i < kMP) slot[lane + 32 * i] = next[i];
+    load(kb + 1, next);
+    __syncwarp();
+    if (!mbar_wait_lazy(smem_u32(&sm.block.acc_full[buf]), use, &sm.abort, p.err_word, kWaitTmemFull))
+      return false;
+    tc_fence_after_sync();
+    const uint32_t taddr =
+        tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kMP;
+#pragma unroll
+    for (int c = 0; c < kMP; c += 16) {
+      if (c < p.mp) {
+        uint32_t r[16];
+        tmem_ld_x16(taddr + c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 s = *reinterpret_cast<const float4 *>(slot + c + j);
+          sum[(c + j) / 2] = fma2(f2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                  f2(s.x, s.y), sum[(c + j) / 2]);
+          sum[(c + j) / 2 + 1] = fma2(f2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
+                                      f2(s.z, s.w), sum[(c + j) / 2 + 1]);
+        }
+      }
+    }
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.block.acc_empty[buf]));
+    if (++buf == kBufs) {
+      buf = 0;
+      use ^= 1u;
+    }
+  }
+  return true;
+}
+
 // tmS: a gated layer's second B.
-template <bool kE4m3, int kMP, bool kGrad, bool kGated>
+template <bool kE4m3, int kMP, bool kGrad, bool kGated, bool kBlock>
 __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     gemm_epi_split_kernel(const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ CUtensorMap tmB,
@@ -278,8 +373,10 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   constexpr int kBK = kE4m3 ? 128 : 64;
   constexpr bool kPair = kGated && !kGrad;
   constexpr int kCols = kPair ? kSplitN / 2 : kSplitN;  // of D in a tile
+  constexpr int kBufs = kBlock ? kSplitBufs<kMP> : 1;
+  constexpr uint32_t kTmem = kBlock ? kBufs * kMP : Cf::kTmem;
   extern __shared__ uint8_t smem_raw[];
-  SplitSmem<kMP> &sm = *reinterpret_cast<SplitSmem<kMP> *>(
+  SplitSmem<kMP, kBlock> &sm = *reinterpret_cast<SplitSmem<kMP, kBlock> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   volatile int *abort = &sm.abort;
@@ -293,6 +390,12 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     }
     mbar_init(smem_u32(&sm.done), 1);
     mbar_init(smem_u32(&sm.drain), 1);
+    if constexpr (kBlock) {
+      for (int i = 0; i < kBufs; ++i) {
+        mbar_init(smem_u32(&sm.block.acc_full[i]), 1);
+        mbar_init(smem_u32(&sm.block.acc_empty[i]), 4);
+      }
+    }
     sm.abort = 0;
     fence_mbar_init();
     prefetch_tmap(&tmA);
@@ -300,7 +403,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     if constexpr (kPair) prefetch_tmap(&tmS);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&sm.tmem_base), Cf::kTmem);
+    tmem_alloc(smem_u32(&sm.tmem_base), kTmem);
     tmem_relinquish();
   }
   tc_fence_before_sync();
@@ -376,9 +479,16 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                                   : smem_desc(smem_u32(sm.b[0]), kRowBytes * 64, kAtomBytes, 2u);
     const uint64_t xdesc = smem_desc(smem_u32(sm.a[0]), 16, kAtomBytes, 2u);
     const uint32_t wstep = (kmajor ? 32u : kRowBytes * 16) >> 4;
-    uint32_t stage = 0, phase = 0;
+    uint32_t stage = 0, phase = 0, buf = 0, use = 0;
     bool ok = true, any = false;
     for (int kb = kb0; kb < kb1; ++kb) {
+      if constexpr (kBlock) {
+        if (!mbar_wait_lazy(smem_u32(&sm.block.acc_empty[buf]), use ^ 1u, abort, p.err_word,
+                            kWaitTmemEmpty)) {
+          ok = false;
+          break;
+        }
+      }
       if (!mbar_wait_lazy(smem_u32(&sm.full[stage]), phase, abort, p.err_word, kWaitFull)) {
         ok = false;
         break;
@@ -389,14 +499,21 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          const uint32_t acc = kk > 0 || kb > kb0 ? 1u : 0u;
+          const uint32_t acc = kk > 0 || (!kBlock && kb > kb0) ? 1u : 0u;
           if constexpr (kE4m3) {
-            tc_mma_f8(tmem_base, wd + kk * wstep, xd + kk * 2, p.idesc, acc);
+            tc_mma_f8(tmem_base + buf * kMP, wd + kk * wstep, xd + kk * 2, p.idesc, acc);
           } else {
             tc_mma_f16(tmem_base, wd + kk * wstep, xd + kk * 2, p.idesc, acc);
           }
         }
         tc_commit(smem_u32(&sm.empty[stage]));
+        if constexpr (kBlock) tc_commit(smem_u32(&sm.block.acc_full[buf]));
+      }
+      if constexpr (kBlock) {
+        if (++buf == kBufs) {
+          buf = 0;
+          use ^= 1u;
+        }
       }
       __syncwarp();
       any = true;
@@ -430,10 +547,15 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
       split_load_cols<kGrad>(p, col, cols);
       split_load_row<kGrad>(p, m0 + t / wq, col, first);
     }
+    F2 blocks[kBlock ? kMP / 2 : 1];
     int got = 0;
-    if (lane == 0)
-      got = mbar_wait_bounded(smem_u32(&sm.done), 0, abort, p.err_word, kWaitTmemFull);
-    got = __shfl_sync(0xffffffffu, got, 0);
+    if constexpr (kBlock) {
+      got = split_blocks<kMP, kPair>(p, sm, tmem_base, quarter, lane, m0, n0, kb0, kb1, blocks);
+    } else {
+      if (lane == 0)
+        got = mbar_wait_bounded(smem_u32(&sm.done), 0, abort, p.err_word, kWaitTmemFull);
+      got = __shfl_sync(0xffffffffu, got, 0);
+    }
     // Every MMA has completed and every copy was consumed by one, so the stages
     // are free: partial sums [row][column], lanes on columns. A CTA whose wait
     // gave up (recorded in the error word, which is what counts) has NaN for sums,
@@ -445,15 +567,17 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     for (int c = 0; c < kMP; c += 16) {
       if (c < p.mp) {
         uint32_t r[16];
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-            "%10, %11, %12, %13, %14, %15}, [%16];\n"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-              "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-            : "r"(taddr + c)
-            : "memory");
-        tmem_ld_wait();
+        if constexpr (kBlock) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            float lo, hi;
+            split(blocks[(c + j) / 2], lo, hi);
+            r[j] = __float_as_uint(lo), r[j + 1] = __float_as_uint(hi);
+          }
+        } else {
+          tmem_ld_x16(taddr + c, r);
+          tmem_ld_wait();
+        }
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           red[(c + j) * kSplitN] = got ? __uint_as_float(r[j]) : __uint_as_float(0x7fffffffu);
@@ -538,7 +662,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
   }
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem_base, Cf::kTmem);
+    tmem_dealloc(tmem_base, kTmem);
   }
 }
 
@@ -568,20 +692,21 @@ inline bool split_clusters_fit(const DeviceInfo &dev, const void *kern, size_t s
   return n > 0;
 }
 
-template <bool kE4m3, int kMP, bool kGrad, bool kGated>
+template <bool kE4m3, int kMP, bool kGrad, bool kGated, bool kBlock>
 cudaError_t launch_split_form(const DeviceInfo &dev, bool b_t, int M, int N, int K, const void *A,
                               int64_t lda, const void *B, int64_t ldb, const EpiCall &epi,
                               float *part, cudaStream_t stream) {
   using Cf = SplitCfg<kMP>;
   constexpr int kEs = kE4m3 ? 1 : 2, kBK = kE4m3 ? 128 : 64;
   // 228 KiB of shared memory per SM, 1 KiB of it reserved per CTA.
-  static_assert(kSplitCtasPerSm * (sizeof(SplitSmem<kMP>) + 2048) <= 228 * 1024, "shared memory");
+  static_assert(kSplitCtasPerSm * (sizeof(SplitSmem<kMP, kBlock>) + 2048) <= 228 * 1024,
+                "shared memory");
   static_assert(Cf::kStages * Cf::kBBytes >= kMP * kSplitN * 4 ||
                     Cf::kStages * (Cf::kBBytes + Cf::kABytes) >= kMP * kSplitN * 4,
                 "partial sums fit in the stages");
-  const size_t smem = sizeof(SplitSmem<kMP>) + 1024;
+  const size_t smem = sizeof(SplitSmem<kMP, kBlock>) + 1024;
   constexpr bool kPair = kGated && !kGrad;
-  auto kern = gemm_epi_split_kernel<kE4m3, kMP, kGrad, kGated>;
+  auto kern = gemm_epi_split_kernel<kE4m3, kMP, kGrad, kGated, kBlock>;
   const void *kp = reinterpret_cast<const void *>(kern);
   cudaError_t e = set_max_dynamic_smem(kp, static_cast<int>(smem), dev.device);
   if (e != cudaSuccess) return e;
@@ -645,15 +770,15 @@ cudaError_t launch_split_form(const DeviceInfo &dev, bool b_t, int M, int N, int
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <bool kE4m3, bool kGrad, bool kGated = false>
+template <bool kE4m3, bool kGrad, bool kGated = false, bool kBlock = false>
 cudaError_t launch_split(const DeviceInfo &dev, int mp, bool b_t, int M, int N, int K,
                          const void *A, int64_t lda, const void *B, int64_t ldb,
                          const EpiCall &epi, float *part, cudaStream_t stream) {
   switch (mp) {
-    case 16: return launch_split_form<kE4m3, 16, kGrad, kGated>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
-    case 32: return launch_split_form<kE4m3, 32, kGrad, kGated>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
-    case 64: return launch_split_form<kE4m3, 64, kGrad, kGated>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
-    default: return launch_split_form<kE4m3, 128, kGrad, kGated>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
+    case 16: return launch_split_form<kE4m3, 16, kGrad, kGated, kBlock>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
+    case 32: return launch_split_form<kE4m3, 32, kGrad, kGated, kBlock>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
+    case 64: return launch_split_form<kE4m3, 64, kGrad, kGated, kBlock>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
+    default: return launch_split_form<kE4m3, 128, kGrad, kGated, kBlock>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
   }
 }
 

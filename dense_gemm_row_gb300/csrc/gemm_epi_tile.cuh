@@ -85,8 +85,8 @@ struct __align__(1024) EpiSmem {
   float scale[kN];
   uint64_t full[Cf::kStages];
   uint64_t empty[Cf::kStages];
-  uint64_t tmem_full[2];
-  uint64_t tmem_empty[2];
+  uint64_t tmem_full[512 / kN];  // two accumulators are used, but for block scales all
+  uint64_t tmem_empty[512 / kN];
   uint64_t arrived[kEpiWarps];  // R is in a warp's buffer
   uint64_t drain;
   uint32_t tmem_base;

@@ -862,7 +862,8 @@ inline bool make_tmap(CUtensorMap *tm, CUtensorMapDataType dt, int esize, const 
 
 // Co-resident CTA pairs for a pair kernel on this device (0 if pairs are not
 // available), queried once per device and kernel.
-inline int pair_capacity(const DeviceInfo &dev, const void *kern, size_t smem) {
+inline int pair_capacity(const DeviceInfo &dev, const void *kern, size_t smem,
+                         int threads = kThreads) {
   static std::mutex mu;
   static std::map<std::pair<const void *, int>, int> cache;
   std::lock_guard<std::mutex> lock(mu);
@@ -873,7 +874,7 @@ inline int pair_capacity(const DeviceInfo &dev, const void *kern, size_t smem) {
   if (set_max_dynamic_smem(kern, static_cast<int>(smem), dev.device) == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * static_cast<unsigned>(dev.sm_count / 2), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -227,6 +227,11 @@ struct EpiCall {
   uint16_t *D2 = nullptr;
   int64_t ldd2 = 0;
   uint16_t *dbias2 = nullptr;
+  // Scales per block of 128 of k (e4m3, forward): block_a[i][b] of row i, block_b[j /
+  // 128][b] of column j, block_b2 likewise of B2; row strides lds*.
+  const float *block_a = nullptr, *block_b = nullptr, *block_b2 = nullptr;
+  int64_t ldsa = 0, ldsb = 0, ldsb2 = 0;
+  bool block = false;
 };
 // The product with that epilogue. 16-bit A and B of the call's format, or, with
 // e4m3, 8-bit A (M x K) and B stored N x K. Layout already checked: A and B
@@ -234,6 +239,12 @@ struct EpiCall {
 cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t, int M, int N,
                             int K, const void *A, int64_t lda, const void *B, int64_t ldb,
                             const EpiCall &epi, cudaStream_t stream);
+
+// e4m3 values and a scale per block of block_rows (1 or 128) x 128 of a 16-bit matrix
+// (quantise.cu).
+cudaError_t launch_quantise(bool bf16, int rows, int cols, int block_rows, const uint16_t *X,
+                            int64_t ldx, uint8_t *Y, int64_t ldy, float *scale, int64_t lds,
+                            cudaStream_t stream);
 
 // dZ = act'(Z) * dD (dZ and Z may be null when act is none), dbias = column sums.
 cudaError_t launch_act_grad(const DeviceInfo &dev, bool bf16, int M, int N, int act,

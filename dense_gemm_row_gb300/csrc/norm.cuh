@@ -30,29 +30,15 @@
 #include <cstdint>
 #include <type_traits>
 
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "e4m3.cuh"
 #include "epi.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 
 namespace dgr {
 namespace {
-
-constexpr float kE4m3Max = 448.f;
-// A row whose largest |y| is below this counts as zeros (scale 0): 448 / |y|
-// must not overflow.
-constexpr float kE4m3Least = 1e-30f;
-
-// The scale of a row whose largest |y| is `most`, and its inverse; NaN and infinity
-// stay visible in both the scale and the values (0 * inf and NaN).
-__device__ __forceinline__ float e4m3_scale(float most) {
-  return most < kE4m3Least ? 0.f : most / kE4m3Max;
-}
-__device__ __forceinline__ float e4m3_inverse(float most) {
-  return most < kE4m3Least ? 0.f : kE4m3Max / most;
-}
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float r;
@@ -119,9 +105,6 @@ template <bool kBf16>
 __device__ __forceinline__ uint4 unit_pack(const float (&v)[8]) {
   return make_uint4(pack16<kBf16>(v[0], v[1]), pack16<kBf16>(v[2], v[3]),
                     pack16<kBf16>(v[4], v[5]), pack16<kBf16>(v[6], v[7]));
-}
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
 // The sum of a and the largest of m over the T threads of a row (a whole block

@@ -31,6 +31,9 @@ decltype(&gemm_rms_norm_grad_bf16) g_norm_grad[2];
 decltype(&gemm_layer_norm_bf16) g_layer_norm[2];
 decltype(&gemm_bf16_gated) g_gated[2];
 decltype(&gemm_bf16_gated_dact) g_gated_dact[2];
+decltype(&gemm_e4m3_bf16_gated) g_gated8[2];
+decltype(&gemm_e4m3_block_bf16_epi) g_block[2];
+decltype(&gemm_quantise_bf16_e4m3) g_quantise[2];
 decltype(&gemm_layer_norm_grad_bf16) g_layer_norm_grad[2];
 
 struct Refused {};  // a Python exception has been set
@@ -145,6 +148,14 @@ void *vector_or_none(PyObject *o, const char *name, int64_t n, at::ScalarType ty
   return t.data_ptr();
 }
 
+// Scales of a rows x cols matrix per block of block_rows x 128, a fp32 matrix.
+Matrix block_scales(PyObject *o, const char *name, int64_t rows, int64_t cols, int64_t block_rows,
+                    int dev) {
+  return matrix(tensor(o, name), name, (rows + block_rows - 1) / block_rows, (cols + 127) / 128,
+                at::kFloat, dev);
+}
+bool is_matrix(PyObject *o) { return THPVariable_Check(o) && THPVariable_Unpack(o).dim() == 2; }
+
 // 0 for bfloat16, 1 for float16.
 int format_of(const at::Tensor &t, const char *name) {
   if (t.scalar_type() == at::kBFloat16) return 0;
@@ -207,6 +218,16 @@ int epilogue(PyObject *const *v) {
   if (e4m3) {
     if (p.op_a == GEMM_OP_T || p.op_b != GEMM_OP_T)
       refuse(PyExc_ValueError, "%s", "float8_e4m3fn takes A as M x K and B as N x K (trans_b=True)");
+    if (is_matrix(v[10]) || is_matrix(v[11])) {  // a scale per block of 128
+      const Matrix sa = block_scales(v[10], "scale_a", p.m, p.k, 1, dev);
+      const Matrix sb = block_scales(v[11], "scale_b", p.n, p.k, 128, dev);
+      return unlocked([&] {
+        return g_block[f](p.m, p.n, p.k, alpha, as<uint8_t>(p.a.p), p.a.ld, as<float>(sa.p), sa.ld,
+                          as<uint8_t>(p.b.p), p.b.ld, as<float>(sb.p), sb.ld, act,
+                          as<uint16_t>(bias), as<uint16_t>(r.p), r.ld, as<uint16_t>(z.p), z.ld,
+                          as<uint16_t>(d.p), d.ld, s);
+      });
+    }
     void *sa = vector_or_none(v[10], "scale_a", p.m, at::kFloat, dev);
     void *sb = vector_or_none(v[11], "scale_b", p.n, at::kFloat, dev);
     return unlocked([&] {
@@ -323,15 +344,18 @@ int rms_norm_grad(PyObject *const *v) {
   });
 }
 
-// (A, Bg, Bu, D, act, alpha, bias_gate, bias_up, gate, up, trans_a, trans_b, stream)
+// (A, Bg, Bu, D, act, alpha, bias_gate, bias_up, gate, up, trans_a, trans_b, scale_a,
+// scale_gate, scale_up, stream)
 int gated(PyObject *const *v) {
   const at::Tensor &A = tensor(v[0], "A"), &Bg = tensor(v[1], "Bg"), &Bu = tensor(v[2], "Bu");
   const at::Tensor &D = tensor(v[3], "D");
   const int dev = device_of(A, "A");
-  const int f = format_of(A, "A");
-  const at::ScalarType type = A.scalar_type();
-  const Product p = product(A, Bg, v[10], v[11], dev, 8);
-  const Matrix b2 = matrix(Bu, "Bu", Bg.size(0), Bg.size(1), type, dev, 8);
+  const bool e4m3 = A.scalar_type() == at::kFloat8_e4m3fn;
+  const int f = e4m3 ? format_of(D, "D") : format_of(A, "A");
+  const at::ScalarType type = e4m3 ? D.scalar_type() : A.scalar_type();
+  const Product p = product(A, Bg, v[10], v[11], dev, e4m3 ? 16 : 8);
+  const Matrix b2 =
+      matrix(Bu, "Bu", Bg.size(0), Bg.size(1), A.scalar_type(), dev, e4m3 ? 16 : 8);
   const Matrix d = matrix(D, "D", p.m, p.n, type, dev);
   const Matrix g = matrix_or_none(v[8], "gate", p.m, p.n, type, dev);
   const Matrix u = matrix_or_none(v[9], "up", p.m, p.n, type, dev);
@@ -339,12 +363,49 @@ int gated(PyObject *const *v) {
   void *bias_u = vector_or_none(v[7], "bias_up", p.n, type, dev);
   const gemm_act_t act = act_of(v[4]);
   const float alpha = number(v[5]);
-  const cudaStream_t s = stream_of(v[12], dev);
+  const cudaStream_t s = stream_of(v[15], dev);
+  if (e4m3) {
+    if (p.op_a == GEMM_OP_T || p.op_b != GEMM_OP_T)
+      refuse(PyExc_ValueError, "%s",
+             "float8_e4m3fn takes A as M x K, Bg and Bu as N x K (trans_b=True)");
+    const Matrix sa = block_scales(v[12], "scale_a", p.m, p.k, 1, dev);
+    const Matrix sg = block_scales(v[13], "scale_gate", p.n, p.k, 128, dev);
+    const Matrix su = block_scales(v[14], "scale_up", p.n, p.k, 128, dev);
+    return unlocked([&] {
+      return g_gated8[f](p.m, p.n, p.k, alpha, as<uint8_t>(p.a.p), p.a.ld, as<float>(sa.p), sa.ld,
+                         as<uint8_t>(p.b.p), p.b.ld, as<float>(sg.p), sg.ld, as<uint8_t>(b2.p),
+                         b2.ld, as<float>(su.p), su.ld, act, as<uint16_t>(bias_g),
+                         as<uint16_t>(bias_u), as<uint16_t>(g.p), g.ld, as<uint16_t>(u.p), u.ld,
+                         as<uint16_t>(d.p), d.ld, s);
+    });
+  }
+  if (v[12] != Py_None || v[13] != Py_None || v[14] != Py_None)
+    refuse(PyExc_ValueError, "%s", "scales go with float8_e4m3fn operands");
   return unlocked([&] {
     return g_gated[f](p.op_a, p.op_b, p.m, p.n, p.k, alpha, as<uint16_t>(p.a.p), p.a.ld,
                       as<uint16_t>(p.b.p), p.b.ld, as<uint16_t>(b2.p), b2.ld, act,
                       as<uint16_t>(bias_g), as<uint16_t>(bias_u), as<uint16_t>(g.p), g.ld,
                       as<uint16_t>(u.p), u.ld, as<uint16_t>(d.p), d.ld, s);
+  });
+}
+
+// (X, Y, scale, rows, stream)
+int quantise_blocks(PyObject *const *v) {
+  const at::Tensor &X = tensor(v[0], "X"), &Y = tensor(v[1], "Y");
+  const int dev = device_of(X, "X");
+  const int f = format_of(X, "X");
+  if (X.dim() != 2) refuse(PyExc_ValueError, "%s must be 2-D", "X");
+  const int64_t m = X.size(0), n = X.size(1);
+  const long rows = PyLong_AsLong(v[3]);
+  if (rows == -1 && PyErr_Occurred()) throw Refused();
+  if (rows != 1 && rows != 128) refuse(PyExc_ValueError, "%s must be 1 or 128", "rows");
+  const Matrix x = matrix(X, "X", m, n, X.scalar_type(), dev);
+  const Matrix y = matrix(Y, "Y", m, n, at::kFloat8_e4m3fn, dev);
+  const Matrix scale = block_scales(v[2], "scale", m, n, rows, dev);
+  const cudaStream_t s = stream_of(v[4], dev);
+  return unlocked([&] {
+    return g_quantise[f](m, n, rows, as<uint16_t>(x.p), x.ld, as<uint8_t>(y.p), y.ld,
+                         as<float>(scale.p), scale.ld, s);
   });
 }
 
@@ -466,6 +527,12 @@ PyObject *bind(PyObject *, PyObject *args) {
       {"gemm_rms_norm_grad_f16", &g_norm_grad[1]},
       {"gemm_bf16_gated", &g_gated[0]},
       {"gemm_f16_gated", &g_gated[1]},
+      {"gemm_e4m3_bf16_gated", &g_gated8[0]},
+      {"gemm_e4m3_f16_gated", &g_gated8[1]},
+      {"gemm_e4m3_block_bf16_epi", &g_block[0]},
+      {"gemm_e4m3_block_f16_epi", &g_block[1]},
+      {"gemm_quantise_bf16_e4m3", &g_quantise[0]},
+      {"gemm_quantise_f16_e4m3", &g_quantise[1]},
       {"gemm_bf16_gated_dact", &g_gated_dact[0]},
       {"gemm_f16_gated_dact", &g_gated_dact[1]},
       {"gemm_layer_norm_bf16", &g_layer_norm[0]},
@@ -496,7 +563,8 @@ PyMethodDef g_methods[] = {
     method<act_grad, 6>("act_grad"),
     method<rms_norm, 9>("rms_norm"),
     method<rms_norm_grad, 8>("rms_norm_grad"),
-    method<gated, 13>("gemm_gated"),
+    method<gated, 16>("gemm_gated"),
+    method<quantise_blocks, 5>("quantise_blocks"),
     method<gated_dact, 13>("gemm_gated_dact"),
     method<layer_norm, 10>("layer_norm"),
     method<layer_norm_grad, 10>("layer_norm_grad"),

@@ -470,6 +470,9 @@ GEMM_API gemm_status_t gemm_rms_norm_grad_f16(int64_t rows, int64_t cols, const 
  * the fp32 values, not of the rounded ones. Layouts, K == 0 and the rest are
  * those of gemm_bf16_epi, with ldbg and ldbu under ldb's rules; G, U and D are
  * distinct.
+ *
+ * gemm_e4m3_bf16_gated, gemm_e4m3_f16_gated -- the same with 8-bit operands and
+ * a scale for each block of 128, as gemm_e4m3_block_bf16_epi takes them.
  */
 GEMM_API gemm_status_t gemm_bf16_gated(gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N,
                                        int64_t K, float alpha, const gemm_bf16_t *A, int64_t lda,
@@ -485,6 +488,19 @@ GEMM_API gemm_status_t gemm_f16_gated(gemm_op_t opA, gemm_op_t opB, int64_t M, i
                                       const gemm_f16_t *bias_u, gemm_f16_t *G, int64_t ldg,
                                       gemm_f16_t *U, int64_t ldu, gemm_f16_t *D, int64_t ldd,
                                       cudaStream_t stream);
+
+GEMM_API gemm_status_t gemm_e4m3_bf16_gated(
+    int64_t M, int64_t N, int64_t K, float alpha, const gemm_e4m3_t *A, int64_t lda,
+    const float *scale_a, int64_t ldsa, const gemm_e4m3_t *Bg, int64_t ldbg, const float *scale_g,
+    int64_t ldsg, const gemm_e4m3_t *Bu, int64_t ldbu, const float *scale_u, int64_t ldsu,
+    gemm_act_t act, const gemm_bf16_t *bias_g, const gemm_bf16_t *bias_u, gemm_bf16_t *G,
+    int64_t ldg, gemm_bf16_t *U, int64_t ldu, gemm_bf16_t *D, int64_t ldd, cudaStream_t stream);
+GEMM_API gemm_status_t gemm_e4m3_f16_gated(
+    int64_t M, int64_t N, int64_t K, float alpha, const gemm_e4m3_t *A, int64_t lda,
+    const float *scale_a, int64_t ldsa, const gemm_e4m3_t *Bg, int64_t ldbg, const float *scale_g,
+    int64_t ldsg, const gemm_e4m3_t *Bu, int64_t ldbu, const float *scale_u, int64_t ldsu,
+    gemm_act_t act, const gemm_f16_t *bias_g, const gemm_f16_t *bias_u, gemm_f16_t *G, int64_t ldg,
+    gemm_f16_t *U, int64_t ldu, gemm_f16_t *D, int64_t ldd, cudaStream_t stream);
 
 /*
  * gemm_bf16_gated_dact, gemm_f16_gated_dact -- the product that carries a
@@ -519,6 +535,52 @@ GEMM_API gemm_status_t gemm_f16_gated_dact(gemm_op_t opA, gemm_op_t opB, int64_t
                                            int64_t lddg, gemm_f16_t *dU, int64_t lddu,
                                            gemm_f16_t *dbias_g, gemm_f16_t *dbias_u,
                                            cudaStream_t stream);
+
+/*
+ * gemm_e4m3_block_bf16_epi, gemm_e4m3_block_f16_epi -- gemm_e4m3_*_epi with a
+ * scale for each block of 128 of the inner dimension: A (M x K, as stored) has
+ * one per row and 128 columns, B (N x K, stored transposed) one per 128 rows
+ * (columns of D) and 128 columns:
+ *
+ *     Z_ij = alpha * sum_b scale_a[i][b] * scale_b[j / 128][b]
+ *                  * sum_{128 b <= k < min(128 b + 128, K)} A_ik B_jk + bias_j
+ *     D = act(Z) + R
+ *
+ * scale_a: M rows of ceil(K / 128) fp32 values, row stride ldsa; scale_b:
+ * ceil(N / 128) such rows, row stride ldsb; neither may be NULL unless it is
+ * empty. Each block's sum is made by the tensor cores and added, scaled, in
+ * fp32 in the order of b. The rest is as gemm_e4m3_*_epi. Results are the
+ * same bits on every call.
+ *
+ * gemm_quantise_bf16_e4m3, gemm_quantise_f16_e4m3 -- a 16-bit matrix X (rows x
+ * cols) as such an operand, with blocks of block_rows x 128 (block_rows 1: A and
+ * scale_a, 128: B and scale_b):
+ *
+ *     scale = max |X| / 448 over the block,   Y8 = X / scale, rounded to nearest even
+ *
+ * X has any layout; Y8 any, but a product wants its rows in whole 16-byte units.
+ * scale: ceil(rows / block_rows) rows of ceil(cols / 128) values, row stride lds.
+ * As in the norm, a block whose largest magnitude is below 1e-30 gets scale 0
+ * and zeros, and one with a NaN or an infinity a NaN or infinite scale.
+ */
+GEMM_API gemm_status_t gemm_e4m3_block_bf16_epi(
+    int64_t M, int64_t N, int64_t K, float alpha, const gemm_e4m3_t *A, int64_t lda,
+    const float *scale_a, int64_t ldsa, const gemm_e4m3_t *B, int64_t ldb, const float *scale_b,
+    int64_t ldsb, gemm_act_t act, const gemm_bf16_t *bias, const gemm_bf16_t *R, int64_t ldr,
+    gemm_bf16_t *Z, int64_t ldz, gemm_bf16_t *D, int64_t ldd, cudaStream_t stream);
+GEMM_API gemm_status_t gemm_e4m3_block_f16_epi(
+    int64_t M, int64_t N, int64_t K, float alpha, const gemm_e4m3_t *A, int64_t lda,
+    const float *scale_a, int64_t ldsa, const gemm_e4m3_t *B, int64_t ldb, const float *scale_b,
+    int64_t ldsb, gemm_act_t act, const gemm_f16_t *bias, const gemm_f16_t *R, int64_t ldr,
+    gemm_f16_t *Z, int64_t ldz, gemm_f16_t *D, int64_t ldd, cudaStream_t stream);
+GEMM_API gemm_status_t gemm_quantise_bf16_e4m3(int64_t rows, int64_t cols, int64_t block_rows,
+                                               const gemm_bf16_t *X, int64_t ldx, gemm_e4m3_t *Y8,
+                                               int64_t ldy, float *scale, int64_t lds,
+                                               cudaStream_t stream);
+GEMM_API gemm_status_t gemm_quantise_f16_e4m3(int64_t rows, int64_t cols, int64_t block_rows,
+                                              const gemm_f16_t *X, int64_t ldx, gemm_e4m3_t *Y8,
+                                              int64_t ldy, float *scale, int64_t lds,
+                                              cudaStream_t stream);
 
 /*
  * gemm_layer_norm_bf16, gemm_layer_norm_f16 -- layer norm of each row, with the

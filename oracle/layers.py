@@ -147,6 +147,22 @@ def quantise_e4m3(y, least=1e-30):
     return np.where(scale[:, None] == 0.0, 0.0, q), scale
 
 
+def spread(scale, rows, shape):
+    """A scale per block of rows x 128 -> one per element of a matrix of `shape`."""
+    return np.repeat(np.repeat(scale, rows, 0)[:shape[0]], 128, 1)[:, :shape[1]]
+
+
+def quantise_blocks(x, rows, least=1e-30):
+    """(q, scale) with a scale per block of rows x 128 values."""
+    m, n = x.shape
+    scale = np.zeros((-(-m // rows), -(-n // 128)))
+    for i, j in np.ndindex(scale.shape):
+        scale[i, j] = np.abs(x[i * rows:(i + 1) * rows, j * 128:(j + 1) * 128]).max() / E4M3_MAX
+    scale[scale < least / E4M3_MAX] = 0
+    wide = spread(scale, rows, x.shape)
+    return np.where(wide == 0, 0.0, round_e4m3(x / np.where(wide == 0, 1.0, wide))), scale
+
+
 def decode_e4m3(bits) -> np.ndarray:
     """Values of e4m3 bytes: sign, 4 exponent bits (bias 7), 3 fraction bits;
     exponent 0 is subnormal, 0x7f / 0xff are NaN."""

@@ -19,6 +19,14 @@ FAMILIES = {
     "gemm_{}_gated_dact": dict(opA=0, opB=0, M=16, N=32, K=64, alpha=1.0, A=P, lda=64, B=P, ldb=32,
                                act=4, G=P, ldg=32, U=P, ldu=32, dG=P, lddg=32, dU=P, lddu=32,
                                dbias_g=P, dbias_u=P, s=None),
+    "gemm_e4m3_{}_gated": dict(M=16, N=32, K=256, alpha=1.0, A=P, lda=256, sa=P, ldsa=2, Bg=P,
+                               ldbg=256, sg=P, ldsg=2, Bu=P, ldbu=256, su=P, ldsu=2, act=4,
+                               bias_g=P, bias_u=P, G=P, ldg=32, U=P, ldu=32, D=P, ldd=32, s=None),
+    "gemm_e4m3_block_{}_epi": dict(M=16, N=32, K=256, alpha=1.0, A=P, lda=256, sa=P, ldsa=2, B=P,
+                                   ldb=256, sb=P, ldsb=2, act=4, bias=P, R=P, ldr=32, Z=P, ldz=32,
+                                   D=P, ldd=32, s=None),
+    "gemm_quantise_{}_e4m3": dict(M=16, N=256, rows=1, X=P, ldx=256, Y=P, ldy=256, scale=P, lds=2,
+                                  s=None),
 }
 PRODUCT = [dict(M=-1), dict(N=-1), dict(K=-1), dict(M=BIG), dict(N=BIG), dict(K=BIG),
            dict(A=None), dict(lda=56), dict(act=5), dict(act=-1)]
@@ -48,6 +56,24 @@ REFUSED = {
          + [{k: 31} for k in ("ldg", "ldu", "lddg", "lddu")]),
         (LAYOUT, [{k: P + 1} for k in ("G", "U", "dG", "dU", "dbias_g", "dbias_u")]
          + [dict(A=P + 8), dict(B=P + 8), dict(lda=68), dict(ldb=36)])],
+    "gemm_e4m3_{}_gated": [
+        (INVALID, PRODUCT + [{k: None} for k in ("Bg", "Bu", "D", "sa", "sg", "su")]
+         + [{k: 240} for k in ("ldbg", "ldbu")] + [{k: 1} for k in ("ldsa", "ldsg", "ldsu")]
+         + [{k: 31} for k in ("ldd", "ldg", "ldu")]),
+        (LAYOUT, [{k: P + 1} for k in ("bias_g", "bias_u", "G", "U", "D")]
+         + [{k: P + 8} for k in ("A", "Bg", "Bu")] + [{k: P + 2} for k in ("sa", "sg", "su")]
+         + [{k: 264} for k in ("lda", "ldbg", "ldbu")])],
+    "gemm_e4m3_block_{}_epi": [
+        (INVALID, PRODUCT + [{k: None} for k in ("B", "D", "sa", "sb")]
+         + [{k: 1} for k in ("ldsa", "ldsb")] + [{k: 31} for k in ("ldd", "ldz", "ldr")]
+         + [dict(ldb=240)]),
+        (LAYOUT, [{k: P + 1} for k in ("bias", "R", "Z", "D")] + [{k: P + 8} for k in "AB"]
+         + [{k: P + 2} for k in ("sa", "sb")] + [{k: 264} for k in ("lda", "ldb")])],
+    "gemm_quantise_{}_e4m3": [
+        (INVALID, [dict(M=-1), dict(N=-1), dict(M=BIG), dict(N=BIG), dict(rows=0), dict(rows=64),
+                   dict(X=None), dict(Y=None), dict(scale=None), dict(ldx=255), dict(ldy=255),
+                   dict(lds=1)]),
+        (LAYOUT, [dict(X=P + 1), dict(scale=P + 2)])],
 }
 # Empty problems: nothing is read, written or enqueued.
 EMPTY = {
@@ -57,6 +83,9 @@ EMPTY = {
     "gemm_{}_gated": [dict(M=0), dict(N=0), dict(M=0, A=None, D=None, G=None)],
     "gemm_{}_gated_dact": [dict(N=0), dict(M=0, dbias_g=None, dbias_u=None),
                            dict(M=0, dbias_g=None, dbias_u=None, G=None, dU=None)],
+    "gemm_e4m3_{}_gated": [dict(M=0), dict(N=0), dict(M=0, A=None, sa=None, D=None)],
+    "gemm_e4m3_block_{}_epi": [dict(M=0), dict(N=0), dict(N=0, B=None, sb=None)],
+    "gemm_quantise_{}_e4m3": [dict(M=0), dict(N=0), dict(M=0, X=None, Y=None, scale=None)],
 }
 
 
@@ -86,6 +115,7 @@ def test_cpu_tensors_are_refused(gemm_mod):
     x, s = torch.zeros(8, 16, dtype=torch.bfloat16), torch.zeros(8)
     for f in (lambda: gemm_mod.gemm_gated(x, x, x, x[:, :8], trans_b=True),
               lambda: gemm_mod.gemm_gated_dact(x, x, *[x[:, :8]] * 4, trans_b=True),
+              lambda: gemm_mod.quantise_blocks(x, x.to(torch.float8_e4m3fn), s.view(8, 1)),
               lambda: gemm_mod.layer_norm(x, x), lambda: gemm_mod.layer_norm_grad(x, x, s, s, x)):
         with pytest.raises(ValueError, match="CUDA"):
             f()

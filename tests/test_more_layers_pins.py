@@ -68,3 +68,22 @@ def test_gated_grad_matches_differences(name):
     dg, du, sg, su = L.gated_grad(E, G, U, name)
     differences(loss, [A, Bg, Bu, bg, bu], [dg @ Bg.T + du @ Bu.T, A.T @ dg, A.T @ du, sg, su],
                 atol=1e-5)
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quantise_blocks_is_the_row_form_of_each_block(rows):
+    x = np.random.default_rng(3).standard_normal((200, 300))
+    x[5, :128] = 0
+    q, s = L.quantise_blocks(x, rows)
+    assert s.shape == (-(-200 // rows), 3)
+    for i, j in ((0, 0), (1, 2), (-1, 1)):
+        i %= len(s)
+        at = (slice(i * rows, (i + 1) * rows), slice(128 * j, 128 * j + 128))
+        flat, scale = L.quantise_e4m3(x[at].reshape(1, -1))
+        np.testing.assert_array_equal(q[at].reshape(1, -1), flat)
+        assert s[i, j] == scale[0]
+    if rows == 1:
+        assert s[5, 0] == 0 and not q[5, :128].any()
+    wide = L.spread(s, rows, x.shape)
+    assert wide.shape == x.shape and wide[130, 290] == s[130 // rows, 2]
+    assert (np.abs(q * wide - x) <= 2.0 ** -4 * np.abs(x) + wide * 2.0 ** -10).all()
