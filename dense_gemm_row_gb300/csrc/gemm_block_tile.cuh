@@ -6,11 +6,17 @@
 //
 // A block of 128 is one 128-byte row of a stage, so the accumulator is restarted for
 // every stage (4 MMAs) and its 256 x kN sums are added, scaled, into fp32 registers:
-// 128 per thread at kN = 256. That addition is what a k-block costs beside its MMAs
-// (512 cycles at the e4m3 rate): 32 KB of tensor memory to read per warp scheduler and
-// 128 packed multiply-adds. The scales of a thread are one value per row and one per
+// 128 per thread at kN = 256. The scales of a thread are one value per row and one per
 // 128 columns, which a warp's columns never cross. The accumulators alternate, so that
 // the MMAs of the next k-block run meanwhile.
+//
+// What bounds it (8192^3: 385 us, 2.85 PFLOP/s; e4m3 with row scales 295): the
+// epilogue's chain of loads from tensor memory, each about 100 cycles, 8 per k-block
+// whose MMAs take 512. Without the multiply-adds 336 us, without all but one of the
+// loads 362, without either 309. Multiply-adds on packed pairs cost moves (441 us);
+// loads of 32 columns or of 8 were slower (419, 397), and so were accumulators of 128
+// columns, four under way, emptied by all eight warps (463) or by half of them (383,
+// but gated 245 against 225).
 //
 // Warps as in gemm_epi_tile.cuh, whose producer this kernel shares; the final epilogue
 // works on the registers. Each warp has two staging buffers: R of both of its blocks
@@ -68,7 +74,7 @@ __device__ __forceinline__ void block_multiply(const EpiArgs &p, BlockSmem<kN> &
   bool ok = true, any = false;
   for (int t = unit; ok && t < p.tiles; t += units) {
     for (int kb = 0; kb < KB; ++kb) {
-      if (!mbar_wait_lazy<true>(smem_u32(&sm.tmem_empty[buf]), use ^ 1u, abort, p.err_word,
+      if (!mbar_wait_lazy(smem_u32(&sm.tmem_empty[buf]), use ^ 1u, abort, p.err_word,
                                 kWaitTmemEmpty) ||
           !mbar_wait_lazy(smem_u32(&sm.full[stage]), phase, abort, p.err_word, kWaitFull)) {
         ok = false;
@@ -106,7 +112,15 @@ __device__ __forceinline__ void block_multiply(const EpiArgs &p, BlockSmem<kN> &
   }
 }
 
-// Adds s times 16 accumulator columns to sum[0 .. 7].
+// Gives an accumulator back to the MMAs. Relaxed: the loads from it are complete
+// (tcgen05.wait::ld), and nothing else is handed over. An arrive that releases waits
+// for the thread's other accesses too, 1 us per k-block: 8192^3 took 916 us with one
+// and 433 with this one.
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr)
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -118,24 +132,37 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
-// The final epilogue of a warp's 64 kBlocks columns: z = alpha sum + bias, and what
-// follows, block of 64 columns by block. bias: the tile's, from the warp's columns on.
+// The bias of a warp's columns, two values per lane and 64 columns (packed), and z =
+// alpha sum + bias: each pair comes from its lane.
+__device__ __forceinline__ uint32_t load_bias(const uint16_t *bias, int col, int N) {
+  if (bias == nullptr) return 0;
+  const uint32_t lo = col < N ? bias[col] : 0, hi = col + 1 < N ? bias[col + 1] : 0;
+  return lo | (hi << 16);
+}
+template <bool kBf16>
+__device__ __forceinline__ void add_bias(float (&sum)[64], float alpha, bool have,
+                                         uint32_t bias) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    float lo, hi;
+    unpack16<kBf16>(have ? __shfl_sync(0xffffffffu, bias, j) : 0, lo, hi);
+    sum[2 * j] = fmaf(sum[2 * j], alpha, lo);
+    sum[2 * j + 1] = fmaf(sum[2 * j + 1], alpha, hi);
+  }
+}
+
+// The final epilogue of a warp's 64 kCount columns, block of 64 columns by block.
 template <bool kBf16, int kCount>
 __device__ __forceinline__ void block_finish(const CUtensorMap &tmD, const CUtensorMap &tmZ,
-                                             const EpiArgs &p, const uint16_t *bias,
-                                             F2 (&sum)[32 * kCount],
+                                             const EpiArgs &p, const uint32_t (&bias)[2],
+                                             float (&sum)[kCount][64],
                                              const uint32_t (&stage)[2], int row0, int col0,
                                              bool early_r, uint32_t rbar, uint32_t &rphase,
                                              const CUtensorMap &tmR, int lane) {
   const bool have_r = p.c.R != nullptr;
 #pragma unroll
-  for (int j = 0; j < 32 * kCount; j += 4) {
-    const uint4 q = *reinterpret_cast<const uint4 *>(bias + 2 * j);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      sum[j + i] = fma2(sum[j + i], f2(p.c.alpha), unpack2<kBf16>(w[i]));
-  }
+  for (int c = 0; c < kCount; ++c)
+    add_bias<kBf16>(sum[c], p.c.alpha, p.c.bias != nullptr, bias[c]);
   if (have_r && early_r && p.r_tma) {
     wait_copy(rbar, rphase, p.err_word);
     rphase ^= 1u;
@@ -149,7 +176,7 @@ __device__ __forceinline__ void block_finish(const CUtensorMap &tmD, const CUten
       for (int h = 0; h < 2; ++h) {
         uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) w[j] = pack2<kBf16>(sum[32 * c + 16 * h + j]);
+        for (int j = 0; j < 16; ++j) w[j] = pack16<kBf16>(sum[c][32 * h + 2 * j], sum[c][32 * h + 2 * j + 1]);
         stage_half(stage[c], lane, h, w);
       }
       store_block(&tmZ, p.z_tma, p.c.Z, p.c.ldz, row0, col, p.M, p.N, stage[c], lane);
@@ -177,7 +204,7 @@ __device__ __forceinline__ void block_finish(const CUtensorMap &tmD, const CUten
       uint32_t r[16];
       F2 v[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = sum[32 * c + 16 * h + j];
+      for (int j = 0; j < 16; ++j) v[j] = f2(sum[c][32 * h + 2 * j], sum[c][32 * h + 2 * j + 1]);
       if (p.c.act != kActNone)
         with_act(p.c.act, [&](auto a) { act_values<decltype(a)::value>(v); });
       if (have_r) {
@@ -200,21 +227,11 @@ __device__ __forceinline__ void block_finish(const CUtensorMap &tmD, const CUten
 template <bool kBf16>
 __device__ __forceinline__ void block_finish_gated(const CUtensorMap &tmD, const CUtensorMap &tmG,
                                                    const CUtensorMap &tmU, const EpiArgs &p,
-                                                   const uint16_t *bias, F2 (&sum)[64],
+                                                   const uint32_t (&bias)[2], float (&sum)[2][64],
                                                    const uint32_t (&stage)[2], int row0, int col,
                                                    int lane) {
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const uint4 q = *reinterpret_cast<const uint4 *>(bias + 128 * which + 2 * j);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sum[32 * which + j + i] =
-            fma2(sum[32 * which + j + i], f2(p.c.alpha), unpack2<kBf16>(w[i]));
-    }
-  }
+  add_bias<kBf16>(sum[0], p.c.alpha, p.c.bias != nullptr, bias[0]);
+  add_bias<kBf16>(sum[1], p.c.alpha, p.c.bias2 != nullptr, bias[1]);
   stage_free(lane);
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
@@ -224,7 +241,8 @@ __device__ __forceinline__ void block_finish_gated(const CUtensorMap &tmD, const
     for (int h = 0; h < 2; ++h) {
       uint32_t w[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) w[j] = pack2<kBf16>(sum[32 * which + 16 * h + j]);
+      for (int j = 0; j < 16; ++j) 
+        w[j] = pack16<kBf16>(sum[which][32 * h + 2 * j], sum[which][32 * h + 2 * j + 1]);
       stage_half(stage[which], lane, h, w);
     }
     store_block(which ? &tmU : &tmG, which ? p.r_tma : p.z_tma, out, which ? p.c.ldz2 : p.c.ldz,
@@ -236,10 +254,11 @@ __device__ __forceinline__ void block_finish_gated(const CUtensorMap &tmD, const
     uint32_t w[16];
     F2 g[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) g[j] = sum[16 * h + j];
+    for (int j = 0; j < 16; ++j) g[j] = f2(sum[0][32 * h + 2 * j], sum[0][32 * h + 2 * j + 1]);
     with_act(p.c.act, [&](auto a) { act_values<decltype(a)::value>(g); });
 #pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = pack2<kBf16>(mul2(g[j], sum[32 + 16 * h + j]));
+    for (int j = 0; j < 16; ++j) 
+      w[j] = pack2<kBf16>(mul2(g[j], f2(sum[1][32 * h + 2 * j], sum[1][32 * h + 2 * j + 1])));
     stage_half(stage[0], lane, h, w);
   }
   store_block(&tmD, p.d_tma, p.c.D, p.c.ldd, row0, col, p.M, p.N, stage[0], lane);
@@ -311,8 +330,6 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
-    // Every epilogue warp walks the same tiles and meets the same named barriers;
-    // after a wait that gave up it skips the work, not the barriers.
     grid_dependency_wait();
     const int e = warp - kBlockFirst, quarter = warp & 3, half = e >> 2;
     const uint32_t stage[2] = {smem_u32(sm.stage[2 * e]), smem_u32(sm.stage[2 * e + 1])};
@@ -324,25 +341,40 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
     };
     const bool vec_a = whole(sc.a, sc.lda), vec_b = whole(sc.b, sc.ldb);
     const bool vec_b2 = kGated && whole(sc.b2, sc.ldb2);
+    // The warp's part of a tile: its place, the rows of its scales and the first of them.
+    struct Part {
+      int row0, col0;
+      const float *sa, *sb, *sb2;
+      float4 a, b, b2;
+    };
+    auto begin = [&](int t) {
+      Part w;
+      int tm = 0, tn = 0;
+      const bool is = t < p.tiles;
+      if (is) tile_coords<kEpiGroupM>(t, p.tiles_m, p.tiles_n, tm, tn);
+      w.row0 = tm * 256 + static_cast<int>(rank) * kBM + quarter * 32;
+      w.col0 = tn * kTileCols + half * (kTileCols / 2);
+      const int64_t row = w.row0 + lane, jb = w.col0 / 128;
+      w.sa = is && row < p.M ? sc.a + row * sc.lda : nullptr;
+      w.sb = is && w.col0 < p.N ? sc.b + jb * sc.ldb : nullptr;
+      w.sb2 = kGated && is && w.col0 < p.N ? sc.b2 + jb * sc.ldb2 : nullptr;
+      w.a = load_scales(w.sa, 0, sc.KB, vec_a);
+      w.b = load_scales(w.sb, 0, sc.KB, vec_b);
+      w.b2 = load_scales(w.sb2, 0, sc.KB, vec_b2);
+      return w;
+    };
     uint32_t rphase = 0, buf = 0, use = 0;
     bool ok = true;
+    Part next = begin(unit);
     for (int t = unit; t < p.tiles; t += units) {
-      int tm, tn;
-      tile_coords<kEpiGroupM>(t, p.tiles_m, p.tiles_n, tm, tn);
-      const int row0 = tm * 256 + static_cast<int>(rank) * kBM + quarter * 32;
-      const int local0 = half * (kTileCols / 2), col0 = tn * kTileCols + local0;
-      epilogue_sync();  // every warp has read the previous tile's bias
-      for (int i = threadIdx.x - 32 * kBlockFirst; i < kN; i += 32 * kEpiWarps) {
-        const uint16_t *bias = !kGated || i < kTileCols ? p.c.bias : p.c.bias2;
-        const int j = tn * kTileCols + (kGated ? i & (kTileCols - 1) : i);
-        sm.bias[i] = bias && j < p.N ? bias[j] : 0;
-      }
-      epilogue_sync();
       // (The warp reads the flag as one: its lanes must take the same branch.)
-      if (__any_sync(0xffffffffu, !ok || *static_cast<volatile int *>(&sm.abort))) {
-        ok = false;
-        continue;
-      }
+      if (__any_sync(0xffffffffu, !ok || *static_cast<volatile int *>(&sm.abort))) break;
+      const Part w = next;
+      float4 a4 = w.a, b4 = w.b, u4 = w.b2;
+      const uint32_t bias[2] = {
+          load_bias(p.c.bias, w.col0 + 2 * lane, p.N),
+          kGated ? load_bias(p.c.bias2, w.col0 + 2 * lane, p.N)
+                 : kCols > 64 ? load_bias(p.c.bias, w.col0 + 64 + 2 * lane, p.N) : 0u};
       if (early_r) {
         stage_free(lane);
         if (p.r_tma) {
@@ -355,39 +387,35 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
             mbar_arrive_expect_tx(rbar, kCols / 64 * kStageCBytes);
 #pragma unroll
             for (int c = 0; c < kCols / 64; ++c)
-              tma_load_3d(stage[c], &tmR, rbar, col0 + 64 * c, row0, 0);
+              tma_load_3d(stage[c], &tmR, rbar, w.col0 + 64 * c, w.row0, 0);
           }
         } else {
 #pragma unroll
           for (int c = 0; c < kCols / 64; ++c)
-            stage_block(p.c.R, p.c.ldr, row0, col0 + 64 * c, p.M, p.N, stage[c], lane);
+            stage_block(p.c.R, p.c.ldr, w.row0, w.col0 + 64 * c, p.M, p.N, stage[c], lane);
         }
       }
-      const int64_t row = row0 + lane, jb = col0 / 128;
-      const float *sa = row < p.M ? sc.a + row * sc.lda : nullptr;
-      const float *sb = col0 < p.N ? sc.b + jb * sc.ldb : nullptr;
-      const float *sb2 = kGated && col0 < p.N ? sc.b2 + jb * sc.ldb2 : nullptr;
-      float4 a4 = load_scales(sa, 0, sc.KB, vec_a), b4 = load_scales(sb, 0, sc.KB, vec_b);
-      float4 u4 = load_scales(sb2, 0, sc.KB, vec_b2);
-      F2 sum[kCols / 2];
+      float sum[kCols / 64][64];
 #pragma unroll
-      for (int j = 0; j < kCols / 2; ++j) sum[j] = f2(0.f);
+      for (int j = 0; j < kCols; ++j) sum[j / 64][j % 64] = 0.f;
       for (int kb0 = 0; ok && kb0 < sc.KB; kb0 += 4) {
-        const float4 an = load_scales(sa, kb0 + 4, sc.KB, vec_a);
-        const float4 bn = load_scales(sb, kb0 + 4, sc.KB, vec_b);
-        const float4 un = load_scales(sb2, kb0 + 4, sc.KB, vec_b2);
+        const float4 an = load_scales(w.sa, kb0 + 4, sc.KB, vec_a);
+        const float4 bn = load_scales(w.sb, kb0 + 4, sc.KB, vec_b);
+        const float4 un = load_scales(w.sb2, kb0 + 4, sc.KB, vec_b2);
         const int left = min(sc.KB - kb0, 4);
 #pragma unroll 1
         for (int i = 0; i < left; ++i) {
-          const F2 s = f2(pick(a4, i) * pick(b4, i));
-          const F2 s2 = kGated ? f2(pick(a4, i) * pick(u4, i)) : s;
-          if (!mbar_wait_lazy(smem_u32(&sm.tmem_full[buf]), use, &sm.abort, p.err_word,
-                              kWaitTmemFull)) {
+          const float s = pick(a4, i) * pick(b4, i);
+          const float s2 = kGated ? pick(a4, i) * pick(u4, i) : s;
+          const uint32_t full = smem_u32(&sm.tmem_full[buf]);
+          if (!__all_sync(0xffffffffu, mbar_try_wait(full, use)) &&
+              !mbar_wait_lazy(full, use, &sm.abort, p.err_word, kWaitTmemFull)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t taddr = tmem_base + lane_addr + buf * kN + local0;
+          const uint32_t taddr =
+              tmem_base + lane_addr + buf * kN + half * (kTileCols / 2);
           // The next 16 columns are on their way while these are added.
           uint32_t r[2][16];
           auto column = [&](int c) {  // gated: 64 of G's columns, then 64 of U's
@@ -402,13 +430,13 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
             } else {  // all in registers: the MMAs may have it
               tc_fence_before_sync();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.tmem_empty[buf]), 0));
+              if (lane == 0) arrive_relaxed(mapa_shared(smem_u32(&sm.tmem_empty[buf]), 0));
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              sum[8 * c + j] = fma2(f2(__uint_as_float(r[c & 1][2 * j]),
-                                       __uint_as_float(r[c & 1][2 * j + 1])),
-                                    kGated && c >= kChunks / 2 ? s2 : s, sum[8 * c + j]);
+            for (int j = 0; j < 16; ++j) {
+              float &to = sum[c / 4][16 * (c % 4) + j];
+              to = fmaf(__uint_as_float(r[c & 1][j]), kGated && c >= kChunks / 2 ? s2 : s, to);
+            }
           }
           if (++buf == kBufs) {
             buf = 0;
@@ -419,25 +447,22 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       }
       if (!ok) {
         // Never leave with a copy of R still writing into shared memory.
-        if (early_r && p.r_tma) {
-          wait_copy(rbar, rphase, p.err_word);
-          rphase ^= 1u;
-        }
-        continue;
+        if (early_r && p.r_tma) wait_copy(rbar, rphase, p.err_word);
+        break;
       }
-      const uint16_t *bias = sm.bias + local0;
+      next = begin(t + units);  // its first scales arrive during the final epilogue
       if constexpr (kGated) {
         if (p.c.bf16) {
-          block_finish_gated<true>(tmD, tmZ, tmR, p, bias, sum, stage, row0, col0, lane);
+          block_finish_gated<true>(tmD, tmZ, tmR, p, bias, sum, stage, w.row0, w.col0, lane);
         } else {
-          block_finish_gated<false>(tmD, tmZ, tmR, p, bias, sum, stage, row0, col0, lane);
+          block_finish_gated<false>(tmD, tmZ, tmR, p, bias, sum, stage, w.row0, w.col0, lane);
         }
       } else if (p.c.bf16) {
-        block_finish<true, kCols / 64>(tmD, tmZ, p, bias, sum, stage, row0, col0, early_r, rbar,
+        block_finish<true, kCols / 64>(tmD, tmZ, p, bias, sum, stage, w.row0, w.col0, early_r, rbar,
                                        rphase, tmR, lane);
       } else {
-        block_finish<false, kCols / 64>(tmD, tmZ, p, bias, sum, stage, row0, col0, early_r, rbar,
-                                        rphase, tmR, lane);
+        block_finish<false, kCols / 64>(tmD, tmZ, p, bias, sum, stage, w.row0, w.col0, early_r,
+                                        rbar, rphase, tmR, lane);
       }
     }
     // Never leave with a TMA store still reading the staging buffers (its writes
