@@ -190,7 +190,7 @@ gemm_status_t quantise(bool bf16, int64_t rows, int64_t cols, int64_t block_rows
   const DeviceInfo *dev = nullptr;
   gemm_status_t st = device(&dev);
   if (st != GEMM_OK) return st;
-  return status(launch_quantise(bf16, static_cast<int>(rows), static_cast<int>(cols),
+  return status(launch_quantise(*dev, bf16, static_cast<int>(rows), static_cast<int>(cols),
                                 static_cast<int>(block_rows), X, ldx, Y, ldy, scale, lds,
                                 stream));
 }

@@ -23,6 +23,7 @@
 // of 64 columns is requested before the main loop, and D takes its place.
 #pragma once
 
+#include "block_scales.cuh"
 #include "gemm_epi_tile.cuh"
 
 namespace dgr {
@@ -33,21 +34,6 @@ struct BlockScales {
   int64_t lda, ldb, ldb2;
   int KB;
 };
-
-// The scales of k-blocks kb .. kb + 3 of one row (zeros past the last).
-__device__ __forceinline__ float4 load_scales(const float *row, int kb, int KB, bool vec) {
-  if (row == nullptr) return make_float4(0.f, 0.f, 0.f, 0.f);
-  if (vec && kb + 4 <= KB) return __ldg(reinterpret_cast<const float4 *>(row + kb));
-  float4 v;
-  v.x = kb < KB ? __ldg(row + kb) : 0.f;
-  v.y = kb + 1 < KB ? __ldg(row + kb + 1) : 0.f;
-  v.z = kb + 2 < KB ? __ldg(row + kb + 2) : 0.f;
-  v.w = kb + 3 < KB ? __ldg(row + kb + 3) : 0.f;
-  return v;
-}
-__device__ __forceinline__ float pick(const float4 &v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
 
 // Three warpgroups: producer, MMAs and two idle warps; the epilogue's eight. They are
 // launched with 168 registers a thread, of which the first group keeps 40 and the
@@ -119,17 +105,6 @@ __device__ __forceinline__ void block_multiply(const EpiArgs &p, BlockSmem<kN> &
 __device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr)
                : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
 }
 
 // The bias of a warp's columns, two values per lane and 64 columns (packed), and z =
@@ -336,11 +311,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
     const uint32_t rbar = smem_u32(&sm.arrived[e]);
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const bool have_r = !kGated && p.c.R != nullptr, early_r = have_r && p.c.Z == nullptr;
-    auto whole = [](const float *q, int64_t ld) {
-      return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % 4 == 0;
-    };
-    const bool vec_a = whole(sc.a, sc.lda), vec_b = whole(sc.b, sc.ldb);
-    const bool vec_b2 = kGated && whole(sc.b2, sc.ldb2);
+    const bool vec_a = scales_whole(sc.a, sc.lda), vec_b = scales_whole(sc.b, sc.ldb);
+    const bool vec_b2 = kGated && scales_whole(sc.b2, sc.ldb2);
     // The warp's part of a tile: its place, the rows of its scales and the first of them.
     struct Part {
       int row0, col0;

@@ -133,14 +133,31 @@ cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t
                             const EpiCall &epi, cudaStream_t stream) {
   if (K == 0) return launch_empty(M, N, epi, stream);
   const bool ragged = N % 8 != 0 || epi.ldd % 8 != 0 || reinterpret_cast<uintptr_t>(epi.D) % 16 != 0;
+  if (epi.block) {
+    // Block scales: the few-rows kernel has token tiles of up to 64 rows, and takes up
+    // to 64 always, more where its tiles fill at most half of the SMs (tiles of 256 rows
+    // against it, us: 128 x 1024 x 4096 12.6, 8.8; 512 x 1024 x 4096 12.7, 10.7; 100 x
+    // 4096 x 4096 12.7, 10.5; but 256 x 4096 x 4096 13.0, 15.7). Short k makes no
+    // difference (256 x 1024 x 1024 7.1, 7.2).
+    const int64_t cols = epi.gated ? 64 : 128;
+    const int64_t split = (N + cols - 1) / cols * ((static_cast<int64_t>(M) + 63) / 64);
+    if (M <= 64 || 2 * split <= dev.sm_count)
+      return launch_block_split(dev, M <= 16 ? 16 : M <= 32 ? 32 : 64, M, N, K, A, lda, B, ldb,
+                                epi, stream);
+    if (epi.gated) return launch_block_gated(dev, M, N, K, A, lda, B, ldb, epi, stream);
+    // 128-wide tiles take 0.62 of the 256-wide ones' time (512 x 16384 x 1024 17.6, 15.1
+    // in as many waves as tiles; 2048 x 8192 x 8192 123, 111): where the waves are as many.
+    const int64_t pairs = std::max(dev.sm_count / 2, 1);
+    const int64_t rows = (static_cast<int64_t>(M) + 255) / 256;
+    const int64_t w256 = (rows * ((static_cast<int64_t>(N) + 255) / 256) + pairs - 1) / pairs;
+    const int64_t w128 = (rows * ((static_cast<int64_t>(N) + 127) / 128) + pairs - 1) / pairs;
+    return launch_block_fwd(dev, 62 * w128 < 100 * w256 ? 128 : 256, M, N, K, A, lda, B, ldb, epi,
+                            stream);
+  }
   // A gated layer is a product of twice the columns, in 256-wide tiles only.
   const EpiPlan plan = plan_epi(dev, a_t, M, N, (K - 1) / (e4m3 ? 128 : 64) + 1, ragged,
                                 epi.gated && !epi.grad);
   const int mp = plan.split_rows, tile_n = plan.tile_n;
-  if (epi.block)
-    return mp          ? launch_block_split(dev, mp, M, N, K, A, lda, B, ldb, epi, stream)
-           : epi.gated ? launch_block_gated(dev, M, N, K, A, lda, B, ldb, epi, stream)
-                       : launch_block_fwd(dev, tile_n, M, N, K, A, lda, B, ldb, epi, stream);
   if (epi.gated && !epi.grad)
     return mp ? launch_gated_split_fwd(dev, mp, b_t, M, N, K, A, lda, B, ldb, epi, nullptr, stream)
               : launch_gated_fwd(dev, a_t, b_t, M, N, K, A, lda, B, ldb, epi, stream);

@@ -19,13 +19,13 @@
 // Block-scaled e4m3 (kBlock; what is computed: gemm_block_tile.cuh): every k-block has
 // an accumulator of its own, of up to eight in turn, and the four warps that drain
 // tensor memory add each one, scaled, into registers. A warp's rows are the weights',
-// with one scale per k-block, its columns the tokens, whose scales it puts in shared
-// memory a k-block ahead.
+// with one scale per k-block, its columns the tokens, whose scales are in shared memory.
 //
 // A gated layer's tile has 64 columns of D: the MMA's rows are those of the first
 // B, then the same ones of the second, and a finishing thread adds both.
 #pragma once
 
+#include "block_scales.cuh"
 #include "epi.cuh"
 #include "gemm_tc_kernel.cuh"
 #include "tc_issue.cuh"
@@ -39,17 +39,6 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
       : "memory");
 }
 
@@ -78,13 +67,13 @@ struct SplitCfg {
 
 // Accumulators of the block-scaled form: half of tensor memory, two CTAs share an SM.
 template <int kMP>
-constexpr int kSplitBufs = kMP <= 32 ? 8 : 256 / kMP;
+constexpr int kSplitBufs = kMP <= 32 ? 8 : 4;
 
 template <int kMP, bool kBlock>
 struct SplitBlock {};
 template <int kMP>
 struct SplitBlock<kMP, true> {
-  alignas(16) float scale[4][2][kMP];  // a draining warp's, of two k-blocks
+  alignas(16) float scale[2][4][kMP];  // the tokens', of two times four k-blocks
   uint64_t acc_full[kSplitBufs<kMP>];
   uint64_t acc_empty[kSplitBufs<kMP>];
 };
@@ -114,6 +103,7 @@ struct SplitArgs {
   bool b_t;     // B stored N x K
   bool r_vec, d_vec, z_vec;  // rows of R / D / Z in whole 8-byte units
   bool r2_vec, d2_vec, z2_vec;
+  bool sa_vec, sb_vec;       // rows of block scales in whole 16-byte units
   uint32_t idesc;
   uint32_t *err_word;
   float *part;  // gradient, several token tiles: column sums of each [tiles_m][N]
@@ -299,67 +289,81 @@ __device__ __forceinline__ void gated_finish(const SplitArgs &p, uint32_t red, i
 }
 
 // The block-scaled sums of k-blocks kb0 .. kb1 - 1 by one of the four warps that drain
-// tensor memory: 32 rows of the transposed product, token j in sum[j / 2]. Returns
-// whether every accumulator arrived.
+// tensor memory: 32 rows of the transposed product, token j in sum[j]. Returns whether
+// every accumulator arrived.
+//
+// The tokens' scales come four k-blocks at a time: thread t of the four warps loads
+// token t's, while the four before are in use, and puts them in shared memory. (Loaded
+// one k-block ahead, each by every warp, their latency was the k-block's time: 24 x
+// 16384 x 4096 gated 25.6 us.) A warp whose wait gave up goes on meeting the barriers.
 template <int kMP, bool kPair>
 __device__ __forceinline__ bool split_blocks(const SplitArgs &p, SplitSmem<kMP, true> &sm,
-                                             uint32_t tmem_base, int quarter, int lane, int m0,
-                                             int n0, int kb0, int kb1, F2 (&sum)[kMP / 2]) {
-  constexpr int kBufs = kSplitBufs<kMP>, kOwn = (kMP + 31) / 32;  // tokens per lane
+                                             uint32_t tmem_base, int t, int quarter, int m0,
+                                             int n0, int kb0, int kb1, float (&sum)[kMP]) {
+  constexpr int kBufs = kSplitBufs<kMP>;
   const bool second = kPair && quarter >= 2;
   const float *sb = second ? p.c.block_b2 + n0 / 128 * p.c.ldsb2
                            : p.c.block_b + n0 / 128 * p.c.ldsb;
-  const float *sa = p.c.block_a + static_cast<int64_t>(m0 + lane) * p.c.ldsa;
-  auto load = [&](int kb, float (&s)[kOwn]) {
-    const float b = kb < kb1 ? __ldg(sb + kb) : 0.f;
+  const float *sa = t < kMP && m0 + t < p.M
+                        ? p.c.block_a + static_cast<int64_t>(m0 + t) * p.c.ldsa
+                        : nullptr;
+  float4 a = load_scales(sa, kb0, kb1, p.sa_vec && kb0 % 4 == 0);
+  float4 b = load_scales(sb, kb0, kb1, p.sb_vec && kb0 % 4 == 0);
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i)
-      s[i] = kb < kb1 && lane + 32 * i < kMP && m0 + lane + 32 * i < p.M
-                 ? __ldg(sa + 32 * i * p.c.ldsa + kb) * b
-                 : 0.f;
-  };
-#pragma unroll
-  for (int j = 0; j < kMP / 2; ++j) sum[j] = f2(0.f);
-  float next[kOwn];
-  load(kb0, next);
+  for (int j = 0; j < kMP; ++j) sum[j] = 0.f;
   uint32_t buf = 0, use = 0;
-  for (int kb = kb0; kb < kb1; ++kb) {
-    float *slot = sm.block.scale[quarter][(kb - kb0) & 1];
+  bool ok = true;
+  for (int kb = kb0; kb < kb1; kb += 4) {
+    float(*slot)[kMP] = sm.block.scale[(kb - kb0) / 4 & 1];
+    if (t < kMP) slot[0][t] = a.x, slot[1][t] = a.y, slot[2][t] = a.z, slot[3][t] = a.w;
+    // Every warp is here: the slots are filled, and those of the k-blocks before the
+    // last four no longer read.
+    asm volatile("bar.sync 1, %0;" ::"n"(kSplitFinish) : "memory");
+    const float4 b4 = b;
+    a = load_scales(sa, kb + 4, kb1, p.sa_vec && kb0 % 4 == 0);
+    b = load_scales(sb, kb + 4, kb1, p.sb_vec && kb0 % 4 == 0);
+    const int left = min(kb1 - kb, 4);
+#pragma unroll 1
+    for (int i = 0; ok && i < left; ++i) {
+      if (!mbar_wait_lazy(smem_u32(&sm.block.acc_full[buf]), use, &sm.abort, p.err_word,
+                          kWaitTmemFull)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const float w = pick(b4, i);
+      const uint32_t taddr =
+          tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kMP;
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i)
-      if (lane + 32 * i < kMP) slot[lane + 32 * i] = next[i];
-    load(kb + 1, next);
-    __syncwarp();
-    if (!mbar_wait_lazy(smem_u32(&sm.block.acc_full[buf]), use, &sm.abort, p.err_word, kWaitTmemFull))
-      return false;
-    tc_fence_after_sync();
-    const uint32_t taddr =
-        tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kMP;
+      for (int c = 0; c < kMP; c += 16) {
+        if (c < p.mp) {
+          uint32_t r[16];
+          tmem_ld_x16(taddr + c, r);
+          tmem_ld_wait();
 #pragma unroll
-    for (int c = 0; c < kMP; c += 16) {
-      if (c < p.mp) {
-        uint32_t r[16];
-        tmem_ld_x16(taddr + c, r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 s = *reinterpret_cast<const float4 *>(slot + c + j);
-          sum[(c + j) / 2] = fma2(f2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
-                                  f2(s.x, s.y), sum[(c + j) / 2]);
-          sum[(c + j) / 2 + 1] = fma2(f2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
-                                      f2(s.z, s.w), sum[(c + j) / 2 + 1]);
+          for (int j = 0; j < 16; j += 4) {
+            const float4 s = *reinterpret_cast<const float4 *>(&slot[i][c + j]);
+            sum[c + j] = fmaf(__uint_as_float(r[j]), s.x * w, sum[c + j]);
+            sum[c + j + 1] = fmaf(__uint_as_float(r[j + 1]), s.y * w, sum[c + j + 1]);
+            sum[c + j + 2] = fmaf(__uint_as_float(r[j + 2]), s.z * w, sum[c + j + 2]);
+            sum[c + j + 3] = fmaf(__uint_as_float(r[j + 3]), s.w * w, sum[c + j + 3]);
+          }
         }
       }
-    }
-    tc_fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm.block.acc_empty[buf]));
-    if (++buf == kBufs) {
-      buf = 0;
-      use ^= 1u;
+      // (Relaxed: the loads are complete, and nothing else is handed over.)
+      tc_fence_before_sync();
+      __syncwarp();
+      if ((t & 31) == 0)
+        asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];\n" ::"r"(
+                         smem_u32(&sm.block.acc_empty[buf]))
+                     : "memory");
+      if (++buf == kBufs) {
+        buf = 0;
+        use ^= 1u;
+      }
     }
   }
-  return true;
+  return ok;
 }
 
 // tmS: a gated layer's second B.
@@ -547,10 +551,10 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
       split_load_cols<kGrad>(p, col, cols);
       split_load_row<kGrad>(p, m0 + t / wq, col, first);
     }
-    F2 blocks[kBlock ? kMP / 2 : 1];
+    float blocks[kBlock ? kMP : 1];
     int got = 0;
     if constexpr (kBlock) {
-      got = split_blocks<kMP, kPair>(p, sm, tmem_base, quarter, lane, m0, n0, kb0, kb1, blocks);
+      got = split_blocks<kMP, kPair>(p, sm, tmem_base, t, quarter, m0, n0, kb0, kb1, blocks);
     } else {
       if (lane == 0)
         got = mbar_wait_bounded(smem_u32(&sm.done), 0, abort, p.err_word, kWaitTmemFull);
@@ -569,11 +573,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
         uint32_t r[16];
         if constexpr (kBlock) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            float lo, hi;
-            split(blocks[(c + j) / 2], lo, hi);
-            r[j] = __float_as_uint(lo), r[j + 1] = __float_as_uint(hi);
-          }
+          for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(blocks[c + j]);
         } else {
           tmem_ld_x16(taddr + c, r);
           tmem_ld_wait();
@@ -722,6 +722,9 @@ cudaError_t launch_split_form(const DeviceInfo &dev, bool b_t, int M, int N, int
   p.r_vec = vec(epi.R, epi.ldr), p.d_vec = vec(epi.D, epi.ldd), p.z_vec = vec(epi.Z, epi.ldz);
   p.r2_vec = vec(epi.R2, epi.ldr2), p.d2_vec = vec(epi.D2, epi.ldd2);
   p.z2_vec = vec(epi.Z2, epi.ldz2);
+  p.sa_vec = scales_whole(epi.block_a, epi.ldsa);
+  p.sb_vec = scales_whole(epi.block_b, epi.ldsb) &&
+             (!kPair || scales_whole(epi.block_b2, epi.ldsb2));
   p.idesc = idesc_mma(kE4m3 || !epi.bf16 ? 0u : kFmtBF16, !b_t, false, kSplitN, p.mp);
   p.err_word = dev.err_word;
   p.part = part;
@@ -778,7 +781,9 @@ cudaError_t launch_split(const DeviceInfo &dev, int mp, bool b_t, int M, int N, 
     case 16: return launch_split_form<kE4m3, 16, kGrad, kGated, kBlock>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
     case 32: return launch_split_form<kE4m3, 32, kGrad, kGated, kBlock>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
     case 64: return launch_split_form<kE4m3, 64, kGrad, kGated, kBlock>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
-    default: return launch_split_form<kE4m3, 128, kGrad, kGated, kBlock>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
+    default:
+      if constexpr (kBlock) return cudaErrorInvalidValue;  // up to 64 rows
+      else return launch_split_form<kE4m3, 128, kGrad, kGated, kBlock>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
   }
 }
 

@@ -242,9 +242,9 @@ cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t
 
 // e4m3 values and a scale per block of block_rows (1 or 128) x 128 of a 16-bit matrix
 // (quantise.cu).
-cudaError_t launch_quantise(bool bf16, int rows, int cols, int block_rows, const uint16_t *X,
-                            int64_t ldx, uint8_t *Y, int64_t ldy, float *scale, int64_t lds,
-                            cudaStream_t stream);
+cudaError_t launch_quantise(const DeviceInfo &dev, bool bf16, int rows, int cols, int block_rows,
+                            const uint16_t *X, int64_t ldx, uint8_t *Y, int64_t ldy, float *scale,
+                            int64_t lds, cudaStream_t stream);
 
 // dZ = act'(Z) * dD (dZ and Z may be null when act is none), dbias = column sums.
 cudaError_t launch_act_grad(const DeviceInfo &dev, bool bf16, int M, int N, int act,

@@ -7,10 +7,11 @@
 // memory: 2 bytes in, 1 out, each value held in registers between the two.
 //
 // A row's block of 128 belongs to 16 threads with 8 values each: one 16-byte load, one
-// 8-byte store. Rows that are not in whole 16-byte units (or 8-byte units of Y) go
-// value by value, 8 consecutive ones per thread, so that a line is fetched once.
+// 8-byte store. Where a row does not start on a 16-byte boundary a thread loads the
+// aligned 16 bytes that its first value is in and takes the rest from its neighbour.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -32,19 +33,46 @@ struct QuantArgs {
   int64_t ldy;
   float *scale;
   int64_t lds;
-  bool x_vec, y_vec;  // rows in whole 16-byte units / 8-byte units
+  bool y_vec;  // Y's rows in whole 8-byte units
 };
 
-// 8 values from column `col` of a row, packed; zeros past the last column.
-__device__ __forceinline__ uint4 load8(const QuantArgs &q, int64_t row, int col) {
-  const uint16_t *p = q.X + row * q.ldx + col;
-  const int n = q.cols - col;
-  if (q.x_vec && n >= 8) return __ldcs(reinterpret_cast<const uint4 *>(p));
+// The 8 values from column `col` on (which may be negative), packed, by one load if all
+// are inside the row and p is aligned; the others zeros.
+__device__ __forceinline__ uint4 load_at(const uint16_t *p, int col, int cols, bool vec) {
+  p += col;
+  if (vec && col >= 0 && col + 8 <= cols) return __ldcs(reinterpret_cast<const uint4 *>(p));
   uint32_t h[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) h[e] = e < n ? p[e] : 0;
+  for (int e = 0; e < 8; ++e) h[e] = col + e >= 0 && col + e < cols ? p[e] : 0;
   return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
                     h[6] | (h[7] << 16));
+}
+// A lane's 8 values of a block, from column `col`; the whole warp. live: there is a row.
+// kAligned: rows in whole 16-byte units.
+template <bool kAligned>
+__device__ __forceinline__ uint4 load8(const QuantArgs &q, int64_t row, int col, int lane,
+                                       bool live) {
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint16_t *p = q.X + row * q.ldx;
+  if constexpr (kAligned) return live ? load_at(p, col, q.cols, true) : zero;
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 7;
+  const uint4 a = live ? load_at(p, col - off, q.cols, true) : zero;
+  uint4 b = lane == kLanes - 1 && live && off ? load_at(p, col - off + 8, q.cols, true) : zero;
+  uint4 n;
+  n.x = __shfl_down_sync(0xffffffffu, a.x, 1, kLanes);
+  n.y = __shfl_down_sync(0xffffffffu, a.y, 1, kLanes);
+  n.z = __shfl_down_sync(0xffffffffu, a.z, 1, kLanes);
+  n.w = __shfl_down_sync(0xffffffffu, a.w, 1, kLanes);
+  if (lane < kLanes - 1) b = n;
+  // Values off .. off + 7 of the two units, in three steps.
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = off & 4 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = off & 2 ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = off & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // The largest magnitude of 8 packed values, as bits: those of |x| order like |x|, NaN last.
 __device__ __forceinline__ uint32_t top8(const uint4 &v) {
@@ -78,108 +106,117 @@ __device__ __forceinline__ void store8(const QuantArgs &q, int64_t row, int col,
   }
 }
 
-// Blocks of 1 x 128: a group of 16 threads takes kAhead of them together.
-constexpr int kRowThreads = 256, kAhead = 4;
-
-template <bool kBf16>
-__global__ void __launch_bounds__(kRowThreads) quantise_rows_kernel(const QuantArgs q) {
+// A block of threads takes 128 columns of kThreads / 16 * kRows rows, kRows per thread;
+// kTile: those 128 rows are one block. (Rows walked along, a group of 16 threads on
+// four blocks of 1 x 128 in turn, took 41.8 us for 8192 x 8192.)
+template <bool kBf16, bool kAligned, bool kTile, int kThreads, int kRows>
+__global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs q) {
+  constexpr int kStep = kThreads / kLanes;
+  static_assert(!kTile || kStep * kRows == kBlock, "a block's rows");
+  static_assert(kTile || kRows <= kLanes, "a lane per row");
+  __shared__ uint32_t tops[kThreads / 32];
   const int lane = threadIdx.x & (kLanes - 1);
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t total = static_cast<int64_t>(q.rows) * q.col_blocks;
-  const int64_t first =
-      (blockIdx.x * static_cast<int64_t>(kRowThreads / kLanes)) * kAhead + threadIdx.x / kLanes;
-  uint4 v[kAhead];
-  int64_t row[kAhead];
-  int cb[kAhead];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    const int64_t at = first + i * (kRowThreads / kLanes);
-    row[i] = at / q.col_blocks;
-    cb[i] = static_cast<int>(at - row[i] * q.col_blocks);
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (at < total) v[i] = load8(q, row[i], cb[i] * kBlock + 8 * lane);
-  }
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    uint32_t top = top8(v[i]);
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1)
-      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (first + i * (kRowThreads / kLanes) >= total) continue;
-    const float most = top_value<kBf16>(top);
-    if (lane == 0) q.scale[row[i] * q.lds + cb[i]] = e4m3_scale(most);
-    store8<kBf16>(q, row[i], cb[i] * kBlock + 8 * lane, v[i], e4m3_inverse(most));
-  }
-}
-
-// Blocks of 128 x 128: one block of threads each, 8 rows per thread.
-constexpr int kTileThreads = 256, kTileRows = kBlock / (kTileThreads / kLanes);
-
-template <bool kBf16>
-__global__ void __launch_bounds__(kTileThreads) quantise_tiles_kernel(const QuantArgs q) {
-  __shared__ uint32_t tops[kTileThreads / 32];
-  const int lane = threadIdx.x & (kLanes - 1);
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int rb = static_cast<int>(blockIdx.x / q.col_blocks);
+  const int rb = static_cast<int>(blockIdx.x / static_cast<uint32_t>(q.col_blocks));
   const int cb = static_cast<int>(blockIdx.x) - rb * q.col_blocks;
-  const int64_t row0 = static_cast<int64_t>(rb) * kBlock + threadIdx.x / kLanes;
+  const int64_t row0 = static_cast<int64_t>(rb) * (kStep * kRows) + threadIdx.x / kLanes;
   const int col = cb * kBlock + 8 * lane;
-  uint4 v[kTileRows];
+  uint4 v[kRows];
 #pragma unroll
-  for (int i = 0; i < kTileRows; ++i) {
-    const int64_t row = row0 + i * (kTileThreads / kLanes);
-    v[i] = row < q.rows ? load8(q, row, col) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t row = row0 + i * kStep;
+    v[i] = load8<kAligned>(q, row, col, lane, row < q.rows);
   }
-  uint32_t top = 0;
+  float most = 0.f;
+  if constexpr (kTile) {
+    uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < kTileRows; ++i) top = __vmaxu2(top, top8(v[i]));
-  top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
-  __syncthreads();
+    for (int i = 0; i < kRows; ++i) top = __vmaxu2(top, top8(v[i]));
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kTileThreads / 32; ++i) top = max(top, tops[i]);
-  const float most = from16<kBf16>(top);
-  if (threadIdx.x == 0) q.scale[rb * q.lds + cb] = e4m3_scale(most);
-  const float inv = e4m3_inverse(most);
+    for (int i = 0; i < kThreads / 32; ++i) top = max(top, tops[i]);
+    most = from16<kBf16>(top);
+    if (threadIdx.x == 0) q.scale[rb * q.lds + cb] = e4m3_scale(most);
+  }
+  float inv = 0.f;
+  if constexpr (kTile) {
+    inv = e4m3_inverse(most);
+  } else {
+    // The lanes of a row exchange halves of their rows' maxima until two lanes are left
+    // with one row, whose divisions they make: 2 per thread instead of 2 per row.
+    uint32_t top[kRows];
 #pragma unroll
-  for (int i = 0; i < kTileRows; ++i) {
-    const int64_t row = row0 + i * (kTileThreads / kLanes);
-    if (row < q.rows) store8<kBf16>(q, row, col, v[i], inv);
+    for (int i = 0; i < kRows; ++i) top[i] = top8(v[i]);
+#pragma unroll
+    for (int n = kRows / 2, o = kLanes / 2; o > 0; o >>= 1, n /= 2) {
+      const bool up = (lane & o) != 0;
+      if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          const uint32_t give = up ? top[i] : top[i + n], keep = up ? top[i + n] : top[i];
+          top[i] = __vmaxu2(keep, __shfl_xor_sync(0xffffffffu, give, o));
+        }
+      } else {
+        top[0] = __vmaxu2(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
+      }
+    }
+    constexpr int kSame = kLanes / kRows;  // lanes left with one row
+    most = top_value<kBf16>(top[0]);
+    inv = e4m3_inverse(most);
+    const int64_t row = row0 + lane / kSame * kStep;
+    if (lane % kSame == 0 && row < q.rows) q.scale[row * q.lds + cb] = e4m3_scale(most);
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t row = row0 + i * kStep;
+    const float by = kTile ? inv : __shfl_sync(0xffffffffu, inv, i * (kLanes / kRows), kLanes);
+    if (row < q.rows) store8<kBf16>(q, row, col, v[i], by);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_quantise(bool bf16, int rows, int cols, int block_rows, const uint16_t *X,
-                            int64_t ldx, uint8_t *Y, int64_t ldy, float *scale, int64_t lds,
-                            cudaStream_t stream) {
+cudaError_t launch_quantise(const DeviceInfo &dev, bool bf16, int rows, int cols, int block_rows,
+                            const uint16_t *X, int64_t ldx, uint8_t *Y, int64_t ldy, float *scale,
+                            int64_t lds, cudaStream_t stream) {
   QuantArgs q;
   q.rows = rows, q.cols = cols;
   q.col_blocks = (cols - 1) / kBlock + 1;
   q.X = X, q.ldx = ldx;
   q.Y = Y, q.ldy = ldy;
   q.scale = scale, q.lds = lds;
-  q.x_vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0;
+  const bool x_vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0;
   q.y_vec = reinterpret_cast<uintptr_t>(Y) % 8 == 0 && ldy % 8 == 0;
-  const bool one = block_rows == 1;
-  const int64_t per_block = one ? kRowThreads / kLanes * kAhead : 1;
-  const int64_t blocks =
-      (static_cast<int64_t>(one ? rows : (rows - 1) / kBlock + 1) * q.col_blocks + per_block - 1) /
-      per_block;
+  // Few blocks of threads: fewer rows per thread, or more threads per block of values.
+  const bool tile = block_rows == kBlock;
+  const int64_t tiles = (static_cast<int64_t>(rows - 1) / kBlock + 1) * q.col_blocks;
+  const bool few = tiles < 4LL * dev.sm_count;
+  const int64_t blocks = few && !tile ? (static_cast<int64_t>(rows - 1) / 16 + 1) * q.col_blocks
+                                      : tiles;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-  cfg.blockDim = dim3(one ? kRowThreads : kTileThreads, 1, 1);
+  cfg.blockDim = dim3(few && tile ? 1024 : 256, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kern = one ? (bf16 ? quantise_rows_kernel<true> : quantise_rows_kernel<false>)
-                  : (bf16 ? quantise_tiles_kernel<true> : quantise_tiles_kernel<false>);
+  auto pick = [&](auto bf, auto al) {
+    constexpr bool kBf16 = decltype(bf)::value, kAligned = decltype(al)::value;
+    return tile ? (few ? quantise_kernel<kBf16, kAligned, true, 1024, 2>
+                       : quantise_kernel<kBf16, kAligned, true, 256, 8>)
+                : (few ? quantise_kernel<kBf16, kAligned, false, 256, 1>
+                       : quantise_kernel<kBf16, kAligned, false, 256, 8>);
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  auto kern = bf16 ? (x_vec ? pick(yes, yes) : pick(yes, no))
+                   : (x_vec ? pick(no, yes) : pick(no, no));
   return cudaLaunchKernelEx(&cfg, kern, q);
 }
 
