@@ -782,7 +782,7 @@ cudaError_t launch_split(const DeviceInfo &dev, int mp, bool b_t, int M, int N, 
     case 32: return launch_split_form<kE4m3, 32, kGrad, kGated, kBlock>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
     case 64: return launch_split_form<kE4m3, 64, kGrad, kGated, kBlock>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
     default:
-      if constexpr (kBlock) return cudaErrorInvalidValue;  // up to 64 rows
+      if constexpr (kGated || kBlock) return cudaErrorInvalidValue;  // up to 64 rows
       else return launch_split_form<kE4m3, 128, kGrad, kGated, kBlock>(dev, b_t, M, N, K, A, lda, B, ldb, epi, part, stream);
   }
 }
