@@ -124,50 +124,83 @@ EpiPlan plan_epi(const DeviceInfo &dev, bool a_t, int M, int64_t N, int KB, bool
   return plan;
 }
 
-// The gated layer and its gradient: the cheapest of 256-row tiles and token tiles of 32
-// and 64 rows, by times fitted to 270 problems of 40 to 1500 rows, N 512 to 8192, K 512
-// to 4096 (us; a wave of tiles takes a part per k-block and one for its epilogue; the
-// choice is 2.3 % and 0.6 % slower than the best one on average, where the other
-// products' rule is 19 % and 14 %; 128-row token tiles hardly ever win). For instance
-// 300 x 1000 x 520, gradient: tiles 10.1, 32 rows 8.2; 128 x 4096 x 4096: tiles 22.9,
-// 64 rows 14.5; 1000 x 2048 x 512: tiles 8.7, 64 rows 14.9.
+// Times of the kernels (us), fitted to measurements: a start, and for each wave of tiles
+// a part per k-block and one for its epilogue.
 struct WaveCost {
   double start, per_kb, per_wave;
   double of(int64_t waves, int64_t kb) const {
     return start + static_cast<double>(waves) * (static_cast<double>(kb) * per_kb + per_wave);
   }
 };
-// Waves and k-blocks per CTA of the few-rows kernel, whose launcher cuts k likewise.
+// Waves and k-blocks per CTA of the few-rows kernel, whose launcher cuts k likewise. (76
+// clusters of 4 CTAs take two waves on 152 SMs that have two CTAs each: clusters leave a
+// few places free.)
 double split_cost(const DeviceInfo &dev, int64_t tiles, int KB, const WaveCost &cost) {
   const int64_t slots = 2LL * dev.sm_count;
   int cl = 1;
   while (cl < 8 && tiles * cl * 2 <= slots && cl * 2 <= KB) cl *= 2;
-  return cost.of((tiles * cl + slots - 1) / slots, (KB + cl - 1) / cl);
+  const int64_t places = cl > 1 ? slots - slots / 16 : slots;
+  return cost.of((tiles * cl + places - 1) / places, (KB + cl - 1) / cl);
 }
+double tile_cost(const DeviceInfo &dev, int M, int N, int width, int KB, const WaveCost &cost) {
+  const int64_t pairs = std::max(dev.sm_count / 2, 1);
+  const int64_t tiles = (static_cast<int64_t>(M) + 255) / 256 *
+                        ((static_cast<int64_t>(N) + width - 1) / width);
+  return cost.of((tiles + pairs - 1) / pairs, KB);
+}
+// The cheapest of 256-row tiles (`best`: their time) and token tiles of the few-rows
+// kernel of 16, 32 and 64 rows; cols: columns of D of one of its tiles.
+int plan_split(const DeviceInfo &dev, int M, int N, int cols, int KB, double best,
+               const WaveCost (&cost)[3]) {
+  const int64_t blocks = (static_cast<int64_t>(N) + cols - 1) / cols;
+  int rows = 0;
+  for (int i = 0; i < 3; ++i) {
+    const int64_t tiles = blocks * ((static_cast<int64_t>(M) + (16 << i) - 1) / (16 << i));
+    const double t = split_cost(dev, tiles, KB, cost[i]);
+    if (t < best) best = t, rows = 16 << i;
+    if (M <= (16 << i)) break;
+  }
+  return rows;
+}
+
+// The gated layer and its gradient. Over 270 problems of 40 to 1500 rows, N 512 to 8192,
+// K 512 to 4096 the choice is 2.2 % and 1.3 % slower than the best kernel on average, where
+// the other products' rule is 19 % and 14 %; 128-row token tiles hardly ever win. For
+// instance 300 x 1000 x 520, gradient: tiles 10.1, 32 rows 8.2; 128 x 4096 x 4096: tiles
+// 22.9, 64 rows 14.5; 1000 x 2048 x 512: tiles 8.7, 64 rows 14.9.
 EpiPlan plan_gated(const DeviceInfo &dev, bool a_t, bool grad, int M, int N, int KB, bool ragged) {
-  EpiPlan plan = plan_epi(dev, true, M, grad ? N : 2 * static_cast<int64_t>(N), KB, ragged);
+  static constexpr WaveCost kForward[3] = {{1.5, 0.17, 3.0}, {1.5, 0.192, 3.4}, {1.4, 0.245, 4.6}};
+  static constexpr WaveCost kGradient[3] = {{0, 0.18, 4.4}, {0, 0.2, 5.4}, {0, 0.273, 7.3}};
+  static constexpr WaveCost kTile = {4.5, 0.266, 1.3};
+  static constexpr WaveCost kWide = {3.3, 0.278, 6.4}, kNarrow = {3.3, 0.137, 3.0};
+  EpiPlan plan{0, 256};
+  if (grad) plan.tile_n = plan_epi(dev, true, M, N, KB, ragged).tile_n;
   if (a_t) return plan;  // the few-rows kernel's token tiles are K-major
-  if (M <= 32) {
-    plan.split_rows = M <= 16 ? 16 : 32;
-    return plan;
+  const bool wide = plan.tile_n == 256;
+  const double tiles = grad ? tile_cost(dev, M, N, plan.tile_n, KB, wide ? kWide : kNarrow)
+                            : tile_cost(dev, M, N, 128, KB, kTile);
+  plan.split_rows = plan_split(dev, M, N, grad ? 128 : 64, KB, tiles, grad ? kGradient : kForward);
+  return plan;
+}
+
+// The block-scaled e4m3 product, plain and gated: 200 problems each of 16 to 1500 rows, N
+// 512 to 16384, K 512 to 16384, 2 % slower than the best on average. For instance 100 x
+// 4096 x 4096: 256-row tiles 12.6 us, token tiles of 64 rows 10.4, of 32 10.7, of 16 12.5;
+// 100 x 512 x 4096: 12.3, 7.3, 6.2, 5.4; 1024 x 4096 x 1024: tiles of 256 columns 9.5, of
+// 128 11.0.
+EpiPlan plan_block(const DeviceInfo &dev, bool gated, int M, int N, int KB) {
+  static constexpr WaveCost kPlain[3] = {{0.8, 0.26, 3.3}, {0, 0.353, 4.5}, {-2.7, 0.564, 7.5}};
+  static constexpr WaveCost kGated[3] = {{1.1, 0.257, 2.8}, {1.0, 0.349, 3.4}, {-0.1, 0.569, 5.0}};
+  EpiPlan plan{0, 256};
+  double best;
+  if (gated) {
+    best = tile_cost(dev, M, N, 128, KB, {3.2, 0.389, 3.2});
+  } else {
+    best = tile_cost(dev, M, N, 256, KB, {3.5, 0.388, 2.5});
+    const double narrow = tile_cost(dev, M, N, 128, KB, {3.5, 0.238, 1.4});
+    if (narrow < best) best = narrow, plan.tile_n = 128;
   }
-  static constexpr WaveCost kForward[3] = {{1.5, 0.192, 3.4}, {1.4, 0.245, 4.6}, {4.5, 0.266, 1.3}};
-  static constexpr WaveCost kGradient[3] = {{0, 0.2, 5.4}, {0, 0.273, 7.3}, {3.3, 0.278, 6.4}};
-  static constexpr WaveCost kNarrow = {3.3, 0.137, 3.0};  // gradient, 128-wide tiles
-  const WaveCost *cost = grad ? kGradient : kForward;
-  const int64_t pairs = std::max(dev.sm_count / 2, 1), width = grad ? plan.tile_n : 128;
-  const int64_t cols = (static_cast<int64_t>(N) + width - 1) / width;
-  const int64_t tiles = (static_cast<int64_t>(M) + 255) / 256 * cols;
-  double best =
-      (grad && width == 128 ? kNarrow : cost[2]).of((tiles + pairs - 1) / pairs, KB);
-  const int64_t blocks = (static_cast<int64_t>(N) + (grad ? 127 : 63)) / (grad ? 128 : 64);
-  for (int i = 0; i < 2; ++i) {
-    const int mp = 32 << i;
-    const int64_t tokens = (static_cast<int64_t>(M) + mp - 1) / mp;
-    if (blocks * tokens > 4096) continue;
-    const double t = split_cost(dev, blocks * tokens, KB, cost[i]);
-    if (t < best) best = t, plan.split_rows = mp;
-  }
+  plan.split_rows = plan_split(dev, M, N, gated ? 64 : 128, KB, best, gated ? kGated : kPlain);
   return plan;
 }
 
@@ -179,25 +212,11 @@ cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t
   if (K == 0) return launch_empty(M, N, epi, stream);
   const bool ragged = N % 8 != 0 || epi.ldd % 8 != 0 || reinterpret_cast<uintptr_t>(epi.D) % 16 != 0;
   if (epi.block) {
-    // Block scales: the few-rows kernel has token tiles of up to 64 rows, and takes up
-    // to 64 always, more where its tiles fill at most half of the SMs (tiles of 256 rows
-    // against it, us: 128 x 1024 x 4096 12.6, 8.8; 512 x 1024 x 4096 12.7, 10.7; 100 x
-    // 4096 x 4096 12.7, 10.5; but 256 x 4096 x 4096 13.0, 15.7). Short k makes no
-    // difference (256 x 1024 x 1024 7.1, 7.2).
-    const int64_t cols = epi.gated ? 64 : 128;
-    const int64_t split = (N + cols - 1) / cols * ((static_cast<int64_t>(M) + 63) / 64);
-    if (M <= 64 || 2 * split <= dev.sm_count)
-      return launch_block_split(dev, M <= 16 ? 16 : M <= 32 ? 32 : 64, M, N, K, A, lda, B, ldb,
-                                epi, stream);
-    if (epi.gated) return launch_block_gated(dev, M, N, K, A, lda, B, ldb, epi, stream);
-    // 128-wide tiles take 0.62 of the 256-wide ones' time (512 x 16384 x 1024 17.6, 15.1
-    // in as many waves as tiles; 2048 x 8192 x 8192 123, 111): where the waves are as many.
-    const int64_t pairs = std::max(dev.sm_count / 2, 1);
-    const int64_t rows = (static_cast<int64_t>(M) + 255) / 256;
-    const int64_t w256 = (rows * ((static_cast<int64_t>(N) + 255) / 256) + pairs - 1) / pairs;
-    const int64_t w128 = (rows * ((static_cast<int64_t>(N) + 127) / 128) + pairs - 1) / pairs;
-    return launch_block_fwd(dev, 62 * w128 < 100 * w256 ? 128 : 256, M, N, K, A, lda, B, ldb, epi,
-                            stream);
+    const EpiPlan plan = plan_block(dev, epi.gated, M, N, (K - 1) / 128 + 1);
+    if (plan.split_rows)
+      return launch_block_split(dev, plan.split_rows, M, N, K, A, lda, B, ldb, epi, stream);
+    return epi.gated ? launch_block_gated(dev, M, N, K, A, lda, B, ldb, epi, stream)
+                     : launch_block_fwd(dev, plan.tile_n, M, N, K, A, lda, B, ldb, epi, stream);
   }
   const int KB = (K - 1) / (e4m3 ? 128 : 64) + 1;
   const EpiPlan plan = epi.gated ? plan_gated(dev, a_t, epi.grad, M, N, KB, ragged)

@@ -334,19 +334,26 @@ __device__ __forceinline__ bool split_blocks(const SplitArgs &p, SplitSmem<kMP, 
       const float w = pick(b4, i);
       const uint32_t taddr =
           tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kMP;
+      // Up to 32 columns at once (those beyond the tile's tokens mean nothing and stay
+      // unused); 64 in four steps, which end with the tokens (0.56 us per k-block against
+      // 0.72 at once).
+      constexpr int kAt = kMP <= 32 ? kMP : 16;
 #pragma unroll
-      for (int c = 0; c < kMP; c += 16) {
-        if (c < p.mp) {
-          uint32_t r[16];
-          tmem_ld_x16(taddr + c, r);
+      for (int c0 = 0; c0 < kMP; c0 += kAt) {
+        if (c0 < p.mp) {
+          uint32_t r[kAt / 16][16];
+#pragma unroll
+          for (int c = 0; c < kAt / 16; ++c) tmem_ld_x16(taddr + c0 + 16 * c, r[c]);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 s = *reinterpret_cast<const float4 *>(&slot[i][c + j]);
-            sum[c + j] = fmaf(__uint_as_float(r[j]), s.x * w, sum[c + j]);
-            sum[c + j + 1] = fmaf(__uint_as_float(r[j + 1]), s.y * w, sum[c + j + 1]);
-            sum[c + j + 2] = fmaf(__uint_as_float(r[j + 2]), s.z * w, sum[c + j + 2]);
-            sum[c + j + 3] = fmaf(__uint_as_float(r[j + 3]), s.w * w, sum[c + j + 3]);
+          for (int c = 0; c < kAt; c += 4) {
+            const float4 s = *reinterpret_cast<const float4 *>(&slot[i][c0 + c]);
+            const uint32_t *now = &r[c / 16][c % 16];
+            float *to = &sum[c0 + c];
+            to[0] = fmaf(__uint_as_float(now[0]), s.x * w, to[0]);
+            to[1] = fmaf(__uint_as_float(now[1]), s.y * w, to[1]);
+            to[2] = fmaf(__uint_as_float(now[2]), s.z * w, to[2]);
+            to[3] = fmaf(__uint_as_float(now[3]), s.w * w, to[3]);
           }
         }
       }

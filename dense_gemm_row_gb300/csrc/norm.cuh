@@ -1066,14 +1066,16 @@ __global__ void __launch_bounds__(T, (NV > 2 ? 512 : 1024) / T)
 // row per block. Memory bounds it: 32768 x 1024 with dh 47.5 us, 5.7 TB/s.
 template <int NV>
 constexpr int kGradRowStages = NV == 8 ? 2 : 8 / NV;
-template <int NV>
-constexpr int kGradRowWarps = NV == 8 ? 8 : 16;  // at most: 192 KB of rows per SM
+// At most: 192 KB of rows per SM. (The layer norm keeps two sums per value: 8 warps
+// where 16 would spill.)
+template <bool kLayer, int NV>
+constexpr int kGradRowWarps = NV == 8 || (kLayer && NV == 4) ? 8 : 16;
 
 // Where column j of a warp's sums is kept: lanes 8 columns apart hit all banks.
 __device__ __forceinline__ int sums_at(int j) { return j + (j >> 5); }
 
 template <bool kLayer, bool kBf16, int NV>
-__global__ void __launch_bounds__(32 * kGradRowWarps<NV>, 1)
+__global__ void __launch_bounds__(32 * kGradRowWarps<kLayer, NV>, 1)
     norm_grad_rows_kernel(const NormGradCall c, float *part) {
   constexpr int kStages = kGradRowStages<NV>;
   constexpr uint32_t kSlab = NV * 512;  // one matrix's row
@@ -1153,42 +1155,51 @@ __global__ void __launch_bounds__(32 * kGradRowWarps<NV>, 1)
     if (++stage == kStages) stage = 0;
   }
   if (part == nullptr) return;
+  __syncthreads();  // the ring is free
+  constexpr int kSets = kLayer ? 2 : 1;
   const int pitch = sums_at(c.cols) + 1;
   float *all = reinterpret_cast<float *>(ring), *own = all + warp * pitch;
+  const int apart = warps * pitch;  // db's sums behind dw's
 #pragma unroll
-  for (int which = 0; which < (kLayer ? 2 : 1); ++which) {
-    __syncthreads();  // the ring is free
+  for (int which = 0; which < kSets; ++which) {
+    float *to = own + which * apart;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (i * 32 + t >= k.units) continue;
       const int j = k.head + 8 * (i * 32 + t);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        split(sums.pair(which, i, q), own[sums_at(j + 2 * q)], own[sums_at(j + 2 * q + 1)]);
+        split(sums.pair(which, i, q), to[sums_at(j + 2 * q)], to[sums_at(j + 2 * q + 1)]);
     }
-    if (k.extra >= 0) own[sums_at(k.extra)] = sums.last(which);
-    __syncthreads();
-    // Eight loads in flight per thread; the adds are in warp order.
-    const int stride = 32 * warps;
-    for (int j = threadIdx.x; j < c.cols; j += 2 * stride) {
-      const bool two = j + stride < c.cols;
-      const int at0 = sums_at(j), at1 = sums_at(two ? j + stride : j);
-      float v0 = 0.f, v1 = 0.f;
-      for (int w = 0; w < warps; w += 4) {
-        float a[4], b[4];
+    if (k.extra >= 0) to[sums_at(k.extra)] = sums.last(which);
+  }
+  __syncthreads();
+  // Eight loads in flight per thread; the adds are in warp order.
+  const int stride = 32 * warps;
+  for (int j = threadIdx.x; j < kSets * c.cols; j += 2 * stride) {
+    const bool two = j + stride < kSets * c.cols;
+    auto place = [&](int n) {  // column n, or of db
+      return kLayer && n >= c.cols ? apart + sums_at(n - c.cols) : sums_at(n);
+    };
+    const int at0 = place(j), at1 = place(two ? j + stride : j);
+    float v0 = 0.f, v1 = 0.f;
+    for (int w = 0; w < warps; w += 4) {
+      float a[4], b[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float *from = all + min(w + i, warps - 1) * pitch;
-          a[i] = from[at0], b[i] = from[at1];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (w + i < warps) v0 += a[i], v1 += b[i];
+      for (int i = 0; i < 4; ++i) {
+        const float *from = all + min(w + i, warps - 1) * pitch;
+        a[i] = from[at0], b[i] = from[at1];
       }
-      float *out = part + (which * static_cast<int64_t>(gridDim.x) + blockIdx.x) * c.cols + j;
-      out[0] = v0;
-      if (two) out[stride] = v1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (w + i < warps) v0 += a[i], v1 += b[i];
     }
+    auto out = [&](int n) {
+      const int64_t row = kLayer && n >= c.cols ? gridDim.x + blockIdx.x : blockIdx.x;
+      return part + row * c.cols + (kLayer && n >= c.cols ? n - c.cols : n);
+    };
+    *out(j) = v0;
+    if (two) *out(j + stride) = v1;
   }
 }
 
@@ -1391,14 +1402,14 @@ cudaError_t launch_grad_rows(const DeviceInfo &dev, const NormGradCall &c, cudaS
   // As few rows per warp as kGradRowWarps warps per SM allow, then as few warps as
   // that takes. A warp's rows are a multiple of 8 apart, or it has one row.
   const int sms = std::max(dev.sm_count / 8 * 8, 8);
-  const int per_warp = (c.rows - 1) / (sms * kGradRowWarps<NV>) + 1;
+  const int per_warp = (c.rows - 1) / (sms * kGradRowWarps<kLayer, NV>) + 1;
   int warps = (c.rows - 1) / (sms * per_warp) + 1;
   // One row each: at least 8 warps a block, for fewer partial rows and more threads
   // to add them (333 x 1001 7.0 -> 6.4 us).
   if (per_warp == 1) warps = std::max(warps, 8);
   const int64_t blocks = per_warp > 1 ? sms : (c.rows - 1) / warps + 1;
   const int smem = std::max(warps * kGradRowStages<NV> * 3 * NV * 512,
-                            warps * (c.cols + c.cols / 32 + 1) * 4);
+                            (kLayer ? 2 : 1) * warps * (c.cols + c.cols / 32 + 1) * 4);
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem, dev.device);
   if (e != cudaSuccess) return e;
   return with_partials<kLayer>(dev, c, blocks, stream, [&](float *part) {
