@@ -1450,7 +1450,9 @@ cudaError_t launch_grad(const DeviceInfo &dev, const NormGradCall &c, cudaStream
   if (units <= 128 && c.rows > 2 * dev.sm_count) return launch_grad_rows<kLayer, kBf16, 4>(dev, c, stream);
   if (units <= 128) return launch_grad_ring<kLayer, kBf16, 128, 1>(dev, c, stream);
   if (units <= 256 && c.rows > 10 * dev.sm_count) return launch_grad_rows<kLayer, kBf16, 8>(dev, c, stream);
-  if (units <= 256) return launch_grad_ring<kLayer, kBf16, 128>(dev, c, stream);
+  // (Layer: 4 units per thread, 1300 x 2048 12.4 -> 11.2 us; 2 spill.)
+  if (units <= 256)
+    return launch_grad_ring<kLayer, kBf16, kLayer ? 64 : 128, kLayer ? 4 : 2>(dev, c, stream);
   if (units <= 512) return launch_grad_ring<kLayer, kBf16, 128, 4>(dev, c, stream);
   if (units <= 1024) return launch_grad_ring<kLayer, kBf16, 256, 4>(dev, c, stream);
   if (units <= 2048) return launch_grad_ring<kLayer, kBf16, 512, 4>(dev, c, stream);

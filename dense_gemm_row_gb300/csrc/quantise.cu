@@ -195,7 +195,9 @@ cudaError_t launch_quantise(const DeviceInfo &dev, bool bf16, int rows, int cols
   q.scale = scale, q.lds = lds;
   const bool x_vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0;
   q.y_vec = reinterpret_cast<uintptr_t>(Y) % 8 == 0 && ldy % 8 == 0;
-  // Few blocks of threads: fewer rows per thread, or more threads per block of values.
+  // Few blocks of threads: fewer rows per thread, or more threads per block of values
+  // (1001 x 4096 in blocks of 128 rows: 3.9 us with 256 threads, 3.6 with 512, 4.2 with
+  // 1024; 1001 x 4095, whose ends take longer: 7.5, 7.3, 6.7).
   const bool tile = block_rows == kBlock;
   const int64_t tiles = (static_cast<int64_t>(rows - 1) / kBlock + 1) * q.col_blocks;
   const bool few = tiles < 4LL * dev.sm_count;
@@ -204,7 +206,7 @@ cudaError_t launch_quantise(const DeviceInfo &dev, bool bf16, int rows, int cols
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-  cfg.blockDim = dim3(few && tile ? 1024 : 256, 1, 1);
+  cfg.blockDim = dim3(!few || !tile ? 256 : x_vec ? 512 : 1024, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -213,7 +215,8 @@ cudaError_t launch_quantise(const DeviceInfo &dev, bool bf16, int rows, int cols
   cfg.numAttrs = 1;
   auto pick = [&](auto bf, auto al) {
     constexpr bool kBf16 = decltype(bf)::value, kAligned = decltype(al)::value;
-    return tile ? (few ? quantise_kernel<kBf16, kAligned, true, 1024, 2>
+    return tile ? (few ? quantise_kernel<kBf16, kAligned, true, kAligned ? 512 : 1024,
+                                         kAligned ? 4 : 2>
                        : quantise_kernel<kBf16, kAligned, true, 256, 8>)
                 : (few ? quantise_kernel<kBf16, kAligned, false, 256, 1>
                        : quantise_kernel<kBf16, kAligned, false, 256, 8>);
