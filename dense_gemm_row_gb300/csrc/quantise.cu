@@ -42,10 +42,12 @@ struct QuantArgs {
 // are inside the row and p is aligned; the others zeros.
 __device__ __forceinline__ uint4 load_at(const uint16_t *p, int col, int cols, bool vec) {
   p += col;
-  if (vec && col >= 0 && col + 8 <= cols) return __ldcs(reinterpret_cast<const uint4 *>(p));
+  // (Columns up to 2^31 - 1: no sum that could pass it.)
+  if (vec && col >= 0 && cols - col >= 8) return __ldcs(reinterpret_cast<const uint4 *>(p));
   uint32_t h[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) h[e] = col + e >= 0 && col + e < cols ? p[e] : 0;
+  for (int e = 0; e < 8; ++e)
+    h[e] = static_cast<uint32_t>(col) + e < static_cast<uint32_t>(cols) ? p[e] : 0;
   return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
                     h[6] | (h[7] << 16));
 }

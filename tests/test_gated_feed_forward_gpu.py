@@ -116,3 +116,44 @@ def test_command_prints_a_line(gemm_mod, capsys):
     main(["--tokens", "128", "--model", "256", "--hidden", "512", "--gated", "--act", "silu"])
     line = capsys.readouterr().out
     assert '"step_tflops"' in line and '"gated": true' in line
+
+
+def test_every_operator_on_a_stream_of_the_caller(gemm_mod):
+    """stream=: the work runs there, behind what that stream holds and unordered with the
+    current one; the bits of calls on the current stream."""
+    g, bf = gemm_mod, torch.bfloat16
+    x, w = (torch.randn(300, 256, device="cuda").to(bf) for _ in range(2))
+    side = torch.cuda.Stream()
+
+    def run(x, stream=None):
+        new = lambda *shape, dtype=bf: torch.empty(*shape, dtype=dtype, device="cuda")  # noqa: E731
+        f32, e4 = torch.float32, torch.float8_e4m3fn
+        y, mean, rstd = new(300, 256), new(300, dtype=f32), new(300, dtype=f32)
+        D, G, U, dG, dU = (new(300, 300) for _ in range(5))
+        dX, dw, db, sg, su = new(300, 256), new(256), new(256), new(300), new(300)
+        y8, w8, sy, sw = new(300, 256, dtype=e4), new(300, 256, dtype=e4), new(300, 2, dtype=f32), \
+            new(3, 2, dtype=f32)
+        D8, Z8 = new(300, 300), new(300, 300)
+        g.layer_norm(x, y, mean=mean, rstd=rstd, stream=stream)
+        g.gemm_gated(y, w, w, D, gate=G, up=U, trans_b=True, stream=stream)
+        g.gemm_gated_dact(x, w, G, U, dG, dU, dbias_gate=sg, dbias_up=su, trans_b=True,
+                          stream=stream)
+        g.layer_norm_grad(y, x, mean, rstd, dX, dweight=dw, dbias=db, stream=stream)
+        g.quantise_blocks(y, y8, sy, stream=stream)
+        g.quantise_blocks(w, w8, sw, rows=128, stream=stream)
+        g.gemm_gated(y8, w8, w8, D8, trans_b=True, scale_a=sy, scale_gate=sw, scale_up=sw,
+                     stream=stream)
+        g.gemm_epilogue(y8, w8, Z8, trans_b=True, scale_a=sy, scale_b=sw, stream=stream)
+        return [y, mean, rstd, D, G, U, dG, dU, sg, su, dX, dw, db, sy, sw, D8, Z8,
+                y8.view(torch.uint8), w8.view(torch.uint8)]
+
+    want = run(x)
+    late = torch.zeros_like(x)  # holds x only once the side stream gets there
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(x)
+    got = run(late, side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert g.check_device_error() == 0
