@@ -7,6 +7,7 @@
 // slot order. Latency is what it costs (a few hundred partial rows at most), so
 // a thread's loads are issued together.
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -19,13 +20,20 @@ namespace {
 
 constexpr int kSlots = 32;
 
-template <bool kBf16>
+// A second sum of the same shape: its partial rows and its result.
+struct Second {
+  int64_t apart;
+  uint16_t *out;
+};
+struct NoSecond {};
+
+template <bool kBf16, typename Two>
 __global__ void __launch_bounds__(32 * kSlots)
-    col_sums_kernel(const float *part, int parts, int n, int64_t ld, uint16_t *out, int64_t apart,
-                    uint16_t *out2) {
+    col_sums_kernel(const float *part, int parts, int n, int64_t ld, uint16_t *out, Two two) {
   __shared__ float red[kSlots][32];
   grid_dependency_wait();
-  if (blockIdx.y != 0) part += apart, out = out2;
+  if constexpr (std::is_same_v<Two, Second>)
+    if (blockIdx.y != 0) part += two.apart, out = two.out;
   const int j = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
   if (j < n) {
@@ -56,9 +64,13 @@ cudaError_t launch_col_sums(bool bf16, const float *part, int parts, int n, int6
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return bf16 ? cudaLaunchKernelEx(&cfg, col_sums_kernel<true>, part, parts, n, ld, out, apart, out2)
-              : cudaLaunchKernelEx(&cfg, col_sums_kernel<false>, part, parts, n, ld, out, apart,
-                                   out2);
+  auto launch = [&](auto two) {
+    using Two = decltype(two);
+    return cudaLaunchKernelEx(&cfg,
+                              bf16 ? col_sums_kernel<true, Two> : col_sums_kernel<false, Two>,
+                              part, parts, n, ld, out, two);
+  };
+  return out2 ? launch(Second{apart, out2}) : launch(NoSecond());
 }
 
 }  // namespace dgr

@@ -103,13 +103,13 @@ struct SplitArgs {
   int cl;
   bool b_t;     // B stored N x K
   bool r_vec, d_vec, z_vec;  // rows of R / D / Z in whole 8-byte units
-  bool r2_vec, d2_vec, z2_vec;
-  bool sa_vec, sb_vec;       // rows of block scales in whole 16-byte units
   uint32_t idesc;
   uint32_t *err_word;
   float *part;  // gradient, several token tiles: column sums of each [tiles_m][N]
                 // (gated: dU's behind dG's)
   EpiCall c;
+  bool r2_vec, d2_vec, z2_vec;
+  bool sa_vec, sb_vec;  // rows of block scales in whole 16-byte units
 };
 
 // Four consecutive 16-bit values, packed; n is how many of them exist.

@@ -101,14 +101,14 @@ struct EpiArgs {
   bool a_t, b_t;
   bool d_tma, z_tma;  // D / Z written through their tensor maps
   bool r_tma;         // R (Zin) read through its tensor map
-  // Gated: D / Z as above (gradient: dG / dU), r_tma for U (written, or gradient: G
-  // read), s_tma for U read.
-  bool s_tma;
   uint32_t idesc;
   uint32_t *err_word;
   float *part;        // gradient: partial column sums [ceil(M / 32)][N], or null
-  int64_t part_apart;  // gated: dU's are this far behind dG's
   EpiCall c;
+  // Gated: D / Z as above (gradient: dG / dU), r_tma for U (written, or gradient: G
+  // read), s_tma for U read; dU's partial sums are part_apart behind dG's.
+  bool s_tma;
+  int64_t part_apart;
 };
 
 // Shared-memory address of 16-byte unit u of row `lane` in a staging buffer.

@@ -264,13 +264,16 @@ struct NormCall {
   bool bf16 = true;
   int rows = 0, cols = 0;
   float eps = 0.f;
-  const uint16_t *X = nullptr, *R = nullptr, *W = nullptr, *B = nullptr;
+  const uint16_t *X = nullptr, *R = nullptr, *W = nullptr;
   int64_t ldx = 0, ldr = 0;
   uint16_t *H = nullptr;
   int64_t ldh = 0;
   void *Y = nullptr;  // 16-bit, or e4m3 when scale is set
   int64_t ldy = 0;
-  float *scale = nullptr, *rstd = nullptr, *mean = nullptr;
+  float *scale = nullptr, *rstd = nullptr;
+  float *mean = nullptr;  // layer norm
+  // (Last: ahead of the others it cost the root-mean-square norm 2 % at 16384 x 4096.)
+  const uint16_t *B = nullptr;
 };
 cudaError_t launch_rms_norm(const DeviceInfo &dev, const NormCall &c, cudaStream_t stream);
 cudaError_t launch_layer_norm(const DeviceInfo &dev, const NormCall &c, cudaStream_t stream);
@@ -280,10 +283,12 @@ struct NormGradCall {
   int rows = 0, cols = 0;
   const uint16_t *dY = nullptr, *H = nullptr, *W = nullptr, *dH = nullptr;
   int64_t lddy = 0, ldh = 0, lddh = 0;
-  const float *rstd = nullptr, *mean = nullptr;
+  const float *rstd = nullptr;
   uint16_t *dX = nullptr;
   int64_t lddx = 0;
-  uint16_t *dW = nullptr, *db = nullptr;
+  uint16_t *dW = nullptr;
+  const float *mean = nullptr;  // layer norm
+  uint16_t *db = nullptr;
 };
 cudaError_t launch_rms_norm_grad(const DeviceInfo &dev, const NormGradCall &c,
                                  cudaStream_t stream);

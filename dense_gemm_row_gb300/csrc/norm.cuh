@@ -1179,30 +1179,29 @@ __global__ void __launch_bounds__(32 * kGradRowWarps<kLayer, NV>, 1)
   __syncthreads();
   // Eight loads in flight per thread; the adds are in warp order.
   const int stride = 32 * warps;
-  for (int j = threadIdx.x; j < kSets * c.cols; j += 2 * stride) {
-    const bool two = j + stride < kSets * c.cols;
-    auto place = [&](int n) {  // column n, or of db
-      return kLayer && n >= c.cols ? apart + sums_at(n - c.cols) : sums_at(n);
-    };
-    const int at0 = place(j), at1 = place(two ? j + stride : j);
-    float v0 = 0.f, v1 = 0.f;
-    for (int w = 0; w < warps; w += 4) {
-      float a[4], b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float *from = all + min(w + i, warps - 1) * pitch;
-        a[i] = from[at0], b[i] = from[at1];
+  for (int which = 0; which < kSets; ++which) {
+    const float *sums_of = all + which * apart;
+    for (int j = threadIdx.x; j < c.cols; j += 2 * stride) {
+      const bool two = j + stride < c.cols;
+      const int at0 = sums_at(j), at1 = sums_at(two ? j + stride : j);
+      float v0 = 0.f, v1 = 0.f;
+      for (int w = 0; w < warps; w += 4) {
+        float a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float *from = sums_of + min(w + i, warps - 1) * pitch;
+          a[i] = from[at0], b[i] = from[at1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (w + i < warps) v0 += a[i], v1 += b[i];
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (w + i < warps) v0 += a[i], v1 += b[i];
+      const int64_t row = kLayer ? which * static_cast<int64_t>(gridDim.x) + blockIdx.x : blockIdx.x;
+      float *out = part + row * c.cols + j;
+      out[0] = v0;
+      if (two) out[stride] = v1;
     }
-    auto out = [&](int n) {
-      const int64_t row = kLayer && n >= c.cols ? gridDim.x + blockIdx.x : blockIdx.x;
-      return part + row * c.cols + (kLayer && n >= c.cols ? n - c.cols : n);
-    };
-    *out(j) = v0;
-    if (two) *out(j + stride) = v1;
   }
 }
 
