@@ -1310,7 +1310,13 @@ cudaError_t launch_norm(const DeviceInfo &dev, const NormCall &c, cudaStream_t s
   // 87; but 2560 58 against 54, 5280 139 against 115 and 12288, of half as many
   // rows, 185 against 131).
   const int slots = units <= 128 ? 128 : units <= 256 ? 256 : 512;
-  const bool full = units > 128 && units <= 512 && 4 * units > 3 * slots;
+  // Layer norm, whose row takes a block longer: only where it fills 13/16 of the block and
+  // all rows start on 16-byte boundaries, or the gain and bias are read value by value for
+  // each row (16384 rows: 3584 79 against 83 us, but 3200 76 against 72 and 4095 107
+  // against 97).
+  const bool whole = reinterpret_cast<uintptr_t>(c.X) % 16 == 0 && c.ldx % 8 == 0 && c.cols % 8 == 0;
+  const bool full = units > 128 && units <= 512 &&
+                    (kLayer ? whole && 16 * units > 13 * slots : 4 * units > 3 * slots);
   if (alike && units > 64 && static_cast<int64_t>(c.rows) * c.cols > 10240LL * dev.sm_count &&
       !(c.R != nullptr && full)) {
     if (units <= 128) return launch_norm_ring<kLayer, kBf16, 32>(dev, c, stream);
