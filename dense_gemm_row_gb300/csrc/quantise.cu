@@ -7,10 +7,12 @@
 // memory: 2 bytes in, 1 out, each value held in registers between the two.
 //
 // A row's block of 128 belongs to 16 threads with 8 values each: one 16-byte load, one
-// 8-byte store. Where a row does not start on a 16-byte boundary a thread loads the
-// aligned 16 bytes that its first value is in and takes the rest from its neighbour.
+// 8-byte store. Rows that are not in whole 16-byte units go value by value, 8 consecutive
+// ones per thread, so that a line is fetched once. (One aligned load per thread, with the
+// rest from its neighbour by shuffles, took as long for many rows and longer for few:
+// 1001 x 4095 in blocks of 128 rows 6.6 us against 5.4.)
 // bf16 8192 x 8192: 33 us in either blocks (6.1 TB/s), where the issue slots are 62 %
-// busy too; 8192 x 8191 60 us.
+// busy too; 8192 x 8191 61-64 us.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -38,45 +40,18 @@ struct QuantArgs {
   bool y_vec;  // Y's rows in whole 8-byte units
 };
 
-// The 8 values from column `col` on (which may be negative), packed, by one load if all
-// are inside the row and p is aligned; the others zeros.
-__device__ __forceinline__ uint4 load_at(const uint16_t *p, int col, int cols, bool vec) {
-  p += col;
-  // (Columns up to 2^31 - 1: no sum that could pass it.)
-  if (vec && col >= 0 && cols - col >= 8) return __ldcs(reinterpret_cast<const uint4 *>(p));
+// 8 values from column `col` of a row, packed; zeros past the last column. kAligned:
+// rows in whole 16-byte units.
+template <bool kAligned>
+__device__ __forceinline__ uint4 load8(const QuantArgs &q, int64_t row, int col) {
+  const uint16_t *p = q.X + row * q.ldx + col;
+  const int n = q.cols - col;
+  if (kAligned && n >= 8) return __ldcs(reinterpret_cast<const uint4 *>(p));
   uint32_t h[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    h[e] = static_cast<uint32_t>(col) + e < static_cast<uint32_t>(cols) ? p[e] : 0;
+  for (int e = 0; e < 8; ++e) h[e] = e < n ? p[e] : 0;
   return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
                     h[6] | (h[7] << 16));
-}
-// A lane's 8 values of a block, from column `col`; the whole warp. live: there is a row.
-// kAligned: rows in whole 16-byte units.
-template <bool kAligned>
-__device__ __forceinline__ uint4 load8(const QuantArgs &q, int64_t row, int col, int lane,
-                                       bool live) {
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const uint16_t *p = q.X + row * q.ldx;
-  if constexpr (kAligned) return live ? load_at(p, col, q.cols, true) : zero;
-  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 7;
-  const uint4 a = live ? load_at(p, col - off, q.cols, true) : zero;
-  uint4 b = lane == kLanes - 1 && live && off ? load_at(p, col - off + 8, q.cols, true) : zero;
-  uint4 n;
-  n.x = __shfl_down_sync(0xffffffffu, a.x, 1, kLanes);
-  n.y = __shfl_down_sync(0xffffffffu, a.y, 1, kLanes);
-  n.z = __shfl_down_sync(0xffffffffu, a.z, 1, kLanes);
-  n.w = __shfl_down_sync(0xffffffffu, a.w, 1, kLanes);
-  if (lane < kLanes - 1) b = n;
-  // Values off .. off + 7 of the two units, in three steps.
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 6; ++i) w[i] = off & 4 ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) w[i] = off & 2 ? w[i + 1] : w[i];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = off & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // The largest magnitude of 8 packed values, as bits: those of |x| order like |x|, NaN last.
 __device__ __forceinline__ uint32_t top8(const uint4 &v) {
@@ -136,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs q) {
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int64_t row = row0 + i * kStep;
-    v[i] = load8<kAligned>(q, row, col, lane, row < q.rows);
+    v[i] = row < q.rows ? load8<kAligned>(q, row, col) : make_uint4(0, 0, 0, 0);
   }
   float most = 0.f;
   if constexpr (kTile) {
@@ -201,7 +176,7 @@ cudaError_t launch_quantise(const DeviceInfo &dev, bool bf16, int rows, int cols
   q.y_vec = reinterpret_cast<uintptr_t>(Y) % 8 == 0 && ldy % 8 == 0;
   // Few blocks of threads: fewer rows per thread, or more threads per block of values
   // (1001 x 4096 in blocks of 128 rows: 3.9 us with 256 threads, 3.6 with 512, 4.2 with
-  // 1024; 1001 x 4095, whose ends take longer: 7.5, 7.3, 6.7).
+  // 1024; 1001 x 4095: 5.4, 5.4, 6.1).
   const bool tile = block_rows == kBlock;
   const int64_t tiles = (static_cast<int64_t>(rows - 1) / kBlock + 1) * q.col_blocks;
   const bool few = tiles < 4LL * dev.sm_count;
@@ -210,7 +185,7 @@ cudaError_t launch_quantise(const DeviceInfo &dev, bool bf16, int rows, int cols
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-  cfg.blockDim = dim3(!few || !tile ? 256 : x_vec ? 512 : 1024, 1, 1);
+  cfg.blockDim = dim3(few && tile ? 512 : 256, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -219,8 +194,7 @@ cudaError_t launch_quantise(const DeviceInfo &dev, bool bf16, int rows, int cols
   cfg.numAttrs = 1;
   auto pick = [&](auto bf, auto al) {
     constexpr bool kBf16 = decltype(bf)::value, kAligned = decltype(al)::value;
-    return tile ? (few ? quantise_kernel<kBf16, kAligned, true, kAligned ? 512 : 1024,
-                                         kAligned ? 4 : 2>
+    return tile ? (few ? quantise_kernel<kBf16, kAligned, true, 512, 4>
                        : quantise_kernel<kBf16, kAligned, true, 256, 8>)
                 : (few ? quantise_kernel<kBf16, kAligned, false, 256, 1>
                        : quantise_kernel<kBf16, kAligned, false, 256, 8>);
