@@ -558,6 +558,7 @@ GEMM_API gemm_status_t gemm_f16_gated_dact(gemm_op_t opA, gemm_op_t opB, int64_t
  *
  *     scale = max |X| / 448 over the block,   Y8 = X / scale, rounded to nearest even
  *
+ * (X times 448 / max |X| in fp32, within 2^-22 of the quotient before it is rounded.)
  * X has any layout; Y8 any, but a product wants its rows in whole 16-byte units.
  * scale: ceil(rows / block_rows) rows of ceil(cols / 128) values, row stride lds.
  * As in the norm, a block whose largest magnitude is below 1e-30 gets scale 0
