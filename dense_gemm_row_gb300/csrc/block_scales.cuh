@@ -11,16 +11,22 @@ namespace {
 __host__ __device__ __forceinline__ bool scales_whole(const float *p, int64_t ld) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 4 == 0;
 }
-// The scales of k-blocks kb .. kb + 3 of one row (zeros past the last).
+// The scales of k-blocks kb .. kb + 3 of one row (zeros past the last). Plain loads: the
+// kernels start while the one that writes the scales may still run, and loads through the
+// read-only path (ld.global.nc) are for memory that does not change while a kernel runs;
+// nothing orders them behind the wait for that kernel.
 __device__ __forceinline__ float4 load_scales(const float *row, int kb, int KB, bool vec) {
   if (row == nullptr) return make_float4(0.f, 0.f, 0.f, 0.f);
-  if (vec && kb + 4 <= KB) return __ldg(reinterpret_cast<const float4 *>(row + kb));
+  if (vec && kb + 4 <= KB) return *reinterpret_cast<const float4 *>(row + kb);
   float4 v;
-  v.x = kb < KB ? __ldg(row + kb) : 0.f;
-  v.y = kb + 1 < KB ? __ldg(row + kb + 1) : 0.f;
-  v.z = kb + 2 < KB ? __ldg(row + kb + 2) : 0.f;
-  v.w = kb + 3 < KB ? __ldg(row + kb + 3) : 0.f;
+  v.x = kb < KB ? row[kb] : 0.f;
+  v.y = kb + 1 < KB ? row[kb + 1] : 0.f;
+  v.z = kb + 2 < KB ? row[kb + 2] : 0.f;
+  v.w = kb + 3 < KB ? row[kb + 3] : 0.f;
   return v;
+}
+__device__ __forceinline__ float4 scale_products(const float4 &a, const float4 &b) {
+  return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
 }
 __device__ __forceinline__ float pick(const float4 &v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
