@@ -60,7 +60,9 @@ __device__ __forceinline__ void block_multiply(const EpiArgs &p, BlockSmem<kN> &
   bool ok = true, any = false;
   for (int t = unit; ok && t < p.tiles; t += units) {
     for (int kb = 0; kb < KB; ++kb) {
-      if (!mbar_wait_lazy(smem_u32(&sm.tmem_empty[buf]), use ^ 1u, abort, p.err_word,
+      // (Cluster scope: both CTAs' warps give the accumulator back. Their relaxed arrivals
+      // hand over nothing but their loads from it, which the fence below orders.)
+      if (!mbar_wait_lazy<true>(smem_u32(&sm.tmem_empty[buf]), use ^ 1u, abort, p.err_word,
                                 kWaitTmemEmpty) ||
           !mbar_wait_lazy(smem_u32(&sm.full[stage]), phase, abort, p.err_word, kWaitFull)) {
         ok = false;

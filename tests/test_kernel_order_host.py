@@ -33,3 +33,22 @@ def test_no_read_only_loads_in_kernels_that_overlap_their_predecessor():
     for kernel in ("u8_row_corr_kernel", "u8_col_corr_kernel"):
         body = re.search(kernel + r"\(const uint8_t.*?\n}\n", writers[0], flags=re.S).group(0)
         assert "grid_launch_dependents" not in body
+
+
+def test_barriers_that_the_peer_signals_are_waited_for_at_cluster_scope():
+    """The epilogue warps of both CTAs of a pair give an accumulator back on the leader's
+    tmem_empty barrier (mapa to rank 0). A wait at CTA scope is not ordered behind the
+    peer's arrival, and the MMAs that follow overwrite what the peer still reads."""
+    waits = []
+    for name, text in sources():
+        if not re.search(r"mapa_shared\(smem_u32\(&sm\.tmem_empty\[buf\]\), 0\)", text):
+            continue
+        for m in re.finditer(r"(mbar_wait\w*(?:<\w+>)?)\(smem_u32\(&sm\.tmem_empty", text):
+            before = text[:m.start()]
+            # the branch of single CTAs, whose barrier no other one signals
+            single = before.rstrip().endswith("got =") and "} else {" in before[-90:]
+            waits.append((name, m.group(1), single))
+    kernels = {"gemm_block_tile.cuh", "gemm_epi_tile.cuh", "gemm_tc_kernel.cuh"}
+    assert {name for name, _, _ in waits} == kernels
+    for name, wait, single in waits:
+        assert single or wait in ("mbar_wait_lazy<true>", "mbar_wait_bounded_cluster"), (name, wait)
