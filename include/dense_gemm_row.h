@@ -591,9 +591,12 @@ GEMM_API gemm_status_t gemm_quantise_f16_e4m3(int64_t rows, int64_t cols, int64_
  *     Y_ij = (H_ij - mean_i) rstd_i W_j + b_j
  *
  * R, H, W (1), b (0), mean and rstd (rows fp32 values each) may be NULL. The
- * statistics and Y are those of the unrounded sum; the squares are summed about
- * the mean, so a large mean costs no accuracy. Aliasing as gemm_rms_norm_bf16;
- * eps >= 0. A row of equal values with eps == 0 gives NaN, as the formula does.
+ * statistics and Y are those of the unrounded sum X + R in fp32. The squares are
+ * summed about the mean, so a large mean costs the variance nothing; the mean is
+ * off by the roundings of its sum, a few 2^-24 of the row's mean |H|, and Y by
+ * rstd_i times that. Sums that fp32 holds exactly leave none: a row of equal X (of
+ * up to 8192 columns in f16, 65536 in bf16) gives Y = b, and with eps == 0 NaN, as
+ * the formula does. Aliasing as gemm_rms_norm_bf16; eps >= 0.
  *
  * gemm_layer_norm_grad_bf16, gemm_layer_norm_grad_f16 -- the gradient. From dY,
  * the H, mean and rstd of the forward call, and W (NULL: 1):
