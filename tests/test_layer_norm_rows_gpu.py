@@ -62,3 +62,62 @@ def test_mean_of_exact_sums(gemm_mod, n):
         gemm_mod.layer_norm(X, Y, mean=mean)
         assert mean[1] == float("-inf") and bool(mean[[0, 2]].isfinite().all())
         assert bool(Y[1].isnan().all())
+
+
+# Bounds for long rows. A thread adds 8 values at a time in fp32; those sums are added
+# with compensation, so that their number does not matter (2 roundings); then 5 steps in
+# the warp and 32 warps: fewer than 64 additions in turn, 2^-18 of the sum of magnitudes.
+LONG = [(1, 1 << 26), (2, 20001 * 64 + 5), (3, 16400)]
+
+
+@pytest.mark.parametrize("shape", LONG, ids=lambda s: "x".join(map(str, s)))
+def test_long_rows_of_equal_values(gemm_mod, shape):
+    """1 + 2^-10: added one at a time, sums beyond 2^14 lose the 2^-10 each time."""
+    X = torch.full(shape, 1 + 2.0 ** -10, dtype=torch.float16, device="cuda")
+    mean, rstd = (torch.empty(shape[0], device="cuda") for _ in range(2))
+    Y = torch.empty_like(X)
+    gemm_mod.layer_norm(X, Y, mean=mean, rstd=rstd, eps=1.0)
+    off = (1 + 2.0 ** -10) * 2.0 ** -18
+    assert bool(((mean.double() - (1 + 2.0 ** -10)).abs() <= off).all())
+    assert bool((rstd.double() - 1).abs().max() <= 2.0 ** -22)
+    assert float(Y.abs().max()) <= off * 1.01
+    # the variance: 1 + 2^-10 and its negative in turn, mean 0, rstd = 1 / (1 + 2^-10)
+    X[:, 1::2] *= -1
+    if shape[1] % 2 == 0:
+        gemm_mod.layer_norm(X, Y, mean=mean, rstd=rstd, eps=0.0)
+        assert not mean.any()
+        assert bool((rstd.double() * (1 + 2.0 ** -10) - 1).abs().max() <= 2.0 ** -18)
+
+
+@pytest.mark.parametrize("shape", LONG, ids=lambda s: "x".join(map(str, s)))
+def test_gradient_of_long_rows(gemm_mod, shape):
+    """g = c and n in turn 1 and -1 but for a level: mean(g) = c and mean(g n) = 0 leave
+    dX = 0; with g = c n they leave c n - n c = 0. (c = 1 + 2^-10.)"""
+    rows, n = shape
+    c = 1 + 2.0 ** -10
+    H = torch.ones(rows, n, dtype=torch.float16, device="cuda")
+    H[:, 1::2] = -1
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    dX = torch.empty_like(H)
+    for dY in (torch.full_like(H, c), H * c):
+        g, h = dY.double(), H.double()
+        want = g - g.mean(1, keepdim=True) - h * (g * h).mean(1, keepdim=True)
+        gemm_mod.layer_norm_grad(dY, H, mean, rstd, dX)
+        # terms of c: g, mean(g) and n mean(g n); then one rounding to 16 bits
+        bound = 2.0 ** -17 * 3 * c + want.abs() * 2.0 ** -11 + 2.0 ** -25
+        assert bool(((dX.double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("shape", LONG, ids=lambda s: "x".join(map(str, s)))
+def test_root_mean_square_of_long_rows(gemm_mod, shape):
+    rows, n = shape
+    c = 1 + 2.0 ** -10
+    X = torch.full(shape, c, dtype=torch.float16, device="cuda")
+    rstd, Y = torch.empty(rows, device="cuda"), torch.empty_like(X)
+    gemm_mod.rms_norm(X, Y, rstd=rstd, eps=0.0)
+    # half the sum of squares' 2^-18, and rsqrt's and the quotient's roundings
+    assert bool((rstd.double() * c - 1).abs().max() <= 2.0 ** -19 + 2.0 ** -22)
+    dX = torch.empty_like(X)
+    rstd.fill_(1 / c)
+    gemm_mod.rms_norm_grad(X, X, rstd, dX)  # g = c, n = 1: dX = (c - mean(c)) / c
+    assert float(dX.abs().max()) <= 2.0 ** -17 * 2 + 2.0 ** -22
