@@ -549,8 +549,10 @@ GEMM_API gemm_status_t gemm_f16_gated_dact(gemm_op_t opA, gemm_op_t opB, int64_t
  * scale_a: M rows of ceil(K / 128) fp32 values, row stride ldsa; scale_b:
  * ceil(N / 128) such rows, row stride ldsb; neither may be NULL unless it is
  * empty. Each block's sum is made by the tensor cores and added, scaled, in
- * fp32 in the order of b. The rest is as gemm_e4m3_*_epi. Results are the
- * same bits on every call.
+ * fp32, in a fixed order: by rising b, for problems of few rows within up to 8
+ * ranges of b whose sums are added next. Results are the same bits on every call
+ * of one size on one device; a row's bits can differ where M, or the number of
+ * SMs, makes other ranges. The rest is as gemm_e4m3_*_epi.
  *
  * gemm_quantise_bf16_e4m3, gemm_quantise_f16_e4m3 -- a 16-bit matrix X (rows x
  * cols) as such an operand, with blocks of block_rows x 128 (block_rows 1: A and
