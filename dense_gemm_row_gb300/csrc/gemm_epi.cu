@@ -163,18 +163,19 @@ int plan_split(const DeviceInfo &dev, int M, int N, int cols, int KB, double bes
   return rows;
 }
 
-// The gated layer and its gradient. Over 270 problems of 40 to 1500 rows, N 512 to 8192,
-// K 512 to 4096 the choice is 2.2 % and 1.3 % slower than the best kernel on average, where
-// the other products' rule is 19 % and 14 %; 128-row token tiles hardly ever win. For
-// instance 300 x 1000 x 520, gradient: tiles 10.1, 32 rows 8.2; 128 x 4096 x 4096: tiles
-// 22.9, 64 rows 14.5; 1000 x 2048 x 512: tiles 8.7, 64 rows 14.9.
-EpiPlan plan_gated(const DeviceInfo &dev, bool a_t, bool grad, int M, int N, int KB, bool ragged) {
+// The gated layer and its gradient. Over 150 problems each of 24 to 1500 rows, N 512 to
+// 8192, K 512 to 4096 (bf16, B stored N x K, without biases, sums or stored projections) the
+// choice is 2.2 % and 1.3 % slower than the best kernel on average, at most 29 % and 18 %,
+// where the other products' rule is 19 % and 14 % slower on average; 128-row token tiles
+// hardly ever win. For instance 300 x 1000 x 520, gradient: tiles 10.1, 32 rows 8.2; 128 x
+// 4096 x 4096: tiles 22.9, 64 rows 14.5; 1000 x 2048 x 512: tiles 8.7, 64 rows 14.9.
+EpiPlan plan_gated(const DeviceInfo &dev, bool a_t, bool grad, int M, int N, int KB) {
   static constexpr WaveCost kForward[3] = {{1.5, 0.17, 3.0}, {1.5, 0.192, 3.4}, {1.4, 0.245, 4.6}};
   static constexpr WaveCost kGradient[3] = {{0, 0.18, 4.4}, {0, 0.2, 5.4}, {0, 0.273, 7.3}};
   static constexpr WaveCost kTile = {4.5, 0.266, 1.3};
   static constexpr WaveCost kWide = {3.3, 0.278, 6.4}, kNarrow = {3.3, 0.137, 3.0};
   EpiPlan plan{0, 256};
-  if (grad) plan.tile_n = plan_epi(dev, true, M, N, KB, ragged).tile_n;
+  if (grad) plan.tile_n = plan_epi(dev, true, M, N, KB, false).tile_n;
   if (a_t) return plan;  // the few-rows kernel's token tiles are K-major
   const bool wide = plan.tile_n == 256;
   const double tiles = grad ? tile_cost(dev, M, N, plan.tile_n, KB, wide ? kWide : kNarrow)
@@ -184,7 +185,8 @@ EpiPlan plan_gated(const DeviceInfo &dev, bool a_t, bool grad, int M, int N, int
 }
 
 // The block-scaled e4m3 product, plain and gated: 200 problems each of 16 to 1500 rows, N
-// 512 to 16384, K 512 to 16384, 2 % slower than the best on average. For instance 100 x
+// 512 to 16384, K 512 to 16384 (bf16 results, no bias or residual), 1.8 % and 1.9 % slower
+// than the best on average, at most 32 % and 38 %. For instance 100 x
 // 4096 x 4096: 256-row tiles 12.6 us, token tiles of 64 rows 10.4, of 32 10.7, of 16 12.5;
 // 100 x 512 x 4096: 12.3, 7.3, 6.2, 5.4; 1024 x 4096 x 1024: tiles of 256 columns 9.5, of
 // 128 11.0.
@@ -219,7 +221,7 @@ cudaError_t launch_gemm_epi(const DeviceInfo &dev, bool e4m3, bool a_t, bool b_t
                      : launch_block_fwd(dev, plan.tile_n, M, N, K, A, lda, B, ldb, epi, stream);
   }
   const int KB = (K - 1) / (e4m3 ? 128 : 64) + 1;
-  const EpiPlan plan = epi.gated ? plan_gated(dev, a_t, epi.grad, M, N, KB, ragged)
+  const EpiPlan plan = epi.gated ? plan_gated(dev, a_t, epi.grad, M, N, KB)
                                  : plan_epi(dev, a_t, M, N, KB, ragged);
   const int mp = plan.split_rows, tile_n = plan.tile_n;
   if (epi.gated && !epi.grad)

@@ -85,7 +85,7 @@ struct __align__(1024) SplitSmem {
   uint8_t a[SplitCfg<kMP>::kStages][SplitCfg<kMP>::kABytes];
   uint64_t full[SplitCfg<kMP>::kStages];
   uint64_t empty[SplitCfg<kMP>::kStages];
-  uint64_t done;
+  uint64_t done;  // all sums are in tensor memory (block-scaled: acc_full of each)
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
       mbar_init(smem_u32(&sm.full[s]), 1);
       mbar_init(smem_u32(&sm.empty[s]), 1);
     }
-    mbar_init(smem_u32(&sm.done), 1);
+    if constexpr (!kBlock) mbar_init(smem_u32(&sm.done), 1);
     mbar_init(smem_u32(&sm.drain), 1);
     if constexpr (kBlock) {
       for (int i = 0; i < kBufs; ++i) {
@@ -537,7 +537,9 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     // A commit covers the MMAs of the lane that issues it: the same lane is
     // elected each time (the lowest of a full warp).
     if (elect_one()) {
-      if (ok) tc_commit(smem_u32(&sm.done));
+      if constexpr (!kBlock) {
+        if (ok) tc_commit(smem_u32(&sm.done));
+      }
       if (any) tc_commit(smem_u32(&sm.drain));
     }
     __syncwarp();
