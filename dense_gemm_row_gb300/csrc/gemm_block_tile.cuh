@@ -10,10 +10,11 @@
 // 128 columns, which a warp's columns never cross. The accumulators alternate, so that
 // the MMAs of the next k-block run meanwhile.
 //
-// What bounds it (8192^3: 385 us, 2.85 PFLOP/s; e4m3 with row scales 295): the
+// What bounds it (8192^3 with a residual: 396 us in short runs, 438 or 2.5 PFLOP/s
+// repeated at the power limit; e4m3 with row scales 302 and 345): the
 // epilogue's chain of loads from tensor memory, each about 100 cycles, 8 per k-block
-// whose MMAs take 512. Without the multiply-adds 336 us, without all but one of the
-// loads 362, without either 309. Multiply-adds on packed pairs cost moves (441 us);
+// whose MMAs take 512. In short runs of a form that took 388: without the multiply-adds
+// 336 us, without all but one of the loads 362, without either 309. Multiply-adds on packed pairs cost moves (441 us);
 // loads of 32 columns or of 8 were slower (419, 397), and so were accumulators of 128
 // columns, four under way, emptied by all eight warps (463) or by half of them (383,
 // but gated 245 against 225).

@@ -27,8 +27,8 @@
 // |h w| is reduced together with the sum of squares, so the 8-bit form has one
 // block reduction too: max |y| = s max |h w| up to rounding.
 //
-// Layer norm, bf16: 16384 x 4096 with a residual 85.7 us (6.3 TB/s), 1 x 4096 2.5 us;
-// gradient 8192 x 8192 with dh 91.6 us (5.9 TB/s), 32768 x 1024 47.3, 333 x 1001 7.1.
+// Layer norm, bf16: 16384 x 4096 with a residual 86.0 us (6.2 TB/s), 1 x 4096 2.6 us;
+// gradient 8192 x 8192 with dh 91.8 us (5.8 TB/s), 32768 x 1024 47.3, f16 333 x 1001 7.0.
 #pragma once
 
 #include <algorithm>

@@ -11,8 +11,8 @@
 // ones per thread, so that a line is fetched once. (One aligned load per thread, with the
 // rest from its neighbour by shuffles, took as long for many rows and longer for few:
 // 1001 x 4095 in blocks of 128 rows 6.6 us against 5.4.)
-// bf16 8192 x 8192: 30 us in either blocks (6.8 TB/s, the copy rate); 8192 x 8191 55 us,
-// 1001 x 4095 in blocks of 128 rows 5.1.
+// bf16 8192 x 8192: 30 us in short runs in either blocks (6.8 TB/s, the copy rate), 31.6
+// repeated; 8192 x 8191 55 us, f16 1001 x 4095 in blocks of 128 rows 4.8.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>

@@ -552,7 +552,8 @@ GEMM_API gemm_status_t gemm_f16_gated_dact(gemm_op_t opA, gemm_op_t opB, int64_t
  * fp32, in a fixed order: by rising b, for problems of few rows within up to 8
  * ranges of b whose sums are added next. Results are the same bits on every call
  * of one size on one device; a row's bits can differ where M, or the number of
- * SMs, makes other ranges. The rest is as gemm_e4m3_*_epi.
+ * SMs, makes other ranges. The product of a block's two scales is formed in fp32 and
+ * must not leave its range. The rest is as gemm_e4m3_*_epi.
  *
  * gemm_quantise_bf16_e4m3, gemm_quantise_f16_e4m3 -- a 16-bit matrix X (rows x
  * cols) as such an operand, with blocks of block_rows x 128 (block_rows 1: A and
