@@ -1,11 +1,15 @@
-"""Chained calls of the block-scaled products on one stream. They start as programmatic
-dependents of the quantisation that writes their operands and scales, and must read
-neither before it has ended. Each chain writes the same buffers again with other data,
-with nothing in between that waits, and every result has the bits of calls that wait
-for each other."""
+"""Calls that overlap others: chained on one stream, and on streams of several threads.
+
+The block-scaled products start as programmatic dependents of the quantisation that
+writes their operands and scales, and must read neither before it has ended. Each chain
+writes the same buffers again with other data, with nothing in between that waits, and
+every result has the bits of calls that wait for each other."""
+import threading
+
 import pytest
 import torch
 
+from dense_gemm_row_gb300.feed_forward import FeedForward, GatedFeedForward
 from tests.layer_util import normal
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +65,42 @@ def test_quantise_then_product_into_the_same_buffers(gemm_mod, shape, gated):
         assert all(torch.equal(p, q) for p, q in zip(got, want))
     assert all(bool(p.isfinite().all()) for p in want)
     assert g.check_device_error() == 0
+
+
+def test_steps_of_several_threads_at_once(gemm_mod):
+    """Training steps and 8-bit passes on four threads' streams: the bits of each alone."""
+    def job(seed, tokens, model, hidden, kind):
+        ff = kind(model, hidden, "silu", seed=seed)
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        x, r, dout = (torch.randn(tokens, model, generator=gen, device="cuda").bfloat16()
+                      for _ in range(3))
+
+        def step():
+            out, saved = ff.forward(x, r)
+            return [out, ff.forward8(x, r), *ff.backward(dout, saved).values()]
+        return step
+
+    jobs = [job(1, 300, 512, 1040, GatedFeedForward), job(2, 7, 1024, 2048, GatedFeedForward),
+            job(3, 1500, 256, 800, GatedFeedForward), job(4, 100, 512, 1024, FeedForward)]
+    want = [step() for step in jobs]
+    torch.cuda.synchronize()
+    done, wrong = [], []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for rep in range(20):
+                got = jobs[i]()
+                stream.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    wrong.append((i, rep))
+        done.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert sorted(done) == list(range(len(jobs))) and not wrong
+    assert gemm_mod.check_device_error() == 0
