@@ -481,9 +481,9 @@ def gemm_gated(A, Bg, Bu, D, *, act="silu", alpha=1.0, bias_gate=None, bias_up=N
     A is M x K (K x M with trans_a), Bg and Bu are K x N (N x K with trans_b), D
     M x N; all are bfloat16 or float16. bias_gate and bias_up (N values each) may be
     None; gate and up (M x N), when given, receive G and U for gemm_gated_dact; they
-    and D are distinct. Bg and Bu may be parts of one matrix. float8_e4m3fn A, Bg and Bu (trans_b only) come
-    with scales per block of 128: scale_a, scale_gate and scale_up as gemm_epilogue's
-    float32 matrices. Layouts as gemm_epilogue."""
+    and D are distinct. Bg and Bu may be parts of one matrix. float8_e4m3fn A, Bg and
+    Bu (trans_b only) come with scales per block of 128: scale_a, scale_gate and
+    scale_up as gemm_epilogue's float32 matrices. Layouts as gemm_epilogue."""
     st = (_layers or _load_layers()).gemm_gated(A, Bg, Bu, D, act, alpha, bias_gate, bias_up,
                                                 gate, up, trans_a, trans_b, scale_a, scale_gate,
                                                 scale_up, stream)

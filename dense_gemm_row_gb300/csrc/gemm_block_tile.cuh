@@ -14,10 +14,10 @@
 // repeated at the power limit; e4m3 with row scales 302 and 345): the
 // epilogue's chain of loads from tensor memory, each about 100 cycles, 8 per k-block
 // whose MMAs take 512. In short runs of a form that took 388: without the multiply-adds
-// 336 us, without all but one of the loads 362, without either 309. Multiply-adds on packed pairs cost moves (441 us);
-// loads of 32 columns or of 8 were slower (419, 397), and so were accumulators of 128
-// columns, four under way, emptied by all eight warps (463) or by half of them (383,
-// but gated 245 against 225).
+// 336 us, without all but one of the loads 362, without either 309. Multiply-adds on
+// packed pairs cost moves (441 us); loads of 32 columns or of 8 were slower (419, 397),
+// and so were accumulators of 128 columns, four under way, emptied by all eight warps
+// (463) or by half of them (383, but gated 245 against 225).
 //
 // Warps as in gemm_epi_tile.cuh, whose producer this kernel shares; the final epilogue
 // works on the registers. Each warp has two staging buffers: R of both of its blocks
