@@ -497,6 +497,7 @@ cudaError_t launch_block_form(const DeviceInfo &dev, int M, int N, int K, const 
   p.idesc = idesc_mma(0u, false, false, Cf::kTileM, kN);
   p.err_word = dev.err_word;
   p.part = nullptr, p.part_apart = 0;
+  p.loop_ns = kWaitLimitNs;  // (not used: every k-block has an accumulator of its own)
   p.c = epi;
   const BlockScales sc{epi.block_a, epi.block_b,  epi.block_b2,     epi.ldsa,
                        epi.ldsb,    epi.ldsb2, (K - 1) / 128 + 1};

@@ -567,7 +567,8 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
       got = split_blocks<kMP, kPair>(p, sm, tmem_base, t, quarter, m0, n0, kb0, kb1, blocks);
     } else {
       if (lane == 0)
-        got = mbar_wait_bounded(smem_u32(&sm.done), 0, abort, p.err_word, kWaitTmemFull);
+        got = mbar_wait_bounded(smem_u32(&sm.done), 0, abort, p.err_word, kWaitTmemFull,
+                                wait_limit_ns(kb1 - kb0));
       got = __shfl_sync(0xffffffffu, got, 0);
     }
     // Every MMA has completed and every copy was consumed by one, so the stages

@@ -109,6 +109,7 @@ struct EpiArgs {
   // read), s_tma for U read; dU's partial sums are part_apart behind dG's.
   bool s_tma;
   int64_t part_apart;
+  uint64_t loop_ns;  // limit of a wait for a whole main loop
 };
 
 // Shared-memory address of 16-byte unit u of row `lane` in a staging buffer.
@@ -432,7 +433,7 @@ __device__ __forceinline__ void epi_tile(const CUtensorMap &tmD, const CUtensorM
   };
   if (have_r) request_r(col0);
   const bool got = mbar_wait_lazy(smem_u32(&sm.tmem_full[buf]), use, abort, p.err_word,
-                                  kWaitTmemFull);
+                                  kWaitTmemFull, p.loop_ns);
   if (have_r) take_r();
   if (!got) {
     ok = false;
@@ -540,7 +541,8 @@ __device__ __forceinline__ void epi_tile_gated(const CUtensorMap &tmD, const CUt
     sm.bias[i] = bias && j < p.N ? bias[j] : 0;
   }
   epilogue_sync();
-  if (!mbar_wait_lazy(smem_u32(&sm.tmem_full[buf]), use, &sm.abort, p.err_word, kWaitTmemFull)) {
+  if (!mbar_wait_lazy(smem_u32(&sm.tmem_full[buf]), use, &sm.abort, p.err_word, kWaitTmemFull,
+                      p.loop_ns)) {
     ok = false;
     return;
   }
@@ -633,7 +635,7 @@ __device__ __forceinline__ void epi_tile_gated_grad(
   };
   request(col0);
   const bool got = mbar_wait_lazy(smem_u32(&sm.tmem_full[buf]), use, &sm.abort, p.err_word,
-                                  kWaitTmemFull);
+                                  kWaitTmemFull, p.loop_ns);
   arrive();
   if (!got) {
     ok = false;
@@ -925,6 +927,7 @@ cudaError_t launch_epi_tile(const DeviceInfo &dev, bool a_t, bool b_t, int M, in
   p.err_word = dev.err_word;
   p.part = part;
   p.c = epi;
+  p.loop_ns = wait_limit_ns((K - 1) / kBK + 1);
   const int units = static_cast<int>(tiles < pairs ? tiles : pairs);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * static_cast<unsigned>(units), 1, 1);

@@ -23,6 +23,12 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // Second safety net, should %globaltimer ever stand still: a wait also gives
 // up after this many polls.
 constexpr uint32_t kWaitMaxPolls = 1u << 28;
+// The limit of a wait that spans `blocks` k-blocks of a main loop: 4 us each more, ten times
+// what they take (one pair's tile over 2^25 k-blocks: 9 s). The waits of the loop itself
+// are for one stage and keep the limit above; when one of them gives up, so do the others.
+__host__ __device__ constexpr uint64_t wait_limit_ns(int64_t blocks) {
+  return kWaitLimitNs + 4000ull * static_cast<uint64_t>(blocks);
+}
 
 __device__ __forceinline__ uint64_t global_timer_ns() {
   uint64_t t;

@@ -49,7 +49,8 @@ __device__ __forceinline__ bool mbar_wait_lazy(uint32_t bar, uint32_t parity, vo
     if ((it & 63u) == 0u) {
       const uint64_t now = global_timer_ns();
       if (t0 == 0) t0 = now;
-      const bool late = now - t0 > limit_ns || it >= kWaitMaxPolls;
+      const uint32_t polls = limit_ns > kWaitLimitNs ? ~0u - 255u : kWaitMaxPolls;
+      const bool late = now - t0 > limit_ns || it >= polls;
       if (__any_sync(kWarp, late || *abort)) {
         if (late) {
           *abort = 1;
