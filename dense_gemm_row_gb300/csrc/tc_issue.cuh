@@ -47,6 +47,9 @@ __device__ __forceinline__ bool mbar_wait_lazy(uint32_t bar, uint32_t parity, vo
                                    : mbar_try_wait(bar, parity)))
       return true;
     if ((it & 63u) == 0u) {
+      // The kernel may have started while the previous one still runs: its time is not
+      // this wait's.
+      if (t0 == 0) grid_dependency_wait();
       const uint64_t now = global_timer_ns();
       if (t0 == 0) t0 = now;
       const uint32_t polls = limit_ns > kWaitLimitNs ? ~0u - 255u : kWaitMaxPolls;

@@ -1,12 +1,15 @@
 """Main loops that take longer than the kernels' bound on a single wait (2 s): the result
-is right and no wait is recorded as given up."""
+is right, the calls behind it are, and no wait is recorded as given up."""
 import pytest
 import torch
 
+from oracle import layers as L
+from tests.layer_util import normal
+
 pytestmark = pytest.mark.gpu
 
-LONG = 5 << 27  # 2^20 * 10 k-blocks of 64 by one pair of CTAs, 0.27 us each: 2.8 s
-MOST = 2 ** 31 - 1  # 9 s
+LONG = 3 << 28  # by one pair of CTAs 2.9 s
+MOST = 2 ** 31 - 1  # 8 s
 PLACES = [0, 63, 64, 12345678, 2 ** 29 + 7, LONG - 65, LONG - 1]
 
 
@@ -46,3 +49,35 @@ def test_gradients(gemm_mod):
     assert (dG.item(), dU.item(), s.item(), t.item()) == (21, 14, 21, 14)
     gemm_mod.gemm_dact(a, a, None, D, dbias=s[0], trans_a=True)
     assert (D.item(), s.item()) == (7, 7)
+
+
+def quantised(g, rows, cols, block_rows, seed):
+    q = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device="cuda")
+    s = torch.empty(-(-rows // block_rows), cols // 128, device="cuda")
+    g.quantise_blocks(normal((rows, cols), torch.bfloat16, seed), q, s, rows=block_rows)
+    return q, s
+
+
+@pytest.mark.parametrize("m", [20, 700], ids=["few rows", "tiles"])
+@pytest.mark.parametrize("kind", ["plain", "block"])
+def test_the_call_behind_a_long_one(gemm_mod, kind, m):
+    """It starts while the long call still runs, on the other SMs, and waits for it."""
+    g, n, k = gemm_mod, 512, 1024
+    D, want = (torch.zeros(m, n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    if kind == "plain":
+        A, B = normal((m, k), torch.bfloat16, 1), normal((n, k), torch.bfloat16, 2)
+
+        def call(D):
+            g.gemm_epilogue(A, B, D, trans_b=True)
+    else:
+        (A, sa), (B, sb) = quantised(g, m, k, 1, 1), quantised(g, n, k, 128, 2)
+
+        def call(D):
+            g.gemm_epilogue(A, B, D, trans_b=True, scale_a=sa, scale_b=sb)
+    a, one = column(LONG), value(5)
+    call(want)
+    torch.cuda.synchronize()
+    g.gemm_epilogue(a, a, one, trans_a=True)
+    call(D)
+    torch.cuda.synchronize()
+    assert one.item() == 7 and torch.equal(D, want) and L.to64(want).any()
